@@ -52,6 +52,7 @@ extern "C" {
 /* Element types of caller tensors. */
 #define PCK_DT_F32       0
 #define PCK_DT_F16       1
+#define PCK_DT_BF16      2  /* the paged-tail calls only */
 
 /* Head dimensions with kernels: fp16 slots 32, 64, 96, 128, 160, 192, 256 (M = 1 and M > 1) and
  * 512 (M = 1 only: M > 1 returns PCK_EUNSUPPORTED); mlx4g32 slots 64, 128, 192, 256 (M > 1: 64,
@@ -286,6 +287,104 @@ int pck_attend_records_noalloc(int H_kv, int N, int D, const void *K_rec, const 
  * one of those calls wrote invalid results. Callers that use the results should check it. */
 int pck_noalloc_status(void *stream, int *code);
 
+/* ---- The paged tail: what a session adds behind (or without) a resident prefix.
+ *
+ * The caller owns a cache of pages and says, per call, which pages each sequence uses. These calls
+ * take the device's tables and lengths as they are when the stream reaches them, allocate nothing
+ * and use no workspace of the context, so calls of several streams, and replays of several
+ * captured graphs, may overlap when their own buffers do not; on the host, one context is still
+ * called by one thread at a time. A value on the device that is out of range (a page number
+ * outside [0, n_pages), a rotary position outside the table, a length beyond the table's width)
+ * is never followed: the call's results are then invalid and pck_sync reports PCK_ECUDA with code
+ * 8, 9 or 10. The current device is left as it was. */
+
+/* A cache: K and V hold [n_pages, H_kv, page_size, D] in any order of the first three dimensions
+ * (strides in elements, D innermost and contiguous), fp16 or bf16. Both must be 16-byte aligned,
+ * strides of dimensions larger than 1 positive multiples of 8. page_size: a multiple of 16. */
+typedef struct pck_paged_cache {
+    void *K, *V;              /* device */
+    int dtype;                /* PCK_DT_F16 or PCK_DT_BF16 */
+    int H_kv, D, page_size;
+    int64_t n_pages;
+    int64_t k_page, k_head, k_token;   /* strides of K */
+    int64_t v_page, v_head, v_token;   /* strides of V */
+} pck_paged_cache;
+
+/* The sequences of a call. Sequence b's rows are cu_rows[b] .. cu_rows[b+1]-1 of T (cu_rows
+ * ascending from 0; rows behind the last sequence's are neither read nor written); they are the
+ * last ones of its kv_len[b] cached tokens: row i of its n rows stands at cache position
+ * kv_len[b] - n + i, and token p of the cache lies in page table[b][p / page_size], slot
+ * p % page_size. Table entries that no visible token needs are not read. cu_rows NULL: one row per
+ * sequence (T == B). Rows with a negative cache position (a padded sequence of length 0) see and
+ * store nothing. */
+typedef struct pck_paged_batch {
+    int B, T;
+    const int32_t *cu_rows;   /* device [B + 1], or NULL */
+    const int32_t *kv_len;    /* device [B] */
+    const int32_t *table;     /* device [B, max_pages] */
+    int max_pages;
+    int max_rows;             /* host bound on one sequence's rows (1 with cu_rows NULL) */
+} pck_paged_batch;
+#define PCK_PAGED_MAX_BATCH 2048
+
+/* A rotation of the first R elements of each head (R a multiple of 16, at most D). cos_sin: device
+ * fp32 [n_pos, R], R/2 cosines and then R/2 sines of each position's angles. Pair i is elements
+ * (i, i + R/2), or (2i, 2i + 1) when interleaved: (a, b) -> (a cos - b sin, b cos + a sin).
+ * positions: device int32 [T], or NULL (append only: the rows' cache positions). */
+typedef struct pck_rotary {
+    const float *cos_sin;
+    int n_pos, R, interleaved;
+    const int32_t *positions;
+} pck_rotary;
+
+/* Rows [T, H, D] in, and the same out (in place allowed): strides in elements, D contiguous,
+ * 16-byte aligned, strides of dimensions larger than 1 multiples of 8 (4 for fp32). */
+typedef struct pck_rows {
+    const void *in;           /* device; NULL: none of this kind */
+    void *out;
+    int H;
+    int64_t in_row, in_head, out_row, out_head;
+    const void *weight;       /* norm weight [D] of the rows' type, or NULL (all ones) */
+} pck_rows;
+
+/* RMS norm of each head of Q and K, then the rotation, in one pass, held in fp32 and rounded once:
+ * y = x / sqrt(mean(x^2) + eps) * weight. Q or K may have no rows (in NULL). norm 0: rotation only;
+ * rope NULL: norm only. dtype: F32, F16 or BF16 (in, out and weights). D: a multiple of 16 up to
+ * 512. The output strides fit Q for pck_query_fused ([H_q, M, D]) and K for its dense suffix as
+ * they fit [T, H, D]. */
+int pck_qk_norm_rope(pck_ctx *ctx, int dtype, int T, int D, const pck_rows *Q, const pck_rows *K, int norm,
+                     float eps, const pck_rotary *rope, void *stream);
+
+/* Append: stores K (normed and rotated as above, where asked) and V (as it is) of every row into
+ * its cache slot, and in the same pass norms and rotates Q, out of or in place, when Q is not NULL.
+ * K->out, V->out and their strides are not used. dtype: the cache's, or F32 (rounded once into the
+ * cache; Q stays F32). D: a multiple of 16 up to 512. Two rows of one call must not name one slot. */
+int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int dtype,
+                     const pck_rows *Q, const pck_rows *K, const pck_rows *V, int norm, float eps,
+                     const pck_rotary *rope, void *stream);
+
+/* Attention of Q rows over the cached tokens of their sequences. Q: device [T, H_q, D] of the
+ * cache's type (strides in elements, D contiguous, 16-byte aligned, multiples of 8), q head h on kv
+ * head h / (H_q / H_kv). A row at cache position p sees tokens 0 .. p; with window > 0 only the
+ * last `window` of these and the first `sinks` of the cache. O: device [T, H_q, D] of the
+ * cache's type, contiguous; LSE: device fp32 [T, H_q] or NULL. A row that sees nothing gets O = 0
+ * and LSE = -inf. Cached tokens that no row of the call sees are not used, whatever they hold.
+ * O_prior (device fp32 [T, H_q, D]) and LSE_prior ([T, H_q]): attention of the same rows over other
+ * keys, e.g. what pck_query_batch gave for a resident prefix: O and LSE are then those over both
+ * (both NULL otherwise).
+ * max_rows == 1: split over the cache's length and joined, D in {64, 128, 192, 256}; more rows are
+ * PCK_EUNSUPPORTED. B <= PCK_PAGED_MAX_BATCH.
+ * workspace: device, 16-byte aligned, pck_paged_workspace bytes (which may be 0), read and written
+ * by this call only while it runs: calls that may overlap need one each. */
+int pck_paged_attend(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int H_q,
+                     const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
+                     const float *O_prior, const float *LSE_prior, void *O, float *LSE,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of that call into *bytes (it depends on sizes only, not on device values). */
+int pck_paged_workspace(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int H_q,
+                        int window, int sinks, size_t *bytes);
+
 /* Counters of ctx. */
 int pck_info(pck_ctx *ctx, pck_info_t *out);
 
@@ -296,7 +395,8 @@ int pck_info(pck_ctx *ctx, pck_info_t *out);
  * MMA warp, 4 prefill softmax, 5 prefill final O, 6 sparse scoring copy, 7 an fp32 Q element
  * of an M=1 query with |q| * log2(e) / sqrt(D) >= 65504 (or not finite): the M=1 kernels
  * carry q * log2(e) / sqrt(D) as an fp16 hi + lo pair, so |q| < 65504 * sqrt(D) / log2(e)
- * (e.g. 363,000 at D = 64) is the valid range. The error word and the selector's counters
+ * (e.g. 363,000 at D = 64) is the valid range; 8 a page number, 9 a rotary position, 10 a cache
+ * length out of range (the paged-tail calls); 11 a page tile of a one-row paged attention. The error word and the selector's counters
  * are then reset, so the context stays usable. */
 int pck_sync(pck_ctx *ctx, void *stream);
 

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libpck.so")
 OK, MISS, COLDMISS = 0, 1, 3
 EINVAL, EUNSUPPORTED, ENOMEM, ECUDA = -1, -2, -3, -4
 FMT_FP16, FMT_MLX4G32 = 0, 1
-DT_F32, DT_F16 = 0, 1
+DT_F32, DT_F16, DT_BF16 = 0, 1, 2
 MAX_BATCH = 64
 
 # Every symbol include/pck.h declares.
@@ -26,7 +26,8 @@ EXPORTS = (
     "pck_drop", "pck_build_block_means", "pck_query", "pck_query_fused", "pck_query_sparse_auto",
     "pck_query_sparse_auto_fused", "pck_query_batch", "pck_query_sparse_batch", "pck_quantize_mlx4g32", "pck_info", "pck_sync",
     "pck_attend_records_noalloc", "pck_noalloc_status", "pck_query_sparse", "pck_get_block_means",
-    "pck_dequantize_mlx4g32", "pck_query_batch_host",
+    "pck_dequantize_mlx4g32", "pck_query_batch_host", "pck_qk_norm_rope", "pck_paged_append", "pck_paged_attend",
+    "pck_paged_workspace",
 )
 
 
@@ -50,6 +51,27 @@ class SparseDesc(ctypes.Structure):
     _fields_ = [("sid", ctypes.c_char_p), ("layer", ctypes.c_int), ("Q", ctypes.c_void_p), ("O", ctypes.c_void_p),
                 ("LSE", ctypes.c_void_p), ("K_suf", ctypes.c_void_p), ("V_suf", ctypes.c_void_p),
                 ("idx_out", ctypes.c_void_p)]
+
+
+class PagedCacheT(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("dtype", ctypes.c_int), ("H_kv", ctypes.c_int),
+                ("D", ctypes.c_int), ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int64)] + [
+                    (n, ctypes.c_int64) for n in ("k_page", "k_head", "k_token", "v_page", "v_head", "v_token")]
+
+
+class PagedBatchT(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("cu_rows", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("max_rows", ctypes.c_int)]
+
+
+class RotaryT(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int), ("R", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p)]
+
+
+class RowsT(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("H", ctypes.c_int)] + [
+        (n, ctypes.c_int64) for n in ("in_row", "in_head", "out_row", "out_head")] + [("weight", ctypes.c_void_p)]
 
 
 _lib = None
@@ -88,6 +110,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "pck_query_sparse": (i, [vp, cp, i, i, i, i, i, vp, vp, vp, vp, i, vp, vp, vp]),
         "pck_get_block_means": (i, [vp, cp, i, i, vp, vp]),
         "pck_dequantize_mlx4g32": (i, [vp, i64, i, i, i, vp, vp]),
+        "pck_qk_norm_rope": (i, [vp, i, i, i, vp, vp, i, ctypes.c_float, vp, vp]),
+        "pck_paged_append": (i, [vp, vp, vp, i, vp, vp, vp, i, ctypes.c_float, vp, vp]),
+        "pck_paged_attend": (i, [vp, vp, vp, i, vp, i64, i64, i, i, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "pck_paged_workspace": (i, [vp, vp, vp, i, i, i, ctypes.POINTER(ctypes.c_size_t)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -213,6 +239,85 @@ def dequantize_mlx4g32(records: torch.Tensor, N: int, H_kv: int, D: int, dtype=t
     return out
 
 
+# ---- paged tail: marshalling
+_PAGED_DT = {torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+_ROWS_DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+
+
+def _need(t, name, dtype, shape, strided=False):
+    """t is a tensor of this dtype and shape, contiguous, or (strided) contiguous in its last dimension."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if strided:
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _on(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: must be on the CUDA device {device}, not {t.device}")
+
+
+def _rows(t, out, weight):
+    """pck_rows of t [T, H, D] (None: no rows of this kind)."""
+    if t is None:
+        return None
+    o = (0, 0) if out is None else out.stride()
+    return RowsT(t.data_ptr(), None if out is None else out.data_ptr(), t.shape[1], t.stride(0), t.stride(1), o[0], o[1],
+                 None if weight is None else weight.data_ptr())
+
+
+def _rotary(cos_sin, interleaved, positions):
+    if cos_sin is None:
+        return None
+    return RotaryT(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
+                   None if positions is None else positions.data_ptr())
+
+
+def _check_rope(cos_sin, positions, T):
+    if cos_sin is None:
+        if positions is not None:
+            raise ValueError("positions without cos_sin")
+        return
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [n_pos, R]")
+    _need(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (T,))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+class PagedCache:
+    """A paged KV cache: k and v [n_pages, H_kv, page_size, D], fp16 or bf16, of the caller's. Any
+    strides with D contiguous do: for pages stored [n_pages, page_size, H_kv, D] pass their
+    transpose(1, 2). Holds the tensors and the descriptor that the calls take; checked once, here."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("k and v must be [n_pages, H_kv, page_size, D] tensors of one shape and dtype")
+        if k.dtype not in _PAGED_DT:
+            raise ValueError(f"k: dtype {k.dtype}, expected float16 or bfloat16")
+        for t, name in ((k, "k"), (v, "v")):
+            _need(t, name, k.dtype, k.shape, strided=True)
+        for t, name in ((k, "k"), (v, "v")):
+            if not t.is_cuda:
+                raise ValueError(f"{name}: must be on the CUDA device")
+        _on(k.device, v=v)
+        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.n_pages, self.H_kv, self.page_size, self.D = k.shape
+        self.c = PagedCacheT(k.data_ptr(), v.data_ptr(), _PAGED_DT[k.dtype], self.H_kv, self.D, self.page_size,
+                             self.n_pages, *k.stride()[:3], *v.stride()[:3])
+        self._ws = {}   # workspace bytes by the sizes of a call
+
+
 class Context:
     """One libpck context (slot table + workspaces) on one device."""
 
@@ -224,6 +329,7 @@ class Context:
         if rc != OK:
             raise PckError(rc, "pck_create failed")
         self.h = h
+        self.device = torch.device("cuda", device)
 
     def close(self):
         if getattr(self, "h", None):
@@ -428,6 +534,161 @@ class Context:
                 raise PckError(rc, self.last_error())
         call._keep = (arr, keep, hm)
         return call
+
+    # ---- paged tail
+    def _launch(self, fn, stream, *args):
+        """fn(context, *args, stream) on the given stream, or the current one of the context's device."""
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        rc = fn(self.h, *args, s.cuda_stream)
+        if rc != OK:
+            raise PckError(rc, self.last_error())
+
+    def _empty(self, stream, *shape, dtype):
+        """A new tensor that the call writes on `stream` (None: the current one) and the caller uses on its own."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+    def _batch(self, cache, table, kv_len, cu_rows, T, max_rows):
+        B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        if table.dim() != 2 or B < 0:
+            raise ValueError("kv_len must be [B] and table [B, max_pages]")
+        W = table.shape[1]
+        _need(kv_len, "kv_len", torch.int32, (B,))
+        _need(table, "table", torch.int32, (B, W))
+        if cu_rows is None:
+            if T != B:
+                raise ValueError(f"{T} rows for {B} sequences: cu_rows is needed")
+            max_rows = 1
+        else:
+            _need(cu_rows, "cu_rows", torch.int32, (B + 1,))
+            max_rows = T if max_rows is None else max_rows
+        if cache.device != self.device:
+            raise ValueError(f"cache: must be on the CUDA device {self.device}, not {cache.device}")
+        _on(self.device, kv_len=kv_len, table=table, cu_rows=cu_rows)
+        return PagedBatchT(B, T, None if cu_rows is None else cu_rows.data_ptr(), kv_len.data_ptr(), table.data_ptr(), W,
+                           max_rows)
+
+    def qk_norm_rope(self, Q, K, positions=None, cos_sin=None, norm=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, Q_out=None, K_out=None, stream=None):
+        """RMS norm of each head of Q [T, H_q, D] and K [T, H_kv, D] (either may be None), then the rotation of the
+        first R elements by row positions[t] of cos_sin [n_pos, R]. norm: None norms when a weight is given.
+        Q_out, K_out (the inputs themselves for in place) are allocated when not given. Returns (Q_out, K_out)."""
+        one = Q if Q is not None else K
+        if one is None or one.dim() != 3:
+            raise ValueError("Q [T, H_q, D], K [T, H_kv, D] or both must be given")
+        T, _, D = one.shape
+        if one.dtype not in _ROWS_DT:
+            raise ValueError(f"dtype {one.dtype}, expected float32, float16 or bfloat16")
+        norm = (q_weight is not None or k_weight is not None) if norm is None else bool(norm)
+        for t, o, w, n in ((Q, Q_out, q_weight, "Q"), (K, K_out, k_weight, "K")):
+            if t is None:
+                if o is not None or w is not None:
+                    raise ValueError(f"{n}_out or a weight without {n}")
+                continue
+            if t.dim() != 3:
+                raise ValueError(f"{n} must be [T, H, D]")
+            _need(t, n, one.dtype, (T, t.shape[1], D), strided=True)
+            if o is not None:
+                _need(o, n + "_out", one.dtype, t.shape, strided=True)
+            if w is not None:
+                _need(w, n + "_weight", one.dtype, (D,))
+        if not norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("a weight without the norm")
+        _check_rope(cos_sin, positions, T)
+        if cos_sin is not None and positions is None:
+            raise ValueError("cos_sin without positions")
+        _on(self.device, Q=Q, K=K, Q_out=Q_out, K_out=K_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+            positions=positions)
+        if Q is not None and Q_out is None:
+            Q_out = self._empty(stream, *Q.shape, dtype=Q.dtype)
+        if K is not None and K_out is None:
+            K_out = self._empty(stream, *K.shape, dtype=K.dtype)
+        self._launch(self.lib.pck_qk_norm_rope, stream, _ROWS_DT[one.dtype], T, D, _ref(_rows(Q, Q_out, q_weight)),
+                     _ref(_rows(K, K_out, k_weight)), int(norm), eps, _ref(_rotary(cos_sin, interleaved, positions)))
+        return Q_out, K_out
+
+    def paged_append(self, cache, table, kv_len, K, V, Q=None, cu_rows=None, cos_sin=None, positions=None, norm=None,
+                     q_weight=None, k_weight=None, eps=1e-6, interleaved=False, Q_out=None, stream=None):
+        """Store K (normed and rotated as by qk_norm_rope) and V rows [T, H_kv, D] into the cache slots of the last
+        rows of each sequence (see pck_paged_batch; kv_len counts them), and norm and rotate Q [T, H_q, D] in the
+        same pass. positions: None takes the cache positions. Returns Q_out (None without Q)."""
+        if K.dim() != 3 or K.shape[1:] != (cache.H_kv, cache.D):
+            raise ValueError(f"K must be [T, {cache.H_kv}, {cache.D}]")
+        T, D, dt = K.shape[0], cache.D, K.dtype
+        if dt != cache.dtype and dt != torch.float32:
+            raise ValueError(f"K: dtype {dt}, expected {cache.dtype} or float32")
+        _need(K, "K", dt, K.shape, strided=True)
+        _need(V, "V", dt, K.shape, strided=True)
+        if Q is not None:
+            if Q.dim() != 3:
+                raise ValueError("Q must be [T, H_q, D]")
+            _need(Q, "Q", dt, (T, Q.shape[1], D), strided=True)
+            if Q_out is not None:
+                _need(Q_out, "Q_out", dt, Q.shape, strided=True)
+        elif Q_out is not None or q_weight is not None:
+            raise ValueError("Q_out or q_weight without Q")
+        norm = (q_weight is not None or k_weight is not None) if norm is None else bool(norm)
+        for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                if not norm:
+                    raise ValueError("a weight without the norm")
+                _need(w, n, dt, (D,))
+        _check_rope(cos_sin, positions, T)
+        batch = self._batch(cache, table, kv_len, cu_rows, T, None)
+        _on(self.device, K=K, V=V, Q=Q, Q_out=Q_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+            positions=positions)
+        if Q is not None and Q_out is None:
+            Q_out = self._empty(stream, *Q.shape, dtype=dt)
+        self._launch(self.lib.pck_paged_append, stream, _ref(cache.c), _ref(batch), _ROWS_DT[dt],
+                     _ref(_rows(Q, Q_out, q_weight)), _ref(_rows(K, None, k_weight)), _ref(_rows(V, None, None)),
+                     int(norm), eps, _ref(_rotary(cos_sin, interleaved, positions)))
+        return Q_out
+
+    def paged_attend(self, cache, table, kv_len, Q, cu_rows=None, max_rows=None, window=0, sinks=0, prior=None, O=None,
+                     LSE=None, want_lse=True, workspace=None, stream=None):
+        """Attention of Q [T, H_q, D] over the cached tokens of its sequences (see pck_paged_attend); prior: (O, LSE)
+        of the same rows over other keys, fp32, merged in. max_rows bounds the rows of a sequence (default: T with
+        cu_rows, else 1). Outputs and the workspace are allocated when not given. Returns (O, LSE)."""
+        if Q.dim() != 3 or Q.shape[2] != cache.D:
+            raise ValueError(f"Q must be [T, H_q, {cache.D}]")
+        T, H_q, D = Q.shape
+        _need(Q, "Q", cache.dtype, Q.shape, strided=True)
+        if O is not None:
+            _need(O, "O", cache.dtype, Q.shape)
+        if LSE is not None:
+            _need(LSE, "LSE", torch.float32, (T, H_q))
+        Op, Lp = (None, None) if prior is None else prior
+        if prior is not None:
+            _need(Op, "prior O", torch.float32, Q.shape)
+            _need(Lp, "prior LSE", torch.float32, (T, H_q))
+        batch = self._batch(cache, table, kv_len, cu_rows, T, max_rows)
+        _on(self.device, Q=Q, O=O, LSE=LSE, prior_O=Op, prior_LSE=Lp, workspace=workspace)
+        key = (batch.B, T, batch.max_pages, batch.max_rows, cu_rows is None, H_q, window, sinks, self.h.value)
+        need = cache._ws.get(key)
+        if need is None:
+            n = ctypes.c_size_t()
+            self._rc(self.lib.pck_paged_workspace(self.h, _ref(cache.c), _ref(batch), H_q, window, sinks, _ref(n)))
+            if len(cache._ws) >= 256:
+                cache._ws.clear()
+            need = cache._ws[key] = n.value
+        if workspace is None:
+            workspace = self._empty(stream, need, dtype=torch.uint8) if need else None
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        if O is None:
+            O = self._empty(stream, T, H_q, D, dtype=cache.dtype)
+        if LSE is None and want_lse:
+            LSE = self._empty(stream, T, H_q, dtype=torch.float32)
+        self._launch(self.lib.pck_paged_attend, stream, _ref(cache.c), _ref(batch), H_q, Q.data_ptr(), Q.stride(0),
+                     Q.stride(1), window, sinks, None if Op is None else Op.data_ptr(),
+                     None if Lp is None else Lp.data_ptr(), O.data_ptr(), None if LSE is None else LSE.data_ptr(),
+                     None if workspace is None else workspace.data_ptr(),
+                     0 if workspace is None else workspace.numel() * workspace.element_size())
+        return O, LSE
 
     def info(self) -> dict:
         out = InfoT()

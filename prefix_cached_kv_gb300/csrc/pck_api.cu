@@ -22,6 +22,7 @@
 #include "../../include/pck.h"
 #include "pck_common.cuh"
 #include "pck_kernels.h"
+#include "pck_paged.cuh"
 
 using namespace pck;
 
@@ -408,6 +409,23 @@ int run_decode(pck_ctx* c, int fmt, int D, int H_q, int H_kv, int S_suf, int q_f
 bool dtype_ok(int dt) { return dt == PCK_DT_F32 || dt == PCK_DT_F16; }
 
 }  // namespace
+
+namespace pck {
+
+CtxView ctx_view(pck_ctx* c) { return CtxView{c->device, c->sms, c->dev_err}; }
+
+int ctx_fail(pck_ctx* c, int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(c, code, "%s", buf);
+}
+
+void ctx_count_query(pck_ctx* c) { ++c->queries; }
+
+}  // namespace pck
 
 extern "C" {
 
@@ -1165,6 +1183,9 @@ int pck_sync(pck_ctx* c, void* stream) {
         cudaMemset(c->dev_err, 0, sizeof(int));
         cudaMemset(c->counters, 0, WS_COUNTERS * sizeof(int));
         cudaDeviceSynchronize();
+        if (herr >= ERR_PAGE_ID && herr <= ERR_KV_LEN)
+            return fail(c, PCK_ECUDA, "a value on the device is out of range (code %d: %s); results of the affected calls are invalid",
+                        herr, herr == ERR_PAGE_ID ? "page number" : herr == ERR_ROPE_POS ? "rotary position" : "cache length");
         return fail(c, PCK_ECUDA, "a device wait gave up (code %d); results of the affected calls are invalid", herr);
     }
     return PCK_OK;

@@ -1,0 +1,672 @@
+// pck_paged_token.cu -- attention of one new token per sequence over a paged KV cache, split over
+// the cache's length and joined.
+//
+// Per sequence b (n = kv_len[b] keys, the new token's own among them) and q head h of kv head g:
+//   s_j = tau q_h . k_j,  O = sum_j 2^(s_j' - m) v_j / l,  LSE = (m + log2 l) ln 2   (s' = s log2 e)
+// over the visible keys: all n, or with a window W the last W and the first `sinks`.
+//
+// Every K and V byte is read once and used for G = H_q / H_kv heads: 4 G flop per 4 bytes, so HBM
+// bounds it and the kernel's business is to keep loads in flight on every SM whatever the lengths:
+//  * A unit is a cache tile of 16 tokens of one kv head (a page is a multiple of 16, so a unit never
+//    leaves its page). The units of all items (sequence, kv head, group of q heads) laid end to end
+//    are cut into equal ranges, one per CTA, from the lengths on the device (one block scan per
+//    CTA), so a ragged batch, one long sequence and many short ones all load every SM evenly, and
+//    a captured graph follows the lengths it finds.
+//  * One CTA per SM; each warp streams every NW-th unit of the range through a ring of its own
+//    (two TMA tile loads a unit, 128-byte swizzle, evict-first: read once). Lane i of a warp
+//    resolves the i-th of its next 32 units (sequence, tile, page number) at once, so page-table
+//    latency is paid once in 32 units and off the critical path; rings run on across items.
+//  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads as columns; the running
+//    maximum moves only when a score passes it by 8 (log2), so every p <= 2^8; p goes into
+//    O^T += V^T p^T as a 16-bit hi + lo pair (two MMAs into one accumulator), which keeps ~22 bits
+//    (16 for bf16) of p: the result's own rounding is then the only visible one, and these MMAs are
+//    hidden behind the loads.
+//  * At the end of an item the CTA's warps join through shared memory. An item that lies within
+//    one CTA's range is finished there; one that crosses CTAs leaves a partial [m, l, O] per CTA,
+//    at most two per CTA, and a second, programmatically launched kernel joins them.
+//  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA of its own and
+//    nothing is joined: one launch.
+#include "pck_paged.cuh"
+
+namespace pck {
+namespace {
+
+constexpr int TK_DIRECT_UNITS = 32;    // 512 tokens
+constexpr int TK_MIN_UNITS = 16;       // units per CTA at least, when ranges are cut
+constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
+
+template <int D>
+struct TCfg {
+    static constexpr int NW = D <= 128 ? 8 : 4;                   // warps per CTA
+    static constexpr int UNIT = PG_SUB * D * 2;                   // bytes of a K (or V) unit
+    static constexpr int STAGE = 2 * UNIT;
+    static constexpr int ST = D <= 64 ? 6 : D == 192 ? 4 : 3;     // stages of a warp's ring
+    static constexpr int RING = NW * ST * STAGE;
+    static constexpr int JROW = D / 2 + 4;                        // floats of a join row (half of D, padded)
+    static constexpr int JOIN = NW * 8 * JROW * 4;
+    static constexpr int OFF_JOIN = RING;
+    static constexpr int OFF_ML = OFF_JOIN + JOIN;                // [NW][16] m, then l
+    static constexpr int OFF_BAR = OFF_ML + NW * 16 * 2 * 4;
+    static constexpr int OFF_SCAN = OFF_BAR + NW * ST * 8 + 8;
+    static constexpr int OFF_PRE = OFF_SCAN + 64 * 4;             // prefix of units per sequence [B + 1]
+    static constexpr int SMEM_BASE = OFF_PRE + 1024;              // + alignment slack; + 4 (B + 1)
+};
+
+template <typename T> struct Elem;
+template <> struct Elem<__half> {
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        mma16816(c, a, b0, b1);
+    }
+    static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) { split_hi_lo(x0, x1, hi, lo); }
+    static __device__ __forceinline__ uint32_t pack(float x0, float x1) { return h2_as_u32(__floats2half2_rn(x0, x1)); }
+};
+template <> struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t pack(float x0, float x1) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+        hi = pack(x0, x1);
+        lo = pack(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+    }
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* tm, int tok, int head, int page, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+        ::"r"(dst), "l"(tm), "r"(0), "r"(tok), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(pol) : "memory");
+}
+
+// The units (cache tiles of 16 tokens) that one sequence's row reads: tiles [0, ns) hold the sinks,
+// then come tiles [w0, w0 + n - ns). A sequence without keys has one unit with nothing visible.
+struct Span {
+    int n, ns, w0;
+};
+__device__ __forceinline__ Span span_of(int len, int window, int sinks) {
+    Span s;
+    const int end = (len + PG_SUB - 1) / PG_SUB;
+    s.ns = 0;
+    s.w0 = 0;
+    if (window > 0 && len > window) {
+        s.w0 = (len - window) / PG_SUB;
+        s.ns = min((min(sinks, len) + PG_SUB - 1) / PG_SUB, s.w0);
+    }
+    s.n = max(1, s.ns + end - s.w0);
+    return s;
+}
+
+__device__ __forceinline__ int clamp_len(const PagedAttn& P, int b, bool report) {
+    int len = P.kv_len[b];
+    const int64_t most = (int64_t)P.max_pages * P.page;
+    if (len > most) {
+        if (report) set_err(P.err, ERR_KV_LEN);
+        len = static_cast<int>(most);
+    }
+    return max(len, 0);
+}
+
+// Weight of a part with maximum m in a join at M. A part without a visible key has m = -inf and sums of 0 (or
+// NaN, from a NaN score), which weight 1 passes on.
+__device__ __forceinline__ float join_weight(float m, float M) { return m > -INFINITY ? ex2_approx(m - M) : 1.f; }
+
+// Writes row (t, hq): O = acc / l merged with the prior, and the LSE. Called by each thread for its
+// elements d, d + 1; `first` also writes the LSE.
+template <typename T>
+__device__ __forceinline__ void finish2(const PagedAttn& P, int t, int hq, int D, int d, float a0, float a1, float m, float l,
+                                        bool first) {
+    const int64_t row = (int64_t)t * P.H_q + hq;
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.0f / l;
+    float lse = none ? -INFINITY : (m + log2f(l)) * PG_LN2;
+    a0 *= inv;
+    a1 *= inv;
+    if (P.O_prior) {
+        const float lp = P.LSE_prior[row];
+        if (lp != -INFINITY) {
+            const float mx = fmaxf(lse, lp);
+            const float wn = expf(lse - mx), wp = expf(lp - mx), sum = wn + wp;
+            const float2 op = *reinterpret_cast<const float2*>(P.O_prior + row * D + d);
+            a0 = none ? op.x : (a0 * wn + op.x * wp) / sum;
+            a1 = none ? op.y : (a1 * wn + op.y * wp) / sum;
+            lse = mx + logf(sum);
+        }
+    }
+    *reinterpret_cast<uint32_t*>(static_cast<T*>(P.O) + row * D + d) = Elem<T>::pack(a0, a1);
+    if (first && P.LSE) P.LSE[row] = lse;
+}
+
+// Partial of a CTA (two slots per CTA): [heads][D + 4] floats: m, l, -, -, O (not normalised).
+__host__ __device__ constexpr int slot_floats(int D, int heads) { return heads * (D + 4); }
+
+// A split item's descriptor, written by the CTA in which it begins (pieces = 0: none).
+struct JoinDesc {
+    int b, x, pieces, pad;
+};
+
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const __grid_constant__ PagedAttn P) {
+    using C = TCfg<D>;
+    constexpr int NW = C::NW, ST = C::ST, KS = D / 16, NT = NW * 32;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_base = smem_u32(smem);
+    float* jbuf = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+    float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+    float* s_l = s_m + NW * 16;
+    int* s_scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+    int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ring = s_base + warp * ST * C::STAGE;
+    const uint32_t bar = s_base + C::OFF_BAR + warp * ST * 8;
+    if (lane == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, 1);
+        fence_mbar_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_v) : "memory");
+    }
+    pdl_wait();
+    pdl_release();
+
+    // ---- this CTA's range of units
+    const int Hg = P.H_kv * P.n_groups;
+    const int B = P.B;
+    int64_t u0, u1;            // units of all items end to end
+    int64_t U = 0;
+    int ncta = gridDim.x;
+    int b_first = 0;
+    if (P.split) {
+        // units before each sequence (per kv head and group): a scan over the lengths
+        const int per = (B + NT - 1) / NT;
+        int sum = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < B) sum += span_of(clamp_len(P, b, blockIdx.x == 0), P.window, P.sinks).n;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int base = 0;
+        for (int w = 0; w < warp; ++w) base += s_scan[w];
+        int run = base + inc - sum;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < B) {
+                pre[b] = run;
+                run += span_of(clamp_len(P, b, false), P.window, P.sinks).n;
+            }
+        }
+        if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
+        __syncthreads();
+        U = (int64_t)pre[B] * Hg;
+        // at least TK_MIN_UNITS units a CTA
+        const int64_t most = (U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
+        if (most < ncta) ncta = static_cast<int>(most);
+        if ((int)blockIdx.x >= ncta) {
+            if (tid == 0) {
+                JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * gridDim.x * slot_floats(D, P.heads_per_group));
+                jd[blockIdx.x].pieces = 0;
+            }
+            return;
+        }
+        u0 = U * blockIdx.x / ncta;
+        u1 = U * (blockIdx.x + 1) / ncta;
+    } else {
+        b_first = blockIdx.x / Hg;
+        const int n = span_of(clamp_len(P, b_first, true), P.window, P.sinks).n;
+        if (tid == 0) {
+            pre[0] = 0;
+            pre[1] = n;
+        }
+        __syncthreads();
+        u0 = (int64_t)(blockIdx.x - b_first * Hg) * n;
+        u1 = u0 + n;
+    }
+    const int nseq = P.split ? B : 1;   // sequences in pre[]
+
+    // ---- a warp's units: u0 + warp + k NW. Lane i resolves unit k0 + i: coordinates of its loads.
+    const uint64_t pol = l2_evict_first();
+    int pl_tok = 0, pl_head = 0, pl_page = 0;
+    auto resolve = [&](int k0) {
+        const int64_t u = u0 + warp + (int64_t)(k0 + lane) * NW;
+        if (u < u1) {
+            const int v = static_cast<int>(u / Hg);
+            int lo = 0, hi = nseq - 1;      // the sequence with pre[b] <= v < pre[b + 1]
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= v) lo = mid;
+                else hi = mid - 1;
+            }
+            const int b = b_first + lo;
+            const int n = pre[lo + 1] - pre[lo];
+            const int64_t rem = u - (int64_t)pre[lo] * Hg;
+            const int x = static_cast<int>(rem / n), j = static_cast<int>(rem - (int64_t)x * n);
+            const int len = clamp_len(P, b, false);
+            const Span s = span_of(len, P.window, P.sinks);
+            const int tile = j < s.ns ? j : j - s.ns + s.w0;
+            const int tok = tile * PG_SUB;
+            const int pi = tok / P.page;
+            pl_tok = tok - pi * P.page;
+            pl_head = x / P.n_groups;
+            pl_page = 0;
+            if (len > 0) {
+                const int pg = P.table[(int64_t)b * P.max_pages + pi];
+                if (pg < 0 || pg >= P.n_pages) set_err(P.err, ERR_PAGE_ID);   // and page 0 is read instead
+                else pl_page = pg;
+            }
+        }
+    };
+    const int nk = static_cast<int>(u1 - u0 > warp ? (u1 - u0 - warp + NW - 1) / NW : 0);   // units of this warp
+    int kp = 0;                          // next unit to load
+    auto produce = [&]() {
+        if (kp >= nk) return;
+        if ((kp & 31) == 0) resolve(kp);
+        const int tok = __shfl_sync(0xffffffffu, pl_tok, kp & 31);
+        const int head = __shfl_sync(0xffffffffu, pl_head, kp & 31);
+        const int page = __shfl_sync(0xffffffffu, pl_page, kp & 31);
+        const int st = kp % ST;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar + 8 * st, C::STAGE);
+            tma_5d(ring + st * C::STAGE, &P.tm_k, tok, head, page, bar + 8 * st, pol);
+            tma_5d(ring + st * C::STAGE + C::UNIT, &P.tm_v, tok, head, page, bar + 8 * st, pol);
+        }
+        ++kp;
+    };
+    for (int i = 0; i < ST; ++i) produce();
+
+    // ---- items of the range, in order
+    bool failed = false;
+    int k_failed = 0;                    // the unit whose copy never landed
+    int k = 0;                           // next unit to consume
+    int64_t u = u0;                      // first unit of the current piece
+    int bi = 0;                          // index into pre[] of the current sequence
+    {
+        const int v = static_cast<int>(u0 / Hg);
+        int hi = nseq - 1;
+        while (bi < hi) {
+            const int mid = (bi + hi + 1) >> 1;
+            if (pre[mid] <= v) bi = mid;
+            else hi = mid - 1;
+        }
+    }
+    const int heads = P.heads_per_group;
+    JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * gridDim.x * slot_floats(D, heads));
+    bool crosses = false;                // an item begins here and goes on in the next CTA
+    while (u < u1) {
+        while ((int64_t)pre[bi + 1] * Hg <= u) ++bi;
+        const int b = b_first + bi;
+        const int n = pre[bi + 1] - pre[bi];
+        const int64_t first_of_b = (int64_t)pre[bi] * Hg;
+        const int x = static_cast<int>((u - first_of_b) / n);
+        const int64_t a = first_of_b + (int64_t)x * n, e = a + n;   // the item's units
+        const int64_t pe = e < u1 ? e : u1;                         // end of this CTA's piece
+        const int g = x / P.n_groups, grp = x - g * P.n_groups;
+        const int hq0 = g * P.G + grp * heads;
+        const int nq = min(heads, P.G - grp * heads);
+        const int len = clamp_len(P, b, false);
+        const Span sp = span_of(len, P.window, P.sinks);
+        const int lo_key = P.window > 0 && len > P.window ? len - P.window : 0;   // first key of the window
+
+        // q as the B operand: head (column) lane / 4, elements 16 s + 2 (lane % 4) and + 8
+        uint32_t qf[NB][KS][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int col = nb * 8 + (lane >> 2);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(P.Q) + (int64_t)b * P.q_row +
+                                                                  (int64_t)(hq0 + col) * P.q_head) + (lane & 3);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                qf[nb][s][0] = col < nq ? q[8 * s] : 0u;
+                qf[nb][s][1] = col < nq ? q[8 * s + 4] : 0u;
+            }
+        }
+        float o[NB][KS][4];
+        float m[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nb][s][i] = 0.f;
+        }
+        for (; k < nk; ++k) {
+            const int64_t uk = u0 + warp + (int64_t)k * NW;
+            if (uk >= pe) break;
+            const int j = static_cast<int>(uk - a);
+            const int tile = j < sp.ns ? j : j - sp.ns + sp.w0;
+            const int st = k % ST;
+            const uint32_t ks = ring + st * C::STAGE, vs = ks + C::UNIT;
+            if (!failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + 8 * st, (k / ST) & 1))) {
+                failed = true;
+                k_failed = k;
+            }
+            if (failed) continue;
+            // visible keys of the tile: token t of it is key key0 + t
+            const int key0 = tile * PG_SUB;
+            const bool full = key0 + PG_SUB <= len && (key0 >= lo_key || key0 + PG_SUB <= P.sinks);
+            auto seen = [&](int t) { return key0 + t < len && (key0 + t >= lo_key || key0 + t < P.sinks); };
+            if (!full) {
+                // hidden V rows may hold anything (also NaN, which 0 * v would keep): zero them
+                for (int t = 0; t < PG_SUB; ++t)
+                    if (!seen(t))
+                        for (int c = lane; c < D / 8; c += 32)
+                            *reinterpret_cast<uint4*>(smem + (vs - s_base) + (c >> 3) * (PG_SUB * 128) + t * 128 + (c & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            // S^T = K q^T
+            float s4[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s4[nb][i] = 0.f;
+            {
+                const int r = lane & 15, half = lane >> 4;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int c = 2 * s + half;
+                    uint32_t af[4];
+                    ldsm_x4(ks + (c >> 3) * (PG_SUB * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), af);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) Elem<T>::mma(s4[nb], af, qf[nb][s][0], qf[nb][s][1]);
+                }
+            }
+            // lane: tokens lane / 4 and + 8, heads 2 (lane % 4) and + 1 of each column block
+            const int t0 = lane >> 2;
+            bool up = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = s4[nb][i] * P.scale_log2;
+                    if (!full && !seen(t0 + (i >> 1) * 8)) v = -INFINITY;
+                    s4[nb][i] = v;
+                    up |= !(v <= m[nb][i & 1] + 8.f);   // (a NaN too)
+                }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float mx = fmaxf(s4[nb][i], s4[nb][i + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        mx = fmaxf(mx, m[nb][i]);
+                        const float al = m[nb][i] > -INFINITY ? ex2_approx(m[nb][i] - mx) : 0.f;
+                        m[nb][i] = mx;
+                        l[nb][i] *= al;
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) {
+                            o[nb][s][i] *= al;
+                            o[nb][s][i + 2] *= al;
+                        }
+                    }
+            }
+            // p, its sum, and its transpose (tokens as k) as hi + lo B fragments
+            uint32_t ph[NB][2], plo[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ex2_approx(s4[nb][2 * r] - (m[nb][0] > -INFINITY ? m[nb][0] : 0.f));
+                    const float p1 = ex2_approx(s4[nb][2 * r + 1] - (m[nb][1] > -INFINITY ? m[nb][1] : 0.f));
+                    l[nb][0] += p0;
+                    l[nb][1] += p1;
+                    uint32_t hi, lo;
+                    Elem<T>::split(p0, p1, hi, lo);
+                    ph[nb][r] = movmatrix_trans(hi);
+                    plo[nb][r] = movmatrix_trans(lo);
+                }
+            // O^T += V^T p^T
+            {
+                const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int c = 2 * s + half;
+                    uint32_t af[4];
+                    ldsm_x4_t(vs + (c >> 3) * (PG_SUB * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), af);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        Elem<T>::mma(o[nb][s], af, ph[nb][0], ph[nb][1]);
+                        Elem<T>::mma(o[nb][s], af, plo[nb][0], plo[nb][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            produce();
+        }
+        // ---- the CTA's warps join: maxima and sums first, then O in two halves of D per column block
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float s = l[nb][i];
+                s += __shfl_xor_sync(0xffffffffu, s, 4);
+                s += __shfl_xor_sync(0xffffffffu, s, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 16);
+                if (lane < 4) {
+                    s_m[warp * 16 + nb * 8 + 2 * lane + i] = m[nb][i];
+                    s_l[warp * 16 + nb * 8 + 2 * lane + i] = s;
+                }
+            }
+        __syncthreads();
+        const bool whole = a >= u0 && e <= u1;
+        const int slot = a < u0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1;
+        float* part = P.ws + (size_t)slot * slot_floats(D, heads);
+        if (a >= u0 && e > u1) crosses = true;
+        if (tid == 0 && P.split && a >= u0 && e > u1) {
+            // the item's last unit e - 1 lies in CTA ((e ncta) - 1) / U
+            const int last = static_cast<int>((e * ncta - 1) / U);
+            jd[blockIdx.x] = JoinDesc{b, x, last - (int)blockIdx.x + 1, 0};
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float al[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * (lane & 3) + i]);
+                al[i] = join_weight(m[nb][i], M);
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float* row = jbuf + (warp * 8 + 2 * (lane & 3)) * C::JROW + (lane >> 2);
+#pragma unroll
+                for (int s = 0; s < KS / 2; ++s) {
+                    const float (&v)[4] = o[nb][hf * (KS / 2) + s];
+                    row[16 * s] = v[0] * al[0];
+                    row[C::JROW + 16 * s] = v[1] * al[1];
+                    row[16 * s + 8] = v[2] * al[0];
+                    row[C::JROW + 16 * s + 8] = v[3] * al[1];
+                }
+                __syncthreads();
+                for (int i = tid; i < 8 * (D / 4); i += NT) {   // (head, pair of elements)
+                    const int h = i / (D / 4), d = 2 * (i - h * (D / 4));
+                    const int lh = nb * 8 + h;
+                    if (lh < nq) {
+                        float M = -INFINITY, L = 0.f;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
+                        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const float mw = s_m[w * 16 + lh];
+                            L += s_l[w * 16 + lh] * join_weight(mw, M);
+                            const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * 8 + h) * C::JROW + d);
+                            a0 += f.x;
+                            a1 += f.y;
+                        }
+                        const int dd = hf * (D / 2) + d;
+                        if (whole) {
+                            finish2<T>(P, b, hq0 + lh, D, dd, a0, a1, M, L, dd == 0);
+                        } else {
+                            float* pr = part + lh * (D + 4);
+                            *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
+                            if (dd == 0) {
+                                pr[0] = M;
+                                pr[1] = L;
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        u = pe;
+    }
+    if (P.split && tid == 0 && !crosses) jd[blockIdx.x].pieces = 0;
+    if (failed) {
+        set_err(P.err, ERR_PAGED_TOKEN);
+        for (k = k_failed; k < kp; ++k)   // copies still in flight, waited for with the same limit
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + 8 * (k % ST), (k / ST) & 1))) break;
+    }
+}
+
+// Joins the partials of one split item and one q head: CTA (c, h) takes the item that begins in
+// CTA c of the attention launch. NT / (D/4) pieces at a time, one float4 of the row a thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_constant__ PagedAttn P) {
+    constexpr int LP = D / 4, NP = 256 / LP;
+    __shared__ float4 s_acc[NP][LP];
+    pdl_wait();
+    pdl_release();
+    const int c = blockIdx.x, h = blockIdx.y;
+    const int heads = P.heads_per_group;
+    const JoinDesc jd = reinterpret_cast<const JoinDesc*>(P.ws + (size_t)2 * P.n_ctas * slot_floats(D, heads))[c];
+    if (jd.pieces == 0) return;
+    const int g = jd.x / P.n_groups, grp = jd.x - g * P.n_groups;
+    if (grp * heads + h >= P.G) return;
+    const int hq = g * P.G + grp * heads + h;
+    const int tid = threadIdx.x, pp = tid / LP, q = tid - pp * LP;
+    // piece i: slot 2 c + 1 for the first, 2 (c + i) for the others
+    auto part = [&](int i) { return P.ws + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_floats(D, heads) + h * (D + 4); };
+    float M = -INFINITY;
+    for (int i = tid & 31; i < jd.pieces; i += 32) M = fmaxf(M, part(i)[0]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int i = tid & 31; i < jd.pieces; i += 32) {
+        const float2 ml = *reinterpret_cast<const float2*>(part(i));
+        L += ml.y * join_weight(ml.x, M);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pp < NP) {
+#pragma unroll 4
+        for (int i = pp; i < jd.pieces; i += NP) {
+            const float* p = part(i);
+            const float mi = p[0];
+            const float4 v = *reinterpret_cast<const float4*>(p + 4 + 4 * q);
+            const float w = join_weight(mi, M);
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        s_acc[pp][q] = acc;
+    }
+    __syncthreads();
+    if (tid < LP) {
+        float4 a = s_acc[0][tid];
+#pragma unroll
+        for (int i = 1; i < NP; ++i) {
+            const float4 v = s_acc[i][tid];
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+        }
+        finish2<T>(P, jd.b, hq, D, 4 * tid, a.x, a.y, M, L, tid == 0);
+        finish2<T>(P, jd.b, hq, D, 4 * tid + 2, a.z, a.w, M, L, false);
+    }
+}
+
+template <typename T, int D, int NB>
+cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
+    using C = TCfg<D>;
+    const int smem = C::SMEM_BASE + 4 * ((p.split ? p.B : 1) + 1);
+    static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
+    const cudaError_t e0 = cudaFuncSetAttribute(paged_token_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                C::SMEM_BASE + 4 * (TK_MAX_B + 1));
+    if (e0 != cudaSuccess) return e0;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_ctas);
+    cfg.blockDim = dim3(C::NW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token_kernel<T, D, NB>, p);
+    if (e != cudaSuccess || !p.split) return e;
+    cfg.gridDim = dim3(p.n_ctas, p.heads_per_group);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, paged_token_join_kernel<T, D>, p);
+}
+
+template <typename T>
+cudaError_t launch_d(PagedAttn& p, int D, cudaStream_t st) {
+    const bool two = p.heads_per_group > 8;
+    switch (D) {
+        case 64: return two ? launch_t<T, 64, 2>(p, st) : launch_t<T, 64, 1>(p, st);
+        case 128: return two ? launch_t<T, 128, 2>(p, st) : launch_t<T, 128, 1>(p, st);
+        case 192: return launch_t<T, 192, 1>(p, st);
+        case 256: return launch_t<T, 256, 1>(p, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+bool paged_token_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
+
+// How a call is cut; fills heads_per_group, n_groups, split and n_ctas, and returns the workspace
+// bytes. Up to 8 q heads (16 at D <= 128) share a work item and one read of the kv head; more are
+// split evenly into several items.
+size_t paged_token_plan(PagedAttn& p, int D, int sms) {
+    const int most = D <= 128 ? 16 : 8;
+    p.n_groups = (p.G + most - 1) / most;
+    p.heads_per_group = (p.G + p.n_groups - 1) / p.n_groups;
+    int64_t bound = ((int64_t)p.max_pages * p.page + PG_SUB - 1) / PG_SUB;   // units of one item
+    if (p.window > 0) {
+        const int64_t w = ((int64_t)p.window + PG_SUB - 1) / PG_SUB + 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;
+        if (w < bound) bound = w;
+    }
+    p.split = bound > TK_DIRECT_UNITS;
+    const int64_t items = (int64_t)p.B * p.H_kv * p.n_groups;
+    p.n_ctas = p.split ? sms : static_cast<int>(items);
+    return p.split ? (size_t)2 * p.n_ctas * slot_floats(D, p.heads_per_group) * sizeof(float) + p.n_ctas * sizeof(JoinDesc) : 0;
+}
+
+cudaError_t launch_paged_token(PagedAttn& p, int D, cudaStream_t st) {
+    return p.dtype == PCK_DT_F16 ? launch_d<__half>(p, D, st) : launch_d<__nv_bfloat16>(p, D, st);
+}
+
+}  // namespace pck
