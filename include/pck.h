@@ -294,8 +294,8 @@ int pck_noalloc_status(void *stream, int *code);
  * and use no workspace of the context, so calls of several streams, and replays of several
  * captured graphs, may overlap when their own buffers do not; on the host, one context is still
  * called by one thread at a time. A value on the device that is out of range (a page number
- * outside [0, n_pages), a rotary position outside the table, a length beyond the table's width)
- * is never followed: the call's results are then invalid and pck_sync reports PCK_ECUDA with code
+ * outside [0, n_pages), a rotary position outside the table, a length beyond the table's width, more
+ * rows than max_rows) is never followed: the call's results are then invalid and pck_sync reports PCK_ECUDA with code
  * 8, 9 or 10. The current device is left as it was. */
 
 /* A cache: K and V hold [n_pages, H_kv, page_size, D] in any order of the first three dimensions
@@ -323,7 +323,7 @@ typedef struct pck_paged_batch {
     const int32_t *kv_len;    /* device [B] */
     const int32_t *table;     /* device [B, max_pages] */
     int max_pages;
-    int max_rows;             /* host bound on one sequence's rows (1 with cu_rows NULL) */
+    int max_rows;             /* host bound on one sequence's rows, at least 1 (T will do) */
 } pck_paged_batch;
 #define PCK_PAGED_MAX_BATCH 2048
 
@@ -372,8 +372,9 @@ int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
  * O_prior (device fp32 [T, H_q, D]) and LSE_prior ([T, H_q]): attention of the same rows over other
  * keys, e.g. what pck_query_batch gave for a resident prefix: O and LSE are then those over both
  * (both NULL otherwise).
- * max_rows == 1: split over the cache's length and joined, D in {64, 128, 192, 256}; more rows are
- * PCK_EUNSUPPORTED. B <= PCK_PAGED_MAX_BATCH.
+ * cu_rows NULL (one row per sequence): split over the cache's length and joined; D in {64, 128, 192,
+ * 256}. Ragged rows: tiles of 256 rows (tokens x heads of a kv head) on the tensor cores, D in {64,
+ * 128}, H_q / H_kv at most 128. B <= PCK_PAGED_MAX_BATCH.
  * workspace: device, 16-byte aligned, pck_paged_workspace bytes (which may be 0), read and written
  * by this call only while it runs: calls that may overlap need one each. */
 int pck_paged_attend(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int H_q,
@@ -396,7 +397,8 @@ int pck_info(pck_ctx *ctx, pck_info_t *out);
  * of an M=1 query with |q| * log2(e) / sqrt(D) >= 65504 (or not finite): the M=1 kernels
  * carry q * log2(e) / sqrt(D) as an fp16 hi + lo pair, so |q| < 65504 * sqrt(D) / log2(e)
  * (e.g. 363,000 at D = 64) is the valid range; 8 a page number, 9 a rotary position, 10 a cache
- * length out of range (the paged-tail calls); 11 a page tile of a one-row paged attention. The error word and the selector's counters
+ * length or row count out of range (the paged-tail calls); 11 a page tile of a one-row paged attention; 12 loads, 13
+ * MMAs, 14 softmax, 15 final O of a ragged paged attention. The error word and the selector's counters
  * are then reset, so the context stays usable. */
 int pck_sync(pck_ctx *ctx, void *stream);
 

@@ -1185,7 +1185,7 @@ int pck_sync(pck_ctx* c, void* stream) {
         cudaDeviceSynchronize();
         if (herr >= ERR_PAGE_ID && herr <= ERR_KV_LEN)
             return fail(c, PCK_ECUDA, "a value on the device is out of range (code %d: %s); results of the affected calls are invalid",
-                        herr, herr == ERR_PAGE_ID ? "page number" : herr == ERR_ROPE_POS ? "rotary position" : "cache length");
+                        herr, herr == ERR_PAGE_ID ? "page number" : herr == ERR_ROPE_POS ? "rotary position" : "cache length or row count");
         return fail(c, PCK_ECUDA, "a device wait gave up (code %d); results of the affected calls are invalid", herr);
     }
     return PCK_OK;

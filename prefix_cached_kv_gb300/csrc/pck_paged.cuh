@@ -18,7 +18,7 @@ namespace pck {
 // Device error codes of these operators (pck_sync reports them).
 constexpr int ERR_PAGE_ID = 8;       // a page number of the table outside [0, n_pages)
 constexpr int ERR_ROPE_POS = 9;      // a position outside the rotary table
-constexpr int ERR_KV_LEN = 10;       // a row's cache position, or a length, beyond the table
+constexpr int ERR_KV_LEN = 10;         // a cache length beyond the table, or more rows than max_rows
 constexpr int ERR_PAGED_TOKEN = 11;  // one-token attention: a page tile never landed
 constexpr int ERR_ROWS_LOAD = 12;    // row attention: producer, MMA warp, softmax, final O
 constexpr int ERR_ROWS_MMA = 13;
@@ -75,7 +75,7 @@ struct PagedAttn {
     int page, max_pages;
     int n_pages;
     int window, sinks;
-    int max_rows;
+    int max_rows;                    // bound on a sequence's rows
     float scale_log2;                // tau * log2(e)
     int dtype;
     float* ws;                       // partials, then the join descriptors
@@ -84,12 +84,21 @@ struct PagedAttn {
     int heads_per_group, n_groups;   // q heads of a kv head that share a work item, and items per kv head
     int split;                       // 1: equal ranges of tiles over the CTAs, joined by a second kernel
     int n_ctas;
+    // row kernel
+    int n_split, row_tiles, box;     // key splits, row tiles of the grid, tokens of a TMA box
+    const void *k_base, *v_base;
+    int64_t kv_stride[6];            // k page, head, token; v page, head, token (elements)
 };
 
 bool paged_token_dim_ok(int D);
 constexpr int paged_token_box_rows() { return PG_SUB; }   // tokens of a TMA tile load
 size_t paged_token_plan(PagedAttn& p, int D, int sms);    // how the call is cut; its workspace in bytes
 cudaError_t launch_paged_token(PagedAttn& p, int D, cudaStream_t st);
+bool paged_rows_dim_ok(int D);
+int paged_rows_box(int page);             // tokens of a TMA box
+int paged_rows_tok_per_tile(int G);
+size_t paged_rows_plan(PagedAttn& p, int D, int sms);
+cudaError_t launch_paged_rows(PagedAttn& p, int D, cudaStream_t st);
 
 // The context behind a handle (pck_api.cu).
 struct CtxView {

@@ -89,8 +89,8 @@ int check_batch(pck_ctx* c, const pck_paged_batch* b, int page_size) {
     if (b->max_pages < 1 || (int64_t)b->max_pages * page_size >= (int64_t(1) << 31))
         return ctx_fail(c, PCK_EINVAL, "max_pages=%d out of range", b->max_pages);
     if (b->max_rows < 1) return ctx_fail(c, PCK_EINVAL, "max_rows=%d", b->max_rows);
-    if (!b->cu_rows && (b->T != b->B || b->max_rows != 1))
-        return ctx_fail(c, PCK_EINVAL, "without cu_rows there is one row per sequence (T=%d, B=%d, max_rows=%d)", b->T, b->B, b->max_rows);
+    if (!b->cu_rows && b->T != b->B)
+        return ctx_fail(c, PCK_EINVAL, "without cu_rows there is one row per sequence (T=%d, B=%d)", b->T, b->B);
     return PCK_OK;
 }
 
@@ -159,9 +159,12 @@ int attend_shape(pck_ctx* c, const pck_paged_cache* k, const pck_paged_batch* b,
     if (rc != PCK_OK) return rc;
     if (H_q < 1 || H_q > 1024 || H_q % k->H_kv) return ctx_fail(c, PCK_EINVAL, "H_q=%d is not a multiple of H_kv=%d (at most 1024)", H_q, k->H_kv);
     if (window < 0 || sinks < 0) return ctx_fail(c, PCK_EINVAL, "window=%d sinks=%d", window, sinks);
-    if (b->max_rows > 1) return ctx_fail(c, PCK_EUNSUPPORTED, "max_rows=%d: one row per sequence", b->max_rows);
-    if (!paged_token_dim_ok(k->D)) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d: 64, 128, 192 or 256", k->D);
-    if (b->cu_rows) return ctx_fail(c, PCK_EUNSUPPORTED, "cu_rows with max_rows 1");
+    if (b->cu_rows) {
+        if (!paged_rows_dim_ok(k->D)) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d with cu_rows: 64 or 128", k->D);
+        if (H_q / k->H_kv > 128) return ctx_fail(c, PCK_EUNSUPPORTED, "%d q heads per kv head: at most 128 with cu_rows", H_q / k->H_kv);
+    } else if (!paged_token_dim_ok(k->D)) {
+        return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d: 64, 128, 192 or 256", k->D);
+    }
     p.B = b->B;
     p.T = b->T;
     p.H_q = H_q;
@@ -172,12 +175,31 @@ int attend_shape(pck_ctx* c, const pck_paged_cache* k, const pck_paged_batch* b,
     p.n_pages = static_cast<int>(k->n_pages);
     p.window = window;
     p.sinks = sinks;
-    p.max_rows = b->max_rows;
+    p.cu_rows = b->cu_rows;
+    p.max_rows = b->max_rows < b->T ? b->max_rows : b->T;
     p.dtype = k->dtype;
     if ((int64_t)b->B * (((int64_t)b->max_pages * k->page_size + PG_SUB - 1) / PG_SUB + 1) >= (int64_t(1) << 31))
         return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld tokens", b->B, (long long)b->max_pages * k->page_size);
-    if ((int64_t)b->B * H_q >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d, H_q=%d", b->B, H_q);
+    if ((int64_t)b->T * H_q >= (int64_t(1) << 31) / 16) return ctx_fail(c, PCK_EUNSUPPORTED, "T=%d, H_q=%d", b->T, H_q);
     return PCK_OK;
+}
+
+// Rows: the tensor-core kernel for ragged rows (cu_rows given), else the one-token kernel.
+size_t attend_plan(PagedAttn& p, int D, int sms) { return p.cu_rows ? paged_rows_plan(p, D, sms) : paged_token_plan(p, D, sms); }
+
+// Q [T, H_q, D] as {64 elements, q head of the group, token, D/64, kv head} with a box of all G heads of `tokens`
+// tokens: row token * G + head of a tile.
+bool encode_q(CUtensorMap* tm, const PagedAttn& p, int D, int tokens) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const int64_t sh = p.H_q > 1 ? p.q_head : D, st = p.T > 1 ? p.q_row : D;
+    const cuuint64_t dims[5] = {64, (cuuint64_t)p.G, (cuuint64_t)p.T, (cuuint64_t)(D / 64), (cuuint64_t)p.H_kv};
+    const cuuint64_t strides[4] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2, 128, (cuuint64_t)(sh * p.G) * 2};
+    const cuuint32_t box[5] = {64, (cuuint32_t)p.G, (cuuint32_t)tokens, 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType dt = p.dtype == PCK_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(tm, dt, 5, const_cast<void*>(p.Q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -260,7 +282,7 @@ int pck_paged_workspace(pck_ctx* c, const pck_paged_cache* cache, const pck_page
     PagedAttn p = {};
     const int rc = attend_shape(c, cache, batch, H_q, window, sinks, p);
     if (rc != PCK_OK) return rc;
-    *bytes = p.B == 0 || p.T == 0 ? 0 : paged_token_plan(p, cache->D, ctx_view(c).sms);
+    *bytes = p.B == 0 || p.T == 0 ? 0 : attend_plan(p, cache->D, ctx_view(c).sms);
     return PCK_OK;
 }
 
@@ -279,7 +301,7 @@ int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     if ((O_prior != nullptr) != (LSE_prior != nullptr)) return ctx_fail(c, PCK_EINVAL, "O_prior and LSE_prior go together");
     const CtxView v = ctx_view(c);
     const int D = cache->D;
-    const size_t need = paged_token_plan(p, D, v.sms);
+    const size_t need = attend_plan(p, D, v.sms);
     if (workspace_bytes < need || (need && !workspace))
         return ctx_fail(c, PCK_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     p.Q = Q;
@@ -289,19 +311,25 @@ int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     p.LSE_prior = LSE_prior;
     p.q_row = q_row;
     p.q_head = q_head;
-    p.cu_rows = batch->cu_rows;
     p.kv_len = batch->kv_len;
     p.table = batch->table;
     p.scale_log2 = PG_LOG2E / sqrtf(static_cast<float>(D));
     p.ws = static_cast<float*>(workspace);
     p.err = v.dev_err;
-    const int rows = paged_token_box_rows(), chunks = D / 64;
+    p.k_base = cache->K;
+    p.v_base = cache->V;
+    const int64_t strides[6] = {cache->k_page, cache->k_head, cache->k_token, cache->v_page, cache->v_head, cache->v_token};
+    for (int i = 0; i < 6; ++i) p.kv_stride[i] = strides[i];
+    const bool ragged = p.cu_rows != nullptr;
+    const int rows = ragged ? p.box : paged_token_box_rows(), chunks = ragged ? 1 : D / 64;
     DeviceScope dev(v.device);
     if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
     if (!encode_pages(&p.tm_k, p.dtype, cache->K, p.page, D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows, chunks) ||
         !encode_pages(&p.tm_v, p.dtype, cache->V, p.page, D, p.H_kv, cache->n_pages, cache->v_token, cache->v_head, cache->v_page, rows, chunks))
         return ctx_fail(c, PCK_ECUDA, "the driver refused the cache's tensor map");
-    const cudaError_t e = launch_paged_token(p, D, static_cast<cudaStream_t>(stream));
+    if (ragged && !encode_q(&p.tm_q, p, D, paged_rows_tok_per_tile(p.G))) return ctx_fail(c, PCK_ECUDA, "the driver refused Q's tensor map");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = ragged ? launch_paged_rows(p, D, st) : launch_paged_token(p, D, st);
     if (e != cudaSuccess) return ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
     ctx_count_query(c);
     return PCK_OK;

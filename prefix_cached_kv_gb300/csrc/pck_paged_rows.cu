@@ -1,0 +1,789 @@
+// pck_paged_rows.cu -- attention of ragged rows (prompts, prompt chunks) over a paged KV cache, causal,
+// with an optional sliding window and first tokens that stay visible, on the 5th-generation tensor cores.
+//
+// Row i of the n rows of a sequence with len cached tokens stands at p = len - n + i and sees the keys
+// j <= p, with a window W > 0 only those with j > p - W or j < sinks:
+//   S = tau q K^T,  O = sum_j 2^(s_j' - m) v_j / l,  LSE = (m + log2 l) ln 2       (s' = s log2 e)
+//
+// 4 D flop per visible (row, head, key) against K and V read through L2 once per CTA: the tensor
+// cores bound it, so the kernel's business is to feed them without a pause.
+//  * A CTA owns two tiles of 128 query rows of one kv head (row = token * G + q head, so grouped heads
+//    share every K and V tile) and walks its keys in blocks of 128. While one tile's softmax runs, the
+//    other tile's MMAs do. TMEM: two S (128 columns each; P of a block overwrites its S as packed 16-bit
+//    values) and two O (D columns each).
+//  * Warp 9 loads Q and a ring of K and V blocks by TMA with 128-byte swizzle, one box per page run (a box
+//    is the largest power-of-two run of tokens that divides both the page and the block). K is the
+//    K-major B operand of S = Q K^T as it lies; V, stored token by token, is the MN-major B operand of
+//    O += P V, so nothing is transposed.
+//  * Warp 8 issues tcgen05.mma: S0(j+1) right behind O0 += P0(j) V(j), then the same for tile 1.
+//  * Warps 0-3 and 4-7 are the tiles' softmax, a thread per row: 128 scores in registers, the block's
+//    maximum (the running maximum moves only when passed by 8 (log2), so p <= 2^8 and O is rarely
+//    rescaled), p = 2^(s - m) rounded once to the cache's type for the second MMA (its rounding is like
+//    that of the 16-bit output), their fp32 sum from the unrounded p.
+//  * Keys: with a window, the sinks' boxes and then the window's are laid end to end, so no block is spent
+//    on hidden keys and the pages between are never touched. Only blocks that some row does not see
+//    whole are masked, by a 16-bit mask per row and 16 keys.
+//  * V rows that no row of the CTA sees (behind the last token, in front of the window) are zeroed in
+//    shared memory, since 0 * NaN would keep what they hold. Where a value that only some rows see is
+//    not finite, the rows it spoiled are recomputed one by one from the visible keys alone.
+//  * Few rows over a long cache: the keys are split over n_split CTAs and a second kernel joins them.
+#include <algorithm>
+
+#include "pck_paged.cuh"
+
+namespace pck {
+namespace {
+
+constexpr int RW_M = 128;              // rows of a tile
+constexpr int RW_BLOCK = 128;          // keys of a block
+constexpr int RW_THREADS = 384;        // two softmax warpgroups; MMA warp, load warp and two idle ones
+// registers a thread: 168 at launch (384 x 168 <= 65,536); 232 x 256 + 40 x 128 = 384 x 168 after the split
+constexpr int RW_REGS_SOFTMAX = 232, RW_REGS_OTHER = 40;
+constexpr int RW_MMA_WARP = 8, RW_LOAD_WARP = 9;
+
+template <int D>
+struct RCfg {
+    static constexpr int CH = D / 64;                          // 128-byte chunks of a row
+    static constexpr int CHUNK = 128 * 128;                    // bytes of a chunk of 128 rows
+    static constexpr int TILE = CH * CHUNK;                    // Q tile, K block or V block
+    static constexpr int NST = D == 128 ? 5 : 8;               // ring stages (a K or a V block each)
+    static constexpr int OFF_RING = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_RING + NST * TILE;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;          // + alignment slack
+    static constexpr int S_COL = 0, O_COL = 256;               // TMEM: S of tile t at 128 t, O at 256 + D t
+    static constexpr int TMEM_COLS = 512;
+};
+
+// ---------------------------------------------------------------- tcgen05 and TMA wrappers
+
+// 128-byte swizzled operand descriptors: K-major (rows of 128 bytes, 8-row groups 1024 bytes apart) and
+// MN-major (runs of 64 elements per token, 8-token groups 1024 bytes apart, runs `lbo` bytes apart).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+// fp32 accumulator; A and B both fp16 (fmt 0) or bf16 (fmt 1); b_mn: B is MN-major
+__device__ __forceinline__ uint32_t idesc_16(int fmt, int N, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(RW_M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p, e; .reg .b32 rx; elect.sync rx|e, 0xffffffff; setp.ne.u32 p, %4, 0; "
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p, e; .reg .b32 rx; elect.sync rx|e, 0xffffffff; setp.ne.u32 p, %4, 0; "
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{ .reg .pred e; .reg .b32 rx; elect.sync rx|e, 0xffffffff; "
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }"
+        ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void ld32(uint32_t taddr, float* f) {   // 32 columns of the thread's lane; not waited for
+    uint32_t* r = reinterpret_cast<uint32_t*>(f);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap* tm, int x, int c1, int c2, int c3, int c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        ::"r"(dst), "l"(tm), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack16(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+template <> __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T> __device__ __forceinline__ float2 unpack16(uint32_t u);
+template <> __device__ __forceinline__ float2 unpack16<__half>(uint32_t u) { return __half22float2(u32_as_h2(u)); }
+template <> __device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// ---------------------------------------------------------------- which rows, which keys
+
+struct RowTile {
+    int b;          // sequence, or -1: no rows for this tile index
+    int tok0;       // first row of the sequence in this CTA
+    int n;          // rows of the sequence
+    int row0;       // first row of the sequence among the call's T
+};
+
+// The sequence and rows of CTA tile `idx` (tiles of tt rows, the sequences' tiles end to end). One warp.
+__device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt, int lane) {
+    int before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32) {
+        const int b = b0 + lane;
+        int r0 = 0, n = 0;
+        if (b < P.B) {
+            r0 = P.cu_rows[b];
+            n = max(0, P.cu_rows[b + 1] - r0);
+        }
+        const int nt = (n + tt - 1) / tt;
+        int inc = nt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, idx < before + inc);
+        if (hit) {
+            const int w = __ffs(hit) - 1;
+            RowTile t;
+            t.b = b0 + w;
+            t.tok0 = (idx - before - __shfl_sync(0xffffffffu, inc - nt, w)) * tt;
+            t.n = __shfl_sync(0xffffffffu, n, w);
+            t.row0 = __shfl_sync(0xffffffffu, r0, w);
+            return t;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return RowTile{-1, 0, 0, 0};
+}
+
+// Whether the sequences' tiles are more than the grid was made for: some sequence has more rows than max_rows.
+__device__ __forceinline__ bool too_many_rows(const PagedAttn& P, int tt, int lane) {
+    int64_t total = 0;
+    for (int b = lane; b < P.B; b += 32) total += (max(0, P.cu_rows[b + 1] - P.cu_rows[b]) + tt - 1) / tt;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total > P.row_tiles;
+}
+
+// The keys of a CTA: boxes of the sinks, [0, se), then [ws, end), laid end to end: total keys, a multiple
+// of the box. p0 and p1: first and last position of its rows.
+struct Keys {
+    int se, ws, total;
+    __device__ __forceinline__ int key(int v) const { return v < se ? v : v - se + ws; }
+};
+__device__ __forceinline__ Keys keys_of(int p0, int p1, int window, int sinks, int box) {
+    Keys k;
+    k.se = 0;
+    k.ws = 0;
+    const int end = (p1 + box) / box * box;      // p1 + 1 rounded up; 0 for p1 < 0
+    if (window > 0) {
+        const int first = max(0, p0 - window + 1);
+        k.ws = first / box * box;
+        const int s = min(sinks, p1 + 1);
+        k.se = min((s + box - 1) / box * box, k.ws);
+        if (k.se < 0) k.se = 0;
+    }
+    k.total = p1 < 0 ? 0 : k.se + end - k.ws;
+    return k;
+}
+
+__device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u; }
+// which of keys key .. key + 15 position p sees
+__device__ __forceinline__ uint32_t seen16(int key, int p, int window, int sinks) {
+    uint32_t m = low_mask(p + 1 - key);
+    if (window > 0) m &= ~low_mask(p - window + 1 - key) | low_mask(sinks - key);
+    return m;
+}
+
+__device__ __forceinline__ int page_of(const PagedAttn& P, int b, int key) {
+    const int pg = P.table[(int64_t)b * P.max_pages + key / P.page];
+    if (pg < 0 || pg >= P.n_pages) {
+        set_err(P.err, ERR_PAGE_ID);     // and page 0 is read instead
+        return 0;
+    }
+    return pg;
+}
+
+// One row over virtual keys [v0, v1) on its own, from global memory: m, l and its O (unnormalised, staged in
+// `o`, D floats, by the calling thread). Only for rows whose O came out not finite while their scores were:
+// V of a key that other rows see is not finite. Slow, and right for any values in keys that the row does not see.
+template <typename T, int D>
+__device__ __noinline__ void row_alone(const PagedAttn& P, int b, int g, int64_t qoff, int p, Keys K, int v0, int v1, float m,
+                                       float* o, const char* kbase, const char* vbase, const int64_t* st) {
+    for (int d = 0; d < D; ++d) o[d] = 0.f;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(P.Q) + qoff);
+    for (int v = v0; v < v1; ++v) {
+        const int key = K.key(v);
+        if (!(seen16(key & ~15, p, P.window, P.sinks) >> (key & 15) & 1)) continue;
+        const int64_t pg = page_of(P, b, key);
+        const int slot = key % P.page;
+        const uint4* k = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(kbase) + pg * st[0] + g * st[1] + slot * st[2]);
+        const uint4* vv = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(vbase) + pg * st[3] + g * st[4] + slot * st[5]);
+        float s = 0.f;
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 a = q[c], e = k[c];
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ew[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack16<T>(aw[i]), y = unpack16<T>(ew[i]);
+                s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+            }
+        }
+        const float w = ex2_approx(fmaf(s, P.scale_log2, -m));
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 e = vv[c];
+            const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 y = unpack16<T>(ew[i]);
+                o[8 * c + 2 * i] = fmaf(w, y.x, o[8 * c + 2 * i]);
+                o[8 * c + 2 * i + 1] = fmaf(w, y.y, o[8 * c + 2 * i + 1]);
+            }
+        }
+    }
+}
+
+// Weights of a row's own attention and of the prior in the result, and the LSE of both.
+struct RowEnd {
+    float wo, wp, lse;
+    bool prior;
+};
+__device__ __forceinline__ RowEnd row_end(const PagedAttn& P, int64_t row, float m, float l) {
+    RowEnd r;
+    const bool none = l == 0.f;
+    r.wo = none ? 0.f : 1.0f / l;
+    r.wp = 0.f;
+    r.lse = none ? -INFINITY : (m + log2f(l)) * PG_LN2;
+    r.prior = false;
+    if (P.O_prior) {
+        const float lp = P.LSE_prior[row];
+        if (lp != -INFINITY) {
+            const float mx = fmaxf(r.lse, lp);
+            const float wn = expf(r.lse - mx), wp = expf(lp - mx), sum = wn + wp;
+            r.wo *= wn / sum;
+            r.wp = wp / sum;
+            r.lse = mx + logf(sum);
+            r.prior = true;
+        }
+    }
+    return r;
+}
+
+__host__ __device__ constexpr int rows_partial_floats(int D) { return D + 4; }   // m, l, -, -, O
+
+template <typename T, int D>
+__global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_constant__ PagedAttn P) {
+    using C = RCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t s_base = smem_u32(smem);
+    // barriers: Q of each tile, ring full / empty, S ready, P ready (128 arrivals), O += P V done
+    constexpr int B_Q = 0, B_F = 16, B_E = B_F + 8 * C::NST, B_S = B_E + 8 * C::NST, B_P = B_S + 16, B_O = B_P + 16,
+                  B_DR = B_O + 16, N_BAR = B_DR / 8 + 1;
+    const uint32_t bar = s_base + C::OFF_BAR;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * N_BAR);
+    RowTile* s_tile = reinterpret_cast<RowTile*>(smem + C::OFF_BAR + 8 * N_BAR + 16);
+    static_assert(8 * N_BAR + 16 + sizeof(RowTile) <= 512, "barrier area");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = P.G, tpt = RW_M / G, tt = 2 * tpt;
+    // later tiles first (they see the most keys); kv heads next to one another, then key splits
+    const int per_tile = P.H_kv * P.n_split;
+    const int tile_idx = P.row_tiles - 1 - blockIdx.x / per_tile;
+    const int sub = blockIdx.x % per_tile;
+    const int g = sub % P.H_kv, split = sub / P.H_kv;
+
+    if (tid == 0) {
+        for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i == B_P || 8 * i == B_P + 8) ? 128 : 1);
+        fence_mbar_init();
+    }
+    if (warp == RW_LOAD_WARP && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_v) : "memory");
+    }
+    if (warp == RW_MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_slot)), "r"(C::TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    pdl_release();
+    if (warp == RW_LOAD_WARP) {
+        const RowTile t = find_tile(P, tile_idx, tt, lane);
+        if (lane == 0) *s_tile = t;
+        if (blockIdx.x == 0 && too_many_rows(P, tt, lane) && lane == 0) set_err(P.err, ERR_KV_LEN);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const RowTile rt = *s_tile;
+
+    if (rt.b >= 0) {
+        const int b = rt.b;
+        int len = P.kv_len[b];
+        if (len > (int64_t)P.max_pages * P.page) {
+            if (tid == 0) set_err(P.err, ERR_KV_LEN);
+            len = P.max_pages * P.page;
+        }
+        const int rows_here = min(rt.n - rt.tok0, tt);          // rows (tokens) of this CTA
+        const int ntile = rows_here > tpt ? 2 : 1;
+        const int p0 = len - rt.n + rt.tok0, p1 = p0 + rows_here - 1;
+        const int box = P.box;
+        const Keys K = keys_of(p0, p1, P.window, P.sinks, box);
+        const int nblk_all = (K.total + RW_BLOCK - 1) / RW_BLOCK;
+        const int j0 = static_cast<int>((int64_t)nblk_all * split / P.n_split);
+        const int j1 = static_cast<int>((int64_t)nblk_all * (split + 1) / P.n_split);
+        const int nb = j1 - j0;
+        auto keys_in = [&](int j) { return min(RW_BLOCK, K.total - (j0 + j) * RW_BLOCK); };   // of block j of this CTA
+        bool failed = false;
+
+        if (warp >= 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_REGS_OTHER));
+            if (warp == RW_LOAD_WARP) {
+                // ------------------------------------------------------------ loads
+                if (nb > 0) {
+                    if (lane < ntile) {   // Q rows token * G + head; rows behind the sequence's hold others' or nothing
+                        mbar_arrive_expect_tx(bar + B_Q + 8 * lane, C::CH * G * tpt * 128);
+                        for (int c = 0; c < C::CH; ++c)
+                            tma5(s_base + lane * C::TILE + c * C::CHUNK, &P.tm_q, 0, 0, rt.row0 + rt.tok0 + lane * tpt, c, g, bar + B_Q + 8 * lane);
+                    }
+                    const int bpb = RW_BLOCK / box;     // boxes of a whole block
+                    int pg = 0, tok = 0;
+                    auto locate = [&](int j) {          // lane i: page and token of box i of block j
+                        const int v = (j0 + j) * RW_BLOCK + lane * box;
+                        if (lane < bpb && v < K.total) {
+                            const int key = K.key(v);
+                            pg = page_of(P, b, key);
+                            tok = key % P.page;
+                        }
+                    };
+                    locate(0);
+                    int i = 0;
+                    for (; i < 2 * nb; ++i) {   // K(0), V(0), K(1), V(1), ...
+                        const int j = i >> 1, st = i % C::NST, nk = keys_in(j);
+                        if (i >= C::NST && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_E + 8 * st, (i / C::NST - 1) & 1))) {
+                            failed = true;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(bar + B_F + 8 * st, nk * D * 2);
+                        __syncwarp();
+                        if (lane * box < nk) {
+                            const uint32_t dst = s_base + C::OFF_RING + st * C::TILE + lane * box * 128;
+                            for (int c = 0; c < C::CH; ++c)
+                                tma5(dst + c * C::CHUNK, (i & 1) ? &P.tm_v : &P.tm_k, 0, tok, c, g, pg, bar + B_F + 8 * st);
+                        }
+                        if ((i & 1) && j + 1 < nb) locate(j + 1);
+                    }
+                    if (failed && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
+                    // the copies in flight land before the CTA can end, whatever the other warps do
+                    for (int q = max(0, i - C::NST); q < i; ++q)
+                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_F + 8 * (q % C::NST), (q / C::NST) & 1))) break;
+                }
+            } else if (warp == RW_MMA_WARP) {
+                // ------------------------------------------------------------ MMAs
+                const int fmt = P.dtype == PCK_DT_BF16 ? 1 : 0;
+                const uint64_t q_desc = desc_sw128(s_base, 16);
+                const uint64_t k_desc = desc_sw128(s_base + C::OFF_RING, 16);
+                const uint64_t v_desc = desc_sw128(s_base + C::OFF_RING, C::CHUNK);
+                const uint32_t id_pv = idesc_16(fmt, D, 1);
+                auto wait = [&](int off, int phase) {
+                    if (!failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + off, phase & 1))) failed = true;
+                    return !failed;
+                };
+                auto issue_S = [&](int t, int j) {   // S_t = Q_t K(j)^T
+                    const int i = 2 * j, st = i % C::NST;
+                    const uint32_t id = idesc_16(fmt, keys_in(j), 0);
+                    const uint64_t qd = q_desc + static_cast<uint64_t>((t * C::TILE) >> 4), kd = k_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
+    #pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint64_t off = (s >> 2) * (C::CHUNK >> 4) + (s & 3) * 2;
+                        mma_ss(tmem + C::S_COL + 128 * t, qd + off, kd + off, id, s > 0);
+                    }
+                    commit(bar + B_S + 8 * t);
+                    if (t == ntile - 1) commit(bar + B_E + 8 * st);
+                };
+                auto issue_PV = [&](int t, int j) {  // O_t += P_t V(j)
+                    const int i = 2 * j + 1, st = i % C::NST, nk = keys_in(j);
+                    const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
+    #pragma unroll
+                    for (int u = 0; u < RW_BLOCK / 16; ++u)
+                        if (16 * u < nk)
+                            mma_ts(tmem + C::O_COL + D * t, tmem + C::S_COL + 128 * t + 8 * u, vd + static_cast<uint64_t>(u * (2048 >> 4)), id_pv,
+                                   j > 0 || u > 0);
+                    commit(bar + B_O + 8 * t);
+                    if (t == ntile - 1) commit(bar + B_E + 8 * st);
+                };
+                if (nb > 0 && wait(B_F, 0)) {
+                    for (int t = 0; t < ntile; ++t)
+                        if (wait(B_Q + 8 * t, 0)) issue_S(t, 0);
+                    for (int j = 0; j < nb && !failed; ++j) {
+                        const int iv = 2 * j + 1, ik = 2 * j + 2;
+                        for (int t = 0; t < ntile; ++t) {
+                            if (!wait(B_P + 8 * t, j)) break;
+                            if (t == 0 && !wait(B_F + 8 * (iv % C::NST), iv / C::NST)) break;
+                            fence_after();
+                            issue_PV(t, j);
+                            if (j + 1 < nb) {
+                                if (t == 0 && !wait(B_F + 8 * (ik % C::NST), ik / C::NST)) break;
+                                issue_S(t, j + 1);
+                            }
+                        }
+                    }
+                }
+                if (failed && lane == 0) set_err(P.err, ERR_ROWS_MMA);
+                commit(bar + B_DR);      // no MMA writes TMEM any more when the CTA gives it back
+                __all_sync(0xffffffffu, mbar_wait_bounded(bar + B_DR, 0));
+            }
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_REGS_SOFTMAX));
+            if (warp < 4 * ntile) {
+                // ------------------------------------------------------------ softmax: row r of tile t
+                const int t = warp >> 2, r = tid & 127;
+                const int rtok = t * tpt + r / G;                     // token of the CTA
+                const bool row_ok = r < tpt * G && rtok < rows_here && rt.row0 + rt.tok0 + rtok < P.T && rt.row0 >= 0;
+                const int p = row_ok ? p0 + rtok : -1;
+                const int hq = g * G + r % G;
+                // positions of the tile's first and last rows
+                const int pa = p0 + t * tpt, pz = min(p1, pa + tpt - 1);
+                const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+                const uint32_t s_tm = tmem + C::S_COL + 128 * t + lane_base, o_tm = tmem + C::O_COL + D * t + lane_base;
+                const float sc = P.scale_log2;
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < nb; ++j) {
+                    const int v0 = (j0 + j) * RW_BLOCK, nk = keys_in(j);
+                    const int ka = K.key(v0), kz = K.key(v0 + nk - 1);
+                    if (t == 0 && (kz > p1 || kz - ka != nk - 1 || (P.window > 0 && ka <= p0 - P.window))) {
+                        // V rows that no row of the CTA sees are cleared (thread r: row r of the block)
+                        const int st = (2 * j + 1) % C::NST;
+                        if (!mbar_wait_bounded(bar + B_F + 8 * st, ((2 * j + 1) / C::NST) & 1)) failed = true;
+                        const int key = K.key(v0 + r);
+                        if (!failed && r < nk && (key > p1 || (P.window > 0 && key <= p0 - P.window && key >= P.sinks))) {
+                            uint4* row = reinterpret_cast<uint4*>(smem + C::OFF_RING + st * C::TILE + r * 128);
+                            for (int c = 0; c < C::CH; ++c)
+    #pragma unroll
+                                for (int i = 0; i < 8; ++i) row[c * (C::CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (!__all_sync(0xffffffffu, !failed && mbar_wait_bounded(bar + B_S + 8 * t, j & 1))) {
+                        failed = true;
+                        break;
+                    }
+                    fence_after();
+                    float s[RW_BLOCK];
+    #pragma unroll
+                    for (int c = 0; c < 4; ++c) ld32(s_tm + 32 * c, s + 32 * c);
+                    wait_ld();
+                    // every row of the tile sees the whole block, or masks: 16 keys at a time
+                    const bool full = nk == RW_BLOCK && kz - ka == RW_BLOCK - 1 && kz <= pa &&
+                                      (P.window <= 0 || ka > pz - P.window || kz < P.sinks);
+                    if (!full) {
+    #pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t see = 16 * c < nk ? seen16(K.key(v0 + 16 * c), p, P.window, P.sinks) : 0u;
+    #pragma unroll
+                            for (int i = 0; i < 16; ++i) s[16 * c + i] = see >> i & 1 ? s[16 * c + i] : -INFINITY;
+                        }
+                    }
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+    #pragma unroll
+                    for (int i = 4; i < RW_BLOCK; i += 8)
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], i + 4 + q < RW_BLOCK ? fmaxf(s[i + q], s[i + 4 + q]) : s[i + q]);
+                    const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    const bool need = row_ok && bm > m + 8.f;
+                    if (__any_sync(0xffffffffu, need)) {
+                        const float mn = need ? bm : m;
+                        const float al = need ? ex2_approx(m - mn) : 1.0f;     // 0 from m = -inf
+                        if (j > 0) {   // O is quiet once P V of the previous block is done
+                            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_O + 8 * t, (j - 1) & 1))) {
+                                failed = true;
+                                break;
+                            }
+                            fence_after();
+    #pragma unroll
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                ld32(o_tm + c, o);
+                                wait_ld();
+    #pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= al;
+                                st32(o_tm + c, reinterpret_cast<const uint32_t*>(o));
+                            }
+                        }
+                        l *= al;
+                        m = mn;
+                    }
+                    const float ms = m > -INFINITY ? m : 0.f;
+                    const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-ms, -ms);
+                    uint64_t a0 = 0, a1 = 0;
+                    uint32_t pk[RW_BLOCK / 2];
+    #pragma unroll
+                    for (int i = 0; i < RW_BLOCK / 2; ++i) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), sc2, nm2), x0, x1);
+                        const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+                        if (i & 1) a1 = f2_add(a1, f2_pack(e0, e1));
+                        else a0 = f2_add(a0, f2_pack(e0, e1));
+                        pk[i] = pack16<T>(e0, e1);
+                    }
+                    st32(s_tm, pk);
+                    st32(s_tm + 32, pk + 32);
+                    float x0, x1, y0, y1;
+                    f2_unpack(a0, x0, x1);
+                    f2_unpack(a1, y0, y1);
+                    l += (x0 + x1) + (y0 + y1);
+                    wait_st();
+                    fence_before();
+                    mbar_arrive(bar + B_P + 8 * t);
+                }
+                if (nb > 0 && !failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_O + 8 * t, (nb - 1) & 1))) {
+                    set_err(P.err, ERR_ROWS_O);
+                    failed = true;
+                } else if (failed) {
+                    set_err(P.err, ERR_ROWS_SOFTMAX);
+                }
+                if (!failed) {
+                    fence_after();
+                    const int64_t trow = rt.row0 + rt.tok0 + rtok;
+                    const int64_t row = trow * P.H_q + hq;
+                    const bool direct = P.n_split == 1;
+                    RowEnd e = {1.f, 0.f, 0.f, false};
+                    if (direct && row_ok) e = row_end(P, row, m, l);
+                    float* part = P.ws + ((size_t)((size_t)tile_idx * per_tile + sub) * (2 * RW_M) + t * RW_M + r) * rows_partial_floats(D);
+                    bool spoiled = false;
+    #pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        if (nb > 0) {
+                            ld32(o_tm + c, o);
+                            wait_ld();
+                        } else {
+    #pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        }
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) spoiled |= !(fabsf(o[i]) < INFINITY);
+                        if (!row_ok) continue;
+                        if (direct) {
+                            if (l == 0.f) {
+    #pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                            }
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.O) + row * D + c);
+                            const float4* pr = reinterpret_cast<const float4*>(P.O_prior + row * D + c);
+    #pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                float x[8];
+    #pragma unroll
+                                for (int q = 0; q < 8; ++q) x[q] = o[i + q] * e.wo;
+                                if (e.prior) {
+                                    const float4 a = pr[i / 4], c4 = pr[i / 4 + 1];
+                                    x[0] = fmaf(a.x, e.wp, x[0]); x[1] = fmaf(a.y, e.wp, x[1]);
+                                    x[2] = fmaf(a.z, e.wp, x[2]); x[3] = fmaf(a.w, e.wp, x[3]);
+                                    x[4] = fmaf(c4.x, e.wp, x[4]); x[5] = fmaf(c4.y, e.wp, x[5]);
+                                    x[6] = fmaf(c4.z, e.wp, x[6]); x[7] = fmaf(c4.w, e.wp, x[7]);
+                                }
+                                dst[i / 8] = make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]), pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
+                            }
+                        } else {
+    #pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *reinterpret_cast<float4*>(part + 4 + c + i) = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                                                      : make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                    }
+                    if (row_ok) {
+                        if (direct) {
+                            if (P.LSE) P.LSE[row] = e.lse;
+                        } else {
+                            part[0] = m;
+                            part[1] = l;
+                        }
+                        if (spoiled && l > 0.f) {
+                            float o[D];
+                            row_alone<T, D>(P, b, g, trow * P.q_row + (int64_t)hq * P.q_head, p, K, j0 * RW_BLOCK,
+                                            min(K.total, j1 * RW_BLOCK), m, o, static_cast<const char*>(P.k_base),
+                                            static_cast<const char*>(P.v_base), P.kv_stride);
+                            for (int d = 0; d < D; d += 2) {
+                                if (direct) {
+                                    float x0 = o[d] * e.wo, x1 = o[d + 1] * e.wo;
+                                    if (e.prior) {
+                                        x0 = fmaf(P.O_prior[row * D + d], e.wp, x0);
+                                        x1 = fmaf(P.O_prior[row * D + d + 1], e.wp, x1);
+                                    }
+                                    *reinterpret_cast<uint32_t*>(static_cast<T*>(P.O) + row * D + d) = pack16<T>(x0, x1);
+                                } else {
+                                    part[4 + d] = o[d];
+                                    part[5 + d] = o[d + 1];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == RW_MMA_WARP)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+}
+
+// Joins the n_split partials of each row: a warp per row, lanes over D (a float4 each).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_rows_join_kernel(const __grid_constant__ PagedAttn P) {
+    constexpr int LP = D / 4;
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31;
+    const int tpt = RW_M / P.G, tt = 2 * tpt;
+    const int tile_idx = blockIdx.x / P.H_kv, g = blockIdx.x % P.H_kv;
+    const RowTile rt = find_tile(P, tile_idx, tt, lane);
+    if (rt.b < 0) return;
+    const int rows_here = min(rt.n - rt.tok0, tt);
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 2 * RW_M; r += gridDim.y * 8) {
+        const int t = r / RW_M, rr = r % RW_M;
+        const int rtok = t * tpt + rr / P.G;
+        if (rr >= tpt * P.G || rtok >= rows_here) continue;
+        const int64_t trow = rt.row0 + rt.tok0 + rtok;
+        if (trow < 0 || trow >= P.T) continue;
+        const int64_t row = trow * P.H_q + g * P.G + rr % P.G;
+        auto part = [&](int s) {
+            return P.ws + ((size_t)((size_t)tile_idx * P.H_kv * P.n_split + s * P.H_kv + g) * (2 * RW_M) + r) * rows_partial_floats(D);
+        };
+        float M = -INFINITY;
+        for (int s = lane; s < P.n_split; s += 32) M = fmaxf(M, part(s)[0]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < P.n_split; ++s) {
+            const float* p = part(s);
+            const float2 ml = *reinterpret_cast<const float2*>(p);
+            const float w = ml.x > -INFINITY ? ex2_approx(ml.x - M) : 1.f;   // (a part without keys holds zeros)
+            L = fmaf(w, ml.y, L);
+            if (lane < LP) {
+                const float4 v = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
+                acc.x = fmaf(w, v.x, acc.x);
+                acc.y = fmaf(w, v.y, acc.y);
+                acc.z = fmaf(w, v.z, acc.z);
+                acc.w = fmaf(w, v.w, acc.w);
+            }
+        }
+        const RowEnd e = row_end(P, row, M, L);
+        if (lane < LP) {
+            float4 x = make_float4(acc.x * e.wo, acc.y * e.wo, acc.z * e.wo, acc.w * e.wo);
+            if (e.prior) {
+                const float4 a = *reinterpret_cast<const float4*>(P.O_prior + row * D + 4 * lane);
+                x.x = fmaf(a.x, e.wp, x.x); x.y = fmaf(a.y, e.wp, x.y);
+                x.z = fmaf(a.z, e.wp, x.z); x.w = fmaf(a.w, e.wp, x.w);
+            }
+            *reinterpret_cast<uint2*>(static_cast<T*>(P.O) + row * D + 4 * lane) = make_uint2(pack16<T>(x.x, x.y), pack16<T>(x.z, x.w));
+        }
+        if (lane == 0 && P.LSE) P.LSE[row] = e.lse;
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
+    using C = RCfg<D>;
+    static_assert(C::SMEM <= 232448, "one CTA's shared memory");
+    cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.row_tiles * p.H_kv * p.n_split);
+    cfg.blockDim = dim3(RW_THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, D>, p);
+    if (e != cudaSuccess || p.n_split == 1) return e;
+    cfg.gridDim = dim3(p.row_tiles * p.H_kv, 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, paged_rows_join_kernel<T, D>, p);
+}
+
+}  // namespace
+
+bool paged_rows_dim_ok(int D) { return D == 64 || D == 128; }
+int paged_rows_box(int page) {
+    int box = 16;
+    while (box < RW_BLOCK && page % (2 * box) == 0) box *= 2;
+    return box;
+}
+int paged_rows_tok_per_tile(int G) { return RW_M / G; }
+
+size_t paged_rows_plan(PagedAttn& p, int D, int sms) {
+    const int tt = 2 * (RW_M / p.G);
+    // at most, whatever the sequences' shares
+    p.row_tiles = static_cast<int>(std::min<int64_t>(p.T / tt + p.B, (int64_t)p.B * ((p.max_rows + tt - 1) / tt)));
+    p.box = paged_rows_box(p.page);
+    // Keys are split when the row tiles leave SMs idle: as many splits as fill them once, each of at least
+    // 4 blocks of the longest cache the table can hold.
+    const int64_t ctas = std::min<int64_t>((p.T + tt - 1) / tt, p.row_tiles) * p.H_kv;
+    int64_t bound = (int64_t)p.max_pages * p.page;
+    if (p.window > 0) {
+        const int64_t w = (int64_t)p.window + tt + p.sinks + 2 * p.box;
+        if (w < bound) bound = w;
+    }
+    int64_t ns = ctas >= sms ? 1 : sms / ctas;
+    const int64_t most = bound / (4 * RW_BLOCK);
+    if (ns > most) ns = most;
+    p.n_split = ns < 1 ? 1 : static_cast<int>(ns);
+    return p.n_split == 1 ? 0 : (size_t)p.row_tiles * p.H_kv * p.n_split * 2 * RW_M * rows_partial_floats(D) * sizeof(float);
+}
+
+cudaError_t launch_paged_rows(PagedAttn& p, int D, cudaStream_t st) {
+    if (p.dtype == PCK_DT_F16) return D == 64 ? launch_t<__half, 64>(p, st) : launch_t<__half, 128>(p, st);
+    return D == 64 ? launch_t<__nv_bfloat16, 64>(p, st) : launch_t<__nv_bfloat16, 128>(p, st);
+}
+
+}  // namespace pck

@@ -1,0 +1,213 @@
+"""Attention of ragged rows over a paged cache (causal, windows with sinks, few rows over long caches,
+merged with a prior) on the GPU against the 64-bit form."""
+import math
+
+import pytest
+import torch
+
+from prefix_cached_kv_gb300 import binding
+from tests import paged_ref as ref
+from tests.gpu_util import need_gpu
+from tests.test_gpu_paged import BF16, F16, _rand, ctx, i32   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _cu(news):
+    return torch.tensor([0] + torch.tensor(news).cumsum(0).tolist(), dtype=i32, device="cuda")
+
+
+def _case(ctx, lens, news, H_q, H_kv, D, page, dtype, W=0, sinks=0, prior=False, nhd=False, seed=1, pad=0, scale=1.0, width=None,
+          max_rows=None):
+    need_gpu()
+    pg = ref.Pages(seed, lens, H_kv, D, page, dtype, nhd=nhd, width=width)
+    T = sum(news)
+    big = _rand(seed + 1, T + pad, H_q + 3, D, dtype=dtype, scale=scale)
+    Q = big[:, 2:H_q + 2]
+    pr = None
+    if prior:
+        pr = _rand(seed + 2, T + pad, H_q, D), _rand(seed + 3, T + pad, H_q) + 3
+        pr[1][0, 0] = -math.inf
+        pr[0][0, 0] = math.nan
+    c = binding.PagedCache(pg.k, pg.v)
+    O = torch.full((T + pad, H_q, D), 5.0, dtype=dtype, device="cuda")
+    L = torch.full((T + pad, H_q), 6.0, device="cuda")
+    kw = dict(cu_rows=_cu(news), window=W, sinks=sinks, prior=pr, max_rows=max_rows)
+    ctx.paged_attend(c, pg.table, pg.lens, Q, O=O, LSE=L, **kw)
+    want = ref.attend(pg.k, pg.v, pg.table, lens, news, Q[:T], W, sinks, None if pr is None else (pr[0][:T], pr[1][:T]))
+    ref.check_attend(O[:T], L[:T], want, dtype, ref.P_ONCE[dtype], f"lens {lens[:4]} news {news[:4]} D {D} W {W}")
+    assert (O[T:] == 5).all() and (L[T:] == 6).all()       # rows behind the last sequence, left as they were
+    O2, L2 = ctx.paged_attend(c, pg.table, pg.lens, Q, **kw)
+    assert torch.equal(O[:T], O2[:T]) and torch.equal(L[:T], L2[:T])
+    ctx.sync()
+    return pg, c, Q, O[:T], L[:T]
+
+
+SHAPES = [
+    ([1], [1], 1, 1, 64, 16), ([5], [5], 4, 2, 128, 16), ([128], [128], 2, 2, 128, 128), ([300], [300], 8, 2, 128, 64),
+    ([129, 0, 17, 500, 64], [129, 0, 17, 100, 1], 6, 2, 64, 32), ([1000], [257], 7, 1, 128, 48), ([700, 900], [3, 600], 16, 1, 128, 16),
+    ([200, 40], [150, 40], 40, 1, 64, 16), ([1500], [1400], 12, 12, 64, 128), ([260], [260], 128, 1, 64, 16), ([4], [9], 2, 1, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,news,H_q,H_kv,D,page", SHAPES)
+def test_rows(ctx, dtype, lens, news, H_q, H_kv, D, page):   # noqa: F811
+    _case(ctx, lens, news, H_q, H_kv, D, page, dtype)
+    _case(ctx, lens, news, H_q, H_kv, D, page, dtype, prior=True, nhd=True, pad=7, seed=5, max_rows=max(news))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("W,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (128, 17), (200, 130), (513, 4), (700, 5000), (100000, 4)])
+def test_rows_window(ctx, dtype, W, sinks):   # noqa: F811
+    _case(ctx, [1100, 333, 0, 17], [1100, 90, 0, 17], 8, 2, 128, 16, dtype, W, sinks)
+    _case(ctx, [900, 1300], [1, 700], 6, 2, 64, 64, dtype, W, sinks, prior=True, nhd=True, pad=3)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("lens,news,H_q,H_kv,D,page,W,sinks", [
+    ([9000], [4], 32, 8, 128, 16, 0, 0), ([20000, 100], [2, 3], 4, 1, 64, 64, 0, 0), ([5000, 0, 7000], [17, 2, 1], 8, 2, 128, 128, 4000, 4),
+    ([12000], [300], 2, 2, 128, 32, 0, 0)])
+def test_few_rows_over_a_long_cache(ctx, dtype, lens, news, H_q, H_kv, D, page, W, sinks):   # noqa: F811
+    _case(ctx, lens, news, H_q, H_kv, D, page, dtype, W, sinks)
+    _case(ctx, lens, news, H_q, H_kv, D, page, dtype, W, sinks, prior=True, max_rows=max(news), width=2000)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_large_scores(ctx, dtype):   # noqa: F811
+    """Scores in the hundreds, and scores that grow along the cache so that every block moves the maximum."""
+    _case(ctx, [700], [500], 4, 2, 128, 16, dtype, scale=20.0)
+    for rows, width in ((1500, None), (5, 900)):
+        pg = ref.Pages(3, [1500], 1, 64, 16, dtype, width=width)
+        Q = torch.ones((rows, 2, 64), dtype=dtype, device="cuda")
+        p = torch.arange(1500, device="cuda")
+        pg.k[pg.table[0, p // 16].long(), :, p % 16] = (p / 20.0).to(dtype)[:, None, None]
+        O, L = ctx.paged_attend(binding.PagedCache(pg.k, pg.v), pg.table, pg.lens, Q, cu_rows=_cu([rows]))
+        ref.check_attend(O, L, ref.attend(pg.k, pg.v, pg.table, [1500], [rows], Q), dtype, ref.P_ONCE[dtype])
+
+
+@pytest.mark.parametrize("rows,width,W,sinks", [(300, None, 0, 0), (20, 3000, 0, 0), (300, None, 60, 5), (20, 3000, 600, 2)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_value_that_is_not_finite_stays_with_the_rows_that_see_it(ctx, rows, width, W, sinks, bad):   # noqa: F811
+    """V (or K) of one token is not finite: rows that do not see it are as if it were not there."""
+    n, D, H_q, H_kv = 1300, 64, 4, 2
+    pg = ref.Pages(7, [n], H_kv, D, 16, F16, width=width)
+    Q = _rand(8, rows, H_q, D, dtype=F16)
+    c = binding.PagedCache(pg.k, pg.v)
+    at = torch.arange(n - rows, n, device="cuda")
+    for which in ("v", "k"):
+        for j in (n - rows + 13, n - 30, n - 7, 1):
+            t = getattr(pg, which)
+            page, slot = int(pg.table[0, j // 16]), j % 16
+            old = t[page, :, slot].clone()
+            t[page, :, slot, 3] = bad
+            O, L = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu([rows]), window=W, sinks=sinks)
+            t[page, :, slot] = old
+            see = at >= j
+            if W:
+                see &= (at - W < j) | (j < sinks)
+            want = ref.attend(pg.k, pg.v, pg.table, [n], [rows], Q, W, sinks)
+            blind = [x[~see] for x in want]
+            if (~see).any():
+                ref.check_attend(O[~see], L[~see], blind, F16, ref.P_ONCE[F16], f"{which} {j}")
+            if which == "v":
+                assert not torch.isfinite(O[see][..., 3]).any()
+                keep = [d for d in range(D) if d != 3]
+                ref.check_attend(O[see][..., keep], L[see], [want[0][see][..., keep]] + [x[see] for x in want[1:]], F16, ref.P_ONCE[F16], f"{which} {j}")
+    ctx.sync()
+
+
+def test_hidden_pages_are_not_read(ctx):   # noqa: F811
+    lens, news, W, sinks = [3000, 700], [50, 1], 300, 20
+    pg, c, Q, O, L = _case(ctx, lens, news, 8, 2, 128, 16, F16, W, sinks)
+    table = pg.table.clone()
+    for b, (n, m) in enumerate(zip(lens, news)):
+        first = n - m + 1 - W
+        for i in range(table.shape[1]):
+            if 16 * i >= n or (16 * i >= sinks and 16 * i + 15 < first):
+                table[b, i] = -7
+                if 16 * i < n:
+                    pg.k[pg.table[b, i]], pg.v[pg.table[b, i]] = math.nan, math.nan
+    O2, L2 = ctx.paged_attend(c, table, pg.lens, Q, cu_rows=_cu(news), window=W, sinks=sinks)
+    assert torch.equal(O, O2) and torch.equal(L, L2)
+    ctx.sync()
+
+
+def test_rows_out_of_range_are_reported(ctx):   # noqa: F811
+    pg, c, Q, O, L = _case(ctx, [400, 100], [300, 20], 4, 2, 64, 16, F16)
+    cu = _cu([300, 20])
+
+    def code(*a, **kw):
+        ctx.paged_attend(*a, **kw)
+        with pytest.raises(binding.PckError) as e:
+            ctx.sync()
+        ctx.sync()
+        return str(e.value)
+
+    for bad in (-1, c.n_pages):
+        t = pg.table.clone()
+        t[0, 3] = bad
+        assert "code 8" in code(c, t, pg.lens, Q, cu_rows=cu)
+    assert "code 10" in code(c, pg.table, pg.lens + 500, Q, cu_rows=cu)
+    assert "code 10" in code(c, pg.table, pg.lens, Q, cu_rows=cu, max_rows=10)
+    O2, L2 = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=cu)
+    assert torch.equal(O, O2) and torch.equal(L, L2)
+    with pytest.raises(binding.PckError) as e:
+        d = torch.zeros((3, 1, 16, 256), dtype=F16, device="cuda")
+        ctx.paged_attend(binding.PagedCache(d, d), pg.table, pg.lens, _rand(1, 320, 2, 256, dtype=F16), cu_rows=cu)
+    assert e.value.code == binding.EUNSUPPORTED
+    with pytest.raises(binding.PckError) as e:
+        ctx.paged_attend(c, pg.table, pg.lens, _rand(1, 320, 2 * 129, 64, dtype=F16), cu_rows=cu)
+    assert e.value.code == binding.EUNSUPPORTED
+    with pytest.raises(binding.PckError) as e:
+        ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=cu, max_rows=0)
+    assert e.value.code == binding.EINVAL
+
+
+def test_chunked_prompt_equals_the_whole_and_the_token_steps(ctx):   # noqa: F811
+    """A prompt appended and attended in chunks gives the rows of one call, and its last row is a one-token call's."""
+    H_q, H_kv, D, P, n = 8, 2, 128, 32, 700
+    x = _rand(3, n, H_q + 2 * H_kv, D, dtype=BF16)
+    cs = ref.angles(n, D, "cuda")
+    table = torch.randperm(30, device="cuda")[:-(-n // P)].to(i32)[None].contiguous()
+    k, v = (torch.full((30, H_kv, P, D), math.nan, dtype=BF16, device="cuda") for _ in range(2))
+    c = binding.PagedCache(k, v)
+    out, at = [], 0
+    for m in (300, 1, 399):
+        at += m
+        s = x[at - m:at]
+        ln = torch.tensor([at], dtype=i32, device="cuda")
+        q = ctx.paged_append(c, table, ln, s[:, H_q:H_q + H_kv], s[:, H_q + H_kv:], Q=s[:, :H_q], cu_rows=_cu([m]), cos_sin=cs, norm=True)
+        out.append((q, *ctx.paged_attend(c, table, ln, q, cu_rows=_cu([m]))))
+    q, O, L = (torch.cat(t) for t in zip(*out))
+    want = ref.attend(k, v, table, [n], [n], q)
+    ref.check_attend(O, L, want, BF16, ref.P_ONCE[BF16])
+    O1, L1 = ctx.paged_attend(c, table, ln, q[-1:])
+    ref.check_attend(O1, L1, [t[-1:] for t in want], BF16, ref.P_SPLIT[BF16])
+    ctx.sync()
+
+
+def test_prompt_in_a_graph_with_other_lengths(ctx):   # noqa: F811
+    """A captured call follows the lengths and row counts it finds at replay."""
+    H_q, H_kv, D, P, T = 8, 2, 64, 16, 400
+    for width, lens, news in ((60, [[300, 100], [50, 900], [0, 400]], [[300, 100], [50, 350], [0, 400]]),
+                              (900, [[9000, 30], [14000, 2]], [[20, 5], [3, 2]])):
+        pg = ref.Pages(4, [16 * width // 2 if b else min(16 * width, 14400) for b in range(2)], H_kv, D, P, F16, width=width)
+        rows = T if width == 60 else 25
+        Q = _rand(5, rows, H_q, D, dtype=F16)
+        ln, cu = torch.zeros(2, dtype=i32, device="cuda"), torch.zeros(3, dtype=i32, device="cuda")
+        c = binding.PagedCache(pg.k, pg.v)
+        ctx.paged_attend(c, pg.table, ln, Q, cu_rows=cu)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            O, L = ctx.paged_attend(c, pg.table, ln, Q, cu_rows=cu)
+        for a, m in zip(lens, news):
+            a = [min(x, int((pg.lens[i]))) for i, x in enumerate(a)]
+            ln.copy_(torch.tensor(a, dtype=i32))
+            cu.copy_(_cu(m))
+            g.replay()
+            torch.cuda.synchronize()
+            t = sum(m)
+            ref.check_attend(O[:t], L[:t], ref.attend(pg.k, pg.v, pg.table, a, m, Q[:t]), F16, ref.P_ONCE[F16])
+    ctx.sync()
