@@ -11,23 +11,24 @@
 //    share every K and V tile) and walks its keys in blocks of 128. While one tile's softmax runs, the
 //    other tile's MMAs do. TMEM: two S (128 columns each; P of a block overwrites its S as packed 16-bit
 //    values) and two O (D columns each).
-//  * Warp 9 loads Q and a ring of K and V blocks by TMA with 128-byte swizzle, one box per page run (a box
+//  * One warp loads Q and a ring of K and V blocks by TMA with 128-byte swizzle, one box per page run (a box
 //    is the largest power-of-two run of tokens that divides both the page and the block). K is the
 //    K-major B operand of S = Q K^T as it lies; V, stored token by token, is the MN-major B operand of
 //    O += P V, so nothing is transposed.
-//  * Warp 8 issues tcgen05.mma: S0(j+1) right behind O0 += P0(j) V(j), then the same for tile 1.
-//  * Warps 0-3 and 4-7 are the tiles' softmax, a thread per row: 128 scores in registers, the block's
-//    maximum (the running maximum moves only when passed by 8 (log2), so p <= 2^8 and O is rarely
-//    rescaled), p = 2^(s - m) rounded once to the cache's type for the second MMA (its rounding is like
-//    that of the 16-bit output), their fp32 sum from the unrounded p.
+//  * One warp issues tcgen05.mma: S0(j+1) right behind O0 += P0(j) V(j), then the same for tile 1.
+//  * Warps 0-3 and 4-7 are the tiles' softmax, a thread per row. p = 2^(s - m) at the running maximum, which
+//    is checked by the weights' sum and moved only when that passes 2^15: no pass over the scores looks for
+//    a maximum, and O is rarely rescaled. p is rounded once to the cache's type for the second MMA (a
+//    rounding like that of the 16-bit output); its fp32 sum takes the unrounded p.
 //  * Keys: with a window, the sinks' boxes and then the window's are laid end to end, so no block is spent
 //    on hidden keys and the pages between are never touched. Only blocks that some row does not see
 //    whole are masked, by a 16-bit mask per row and 16 keys.
 //  * V rows that no row of the CTA sees (behind the last token, in front of the window) are zeroed in
-//    shared memory, since 0 * NaN would keep what they hold. Where a value that only some rows see is
-//    not finite, the rows it spoiled are recomputed one by one from the visible keys alone.
+//    shared memory, since 0 * NaN would keep what they hold. V rows of partly hidden blocks that are not
+//    finite are cleared too, and added at the end by the rows that see them.
 //  * Few rows over a long cache: the keys are split over n_split CTAs and a second kernel joins them.
 #include <algorithm>
+#include <type_traits>
 
 #include "pck_paged.cuh"
 
@@ -37,9 +38,9 @@ namespace {
 constexpr int RW_M = 128;              // rows of a tile
 constexpr int RW_BLOCK = 128;          // keys of a block
 constexpr int RW_THREADS = 384;        // two softmax warpgroups; MMA warp, load warp and two idle ones
-// registers a thread: 168 at launch (384 x 168 <= 65,536); 232 x 256 + 40 x 128 = 384 x 168 after the split
-constexpr int RW_REGS_SOFTMAX = 232, RW_REGS_OTHER = 40;
 constexpr int RW_MMA_WARP = 8, RW_LOAD_WARP = 9;
+// registers a thread: 168 at launch (384 x 168 <= 65,536); 216 x 256 + 72 x 128 = 384 x 168 after the split
+constexpr int RW_REGS_SOFTMAX = 216, RW_REGS_OTHER = 72;
 
 template <int D>
 struct RCfg {
@@ -49,7 +50,8 @@ struct RCfg {
     static constexpr int NST = D == 128 ? 5 : 8;               // ring stages (a K or a V block each)
     static constexpr int OFF_RING = 2 * TILE;
     static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-    static constexpr int SMEM = OFF_BAR + 512 + 1024;          // + alignment slack
+    static constexpr int BAR_BYTES = 768;                      // barriers, TMEM address, this CTA's rows, spoilt keys
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;    // + alignment slack
     static constexpr int S_COL = 0, O_COL = 256;               // TMEM: S of tile t at 128 t, O at 256 + D t
     static constexpr int TMEM_COLS = 512;
 };
@@ -68,15 +70,47 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo) {
     return d;
 }
 // fp32 accumulator; A and B both fp16 (fmt 0) or bf16 (fmt 1); b_mn: B is MN-major
-__device__ __forceinline__ uint32_t idesc_16(int fmt, int N, int b_mn) {
+__host__ __device__ constexpr uint32_t idesc_16(int fmt, int N, int b_mn) {
     return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) | (static_cast<uint32_t>(b_mn) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(RW_M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMAs of one block and tile, issued by one elected lane of a converged warp: one election for all of
+// them, the operands' descriptors advanced by constants. The whole warp walks the issuing loop with values
+// that are warp-uniform; elected one by one, or issued from a lane's own branch, an MMA cost about 100
+// cycles to issue where its 16 k run 64.
+// D += A B^T over 64 elements of k (4 MMAs), A and B from shared memory; acc 0: the first one overwrites D
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{ .reg .pred p, e; .reg .b32 rx; elect.sync rx|e, 0xffffffff; setp.ne.u32 p, %4, 0; "
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+        "{ .reg .pred p, e, t; .reg .b32 rx; .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "setp.ne.u32 p, %4, 0; setp.eq.u32 t, 0, 0;\n"
+        "add.u64 a1, %1, 2; add.u64 a2, %1, 4; add.u64 a3, %1, 6;\n"
+        "add.u64 b1, %2, 2; add.u64 b2, %2, 4; add.u64 b3, %2, 6;\n"
+        "elect.sync rx|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t; }"
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// D += A B over 128 k (8 MMAs), A from TMEM (8 columns an MMA), B MN-major (2048 bytes an MMA)
+__device__ __forceinline__ void mma_ts8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{ .reg .pred p, e, t; .reg .b32 rx, a1, a2, a3, a4, a5, a6, a7; .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n"
+        "setp.ne.u32 p, %4, 0; setp.eq.u32 t, 0, 0;\n"
+        "add.u32 a1, %1, 8; add.u32 a2, %1, 16; add.u32 a3, %1, 24; add.u32 a4, %1, 32;\n"
+        "add.u32 a5, %1, 40; add.u32 a6, %1, 48; add.u32 a7, %1, 56;\n"
+        "add.u64 b1, %2, 128; add.u64 b2, %2, 256; add.u64 b3, %2, 384; add.u64 b4, %2, 512;\n"
+        "add.u64 b5, %2, 640; add.u64 b6, %2, 768; add.u64 b7, %2, 896;\n"
+        "elect.sync rx|e, 0xffffffff;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t; }"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -142,6 +176,8 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     return d;
 }
 
+template <typename T> struct IsBf16 { static constexpr bool value = false; };
+template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
 template <typename T> __device__ __forceinline__ uint32_t pack16(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 template <> __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
@@ -152,6 +188,20 @@ template <typename T> __device__ __forceinline__ float2 unpack16(uint32_t u);
 template <> __device__ __forceinline__ float2 unpack16<__half>(uint32_t u) { return __half22float2(u32_as_h2(u)); }
 template <> __device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Bounded wait on an mbarrier phase that lets the warp sleep in the barrier: with a time hint (20 us) try_wait
+// suspends it, without one it comes back soon and the polls take issue slots from the other tile's softmax.
+// Gives up after 2^17 hints (over two seconds).
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+    for (uint32_t it = 0; it < (1u << 17); ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+            : "=r"(ok) : "r"(bar), "r"(parity), "r"(20000u) : "memory");
+        if (ok) return true;
+    }
+    return false;
 }
 
 // ---------------------------------------------------------------- which rows, which keys
@@ -243,43 +293,68 @@ __device__ __forceinline__ int page_of(const PagedAttn& P, int b, int key) {
     return pg;
 }
 
-// One row over virtual keys [v0, v1) on its own, from global memory: m, l and its O (unnormalised, staged in
-// `o`, D floats, by the calling thread). Only for rows whose O came out not finite while their scores were:
-// V of a key that other rows see is not finite. Slow, and right for any values in keys that the row does not see.
+// Keys of partly hidden blocks whose V is not finite: the MMAs ran with those V rows cleared (0 * NaN is NaN, and a row
+// that does not see the key must not get it), and the rows that do see them add p V here, at the end. One record per
+// partly hidden block: its number and a bit per key.
+constexpr int RW_MAX_EDGE = 12;        // blocks that some row of a CTA sees and another does not: 8 at most
+struct Spoilt {
+    int any, n;
+    struct {
+        int block;
+        uint32_t keys[4];
+    } e[RW_MAX_EDGE];
+};
+
 template <typename T, int D>
-__device__ __noinline__ void row_alone(const PagedAttn& P, int b, int g, int64_t qoff, int p, Keys K, int v0, int v1, float m,
-                                       float* o, const char* kbase, const char* vbase, const int64_t* st) {
-    for (int d = 0; d < D; ++d) o[d] = 0.f;
+__device__ __noinline__ void add_spoilt(const PagedAttn& P, const Spoilt* sp, int b, int g, int64_t qoff, int p, Keys K, float m, uint32_t o_tm) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(P.Q) + qoff);
-    for (int v = v0; v < v1; ++v) {
-        const int key = K.key(v);
-        if (!(seen16(key & ~15, p, P.window, P.sinks) >> (key & 15) & 1)) continue;
-        const int64_t pg = page_of(P, b, key);
-        const int slot = key % P.page;
-        const uint4* k = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(kbase) + pg * st[0] + g * st[1] + slot * st[2]);
-        const uint4* vv = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(vbase) + pg * st[3] + g * st[4] + slot * st[5]);
-        float s = 0.f;
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 a = q[c], e = k[c];
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, ew[4] = {e.x, e.y, e.z, e.w};
+    for (int c = 0; c < D; c += 32) {
+        float o[32];
+        ld32(o_tm + c, o);
+        wait_ld();
+        for (int e = 0; e < sp->n; ++e)
+            for (int i = 0; i < RW_BLOCK; ++i) {
+                if (!(sp->e[e].keys[i >> 5] >> (i & 31) & 1)) continue;
+                const int key = K.key(sp->e[e].block * RW_BLOCK + i);
+                if (p < 0 || !(seen16(key & ~15, p, P.window, P.sinks) >> (key & 15) & 1)) continue;
+                const int64_t pg = page_of(P, b, key);
+                const int slot = key % P.page;
+                const int64_t* st = P.kv_stride;
+                const uint4* k = reinterpret_cast<const uint4*>(static_cast<const T*>(P.k_base) + pg * st[0] + g * st[1] + slot * st[2]);
+                const uint4* v = reinterpret_cast<const uint4*>(static_cast<const T*>(P.v_base) + pg * st[3] + g * st[4] + slot * st[5]) + c / 8;
+                float s = 0.f;
+                for (int d = 0; d < D / 8; ++d) {
+                    const uint4 x = q[d], y = k[d];
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack16<T>(aw[i]), y = unpack16<T>(ew[i]);
-                s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
-            }
-        }
-        const float w = ex2_approx(fmaf(s, P.scale_log2, -m));
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 e = vv[c];
-            const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 f = unpack16<T>(xw[h]), w = unpack16<T>(yw[h]);
+                        s = fmaf(f.x, w.x, fmaf(f.y, w.y, s));
+                    }
+                }
+                const float w = ex2_approx(fmaf(s, P.scale_log2, -m));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 y = unpack16<T>(ew[i]);
-                o[8 * c + 2 * i] = fmaf(w, y.x, o[8 * c + 2 * i]);
-                o[8 * c + 2 * i + 1] = fmaf(w, y.y, o[8 * c + 2 * i + 1]);
+                for (int d = 0; d < 4; ++d) {
+                    const uint4 x = v[d];
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 f = unpack16<T>(xw[h]);
+                        o[8 * d + 2 * h] = fmaf(w, f.x, o[8 * d + 2 * h]);
+                        o[8 * d + 2 * h + 1] = fmaf(w, f.y, o[8 * d + 2 * h + 1]);
+                    }
+                }
             }
-        }
+        __syncwarp();
+        st32(o_tm + c, reinterpret_cast<const uint32_t*>(o));
+        wait_st();
     }
+}
+
+// Whether one of the two values of a packed pair is infinite or NaN.
+template <typename T> __device__ __forceinline__ bool not_finite2(uint32_t u) {
+    const uint32_t e = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
+    return (u & e) == e || ((u >> 16) & e) == e;
 }
 
 // Weights of a row's own attention and of the prior in the result, and the LSE of both.
@@ -316,14 +391,15 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_u32(smem);
-    // barriers: Q of each tile, ring full / empty, S ready, P ready (128 arrivals), O += P V done
+    // barriers: Q of each tile, ring full / empty; of each tile: S ready, P ready (4 warps), O += P V done
     constexpr int B_Q = 0, B_F = 16, B_E = B_F + 8 * C::NST, B_S = B_E + 8 * C::NST, B_P = B_S + 16, B_O = B_P + 16,
                   B_DR = B_O + 16, N_BAR = B_DR / 8 + 1;
     const uint32_t bar = s_base + C::OFF_BAR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * N_BAR);
     RowTile* s_tile = reinterpret_cast<RowTile*>(smem + C::OFF_BAR + 8 * N_BAR + 16);
-    static_assert(8 * N_BAR + 16 + sizeof(RowTile) <= 512, "barrier area");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Spoilt* s_spoilt = reinterpret_cast<Spoilt*>(s_tile + 1);
+    static_assert(8 * N_BAR + 16 + sizeof(RowTile) + sizeof(Spoilt) <= C::BAR_BYTES, "barrier area");
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int G = P.G, tpt = RW_M / G, tt = 2 * tpt;
     // later tiles first (they see the most keys); kv heads next to one another, then key splits
     const int per_tile = P.H_kv * P.n_split;
@@ -332,8 +408,9 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     const int g = sub % P.H_kv, split = sub / P.H_kv;
 
     if (tid == 0) {
-        for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i == B_P || 8 * i == B_P + 8) ? 128 : 1);
+        for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i >= B_P && 8 * i < B_P + 16) ? 4 : 1);
         fence_mbar_init();
+        s_spoilt->any = s_spoilt->n = 0;
     }
     if (warp == RW_LOAD_WARP && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_q) : "memory");
@@ -377,7 +454,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
         auto keys_in = [&](int j) { return min(RW_BLOCK, K.total - (j0 + j) * RW_BLOCK); };   // of block j of this CTA
         bool failed = false;
 
-        if (warp >= 8) {
+        if (warp >= RW_MMA_WARP) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RW_REGS_OTHER));
             if (warp == RW_LOAD_WARP) {
                 // ------------------------------------------------------------ loads
@@ -401,7 +478,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     int i = 0;
                     for (; i < 2 * nb; ++i) {   // K(0), V(0), K(1), V(1), ...
                         const int j = i >> 1, st = i % C::NST, nk = keys_in(j);
-                        if (i >= C::NST && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_E + 8 * st, (i / C::NST - 1) & 1))) {
+                        if (i >= C::NST && !__all_sync(0xffffffffu, wait_bar(bar + B_E + 8 * st, (i / C::NST - 1) & 1))) {
                             failed = true;
                             break;
                         }
@@ -417,68 +494,72 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     if (failed && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
                     // the copies in flight land before the CTA can end, whatever the other warps do
                     for (int q = max(0, i - C::NST); q < i; ++q)
-                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_F + 8 * (q % C::NST), (q / C::NST) & 1))) break;
+                        if (!__all_sync(0xffffffffu, wait_bar(bar + B_F + 8 * (q % C::NST), (q / C::NST) & 1))) break;
                 }
             } else if (warp == RW_MMA_WARP) {
                 // ------------------------------------------------------------ MMAs
-                const int fmt = P.dtype == PCK_DT_BF16 ? 1 : 0;
+                // broadcasts, so that the compiler sees them as uniform
+                const int nbu = __shfl_sync(0xffffffffu, nb, 0), ntu = __shfl_sync(0xffffffffu, ntile, 0);
+                const int nk_last = __shfl_sync(0xffffffffu, nb > 0 ? keys_in(nb - 1) : 0, 0);
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                constexpr int FMT = IsBf16<T>::value ? 1 : 0;
+                constexpr uint32_t ID_PV = idesc_16(FMT, D, 1), ID_S = idesc_16(FMT, RW_BLOCK, 0);
                 const uint64_t q_desc = desc_sw128(s_base, 16);
                 const uint64_t k_desc = desc_sw128(s_base + C::OFF_RING, 16);
                 const uint64_t v_desc = desc_sw128(s_base + C::OFF_RING, C::CHUNK);
-                const uint32_t id_pv = idesc_16(fmt, D, 1);
                 auto wait = [&](int off, int phase) {
-                    if (!failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + off, phase & 1))) failed = true;
+                    if (!failed && !__all_sync(0xffffffffu, wait_bar(bar + off, phase & 1))) failed = true;
                     return !failed;
                 };
                 auto issue_S = [&](int t, int j) {   // S_t = Q_t K(j)^T
-                    const int i = 2 * j, st = i % C::NST;
-                    const uint32_t id = idesc_16(fmt, keys_in(j), 0);
+                    const int st = (2 * j) % C::NST;
+                    const uint32_t id = j + 1 < nbu ? ID_S : idesc_16(FMT, nk_last, 0);
                     const uint64_t qd = q_desc + static_cast<uint64_t>((t * C::TILE) >> 4), kd = k_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
-    #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint64_t off = (s >> 2) * (C::CHUNK >> 4) + (s & 3) * 2;
-                        mma_ss(tmem + C::S_COL + 128 * t, qd + off, kd + off, id, s > 0);
-                    }
+#pragma unroll
+                    for (int c = 0; c < C::CH; ++c)
+                        mma_ss4(tm + C::S_COL + 128 * t, qd + c * (C::CHUNK >> 4), kd + c * (C::CHUNK >> 4), id, c > 0);
                     commit(bar + B_S + 8 * t);
-                    if (t == ntile - 1) commit(bar + B_E + 8 * st);
+                    if (t == ntu - 1) commit(bar + B_E + 8 * st);
                 };
                 auto issue_PV = [&](int t, int j) {  // O_t += P_t V(j)
-                    const int i = 2 * j + 1, st = i % C::NST, nk = keys_in(j);
+                    const int st = (2 * j + 1) % C::NST;
                     const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
-    #pragma unroll
-                    for (int u = 0; u < RW_BLOCK / 16; ++u)
-                        if (16 * u < nk)
-                            mma_ts(tmem + C::O_COL + D * t, tmem + C::S_COL + 128 * t + 8 * u, vd + static_cast<uint64_t>(u * (2048 >> 4)), id_pv,
-                                   j > 0 || u > 0);
+                    const uint32_t d = tm + C::O_COL + D * t, a = tm + C::S_COL + 128 * t;
+                    if (j + 1 < nbu || nk_last == RW_BLOCK) {
+                        mma_ts8(d, a, vd, ID_PV, j > 0);
+                    } else {
+                        for (int u = 0; 16 * u < nk_last; ++u)
+                            mma_ts(d, a + 8 * u, vd + static_cast<uint64_t>(u * (2048 >> 4)), ID_PV, j > 0 || u > 0);
+                    }
                     commit(bar + B_O + 8 * t);
-                    if (t == ntile - 1) commit(bar + B_E + 8 * st);
+                    if (t == ntu - 1) commit(bar + B_E + 8 * st);
                 };
-                if (nb > 0 && wait(B_F, 0)) {
-                    for (int t = 0; t < ntile; ++t)
+                if (nbu > 0 && wait(B_F, 0)) {
+                    for (int t = 0; t < ntu; ++t)
                         if (wait(B_Q + 8 * t, 0)) issue_S(t, 0);
-                    for (int j = 0; j < nb && !failed; ++j) {
+                    for (int j = 0; j < nbu && !failed; ++j) {
                         const int iv = 2 * j + 1, ik = 2 * j + 2;
-                        for (int t = 0; t < ntile; ++t) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (t >= ntu) break;
+                            if (t == 0 && !(wait(B_F + 8 * (iv % C::NST), iv / C::NST) &&
+                                            (j + 1 == nbu || wait(B_F + 8 * (ik % C::NST), ik / C::NST)))) break;
                             if (!wait(B_P + 8 * t, j)) break;
-                            if (t == 0 && !wait(B_F + 8 * (iv % C::NST), iv / C::NST)) break;
                             fence_after();
                             issue_PV(t, j);
-                            if (j + 1 < nb) {
-                                if (t == 0 && !wait(B_F + 8 * (ik % C::NST), ik / C::NST)) break;
-                                issue_S(t, j + 1);
-                            }
+                            if (j + 1 < nbu) issue_S(t, j + 1);
                         }
                     }
                 }
                 if (failed && lane == 0) set_err(P.err, ERR_ROWS_MMA);
                 commit(bar + B_DR);      // no MMA writes TMEM any more when the CTA gives it back
-                __all_sync(0xffffffffu, mbar_wait_bounded(bar + B_DR, 0));
+                __all_sync(0xffffffffu, wait_bar(bar + B_DR, 0));
             }
         } else {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_REGS_SOFTMAX));
             if (warp < 4 * ntile) {
-                // ------------------------------------------------------------ softmax: row r of tile t
-                const int t = warp >> 2, r = tid & 127;
+                // -------------------------------------------------------- softmax: row r of tile t
+                const int t = warp >> 2, r = (warp & 3) * 32 + lane;
                 const int rtok = t * tpt + r / G;                     // token of the CTA
                 const bool row_ok = r < tpt * G && rtok < rows_here && rt.row0 + rt.tok0 + rtok < P.T && rt.row0 >= 0;
                 const int p = row_ok ? p0 + rtok : -1;
@@ -489,110 +570,167 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 const uint32_t s_tm = tmem + C::S_COL + 128 * t + lane_base, o_tm = tmem + C::O_COL + D * t + lane_base;
                 const float sc = P.scale_log2;
                 float m = -INFINITY, l = 0.f;
+                int n_edge = 0;
+                // A wait that runs out only marks the warp: it goes on, without work, to the barrier at the end.
                 for (int j = 0; j < nb; ++j) {
                     const int v0 = (j0 + j) * RW_BLOCK, nk = keys_in(j);
                     const int ka = K.key(v0), kz = K.key(v0 + nk - 1);
-                    if (t == 0 && (kz > p1 || kz - ka != nk - 1 || (P.window > 0 && ka <= p0 - P.window))) {
-                        // V rows that no row of the CTA sees are cleared (thread r: row r of the block)
+                    // Partly hidden from the CTA's rows: V rows that none of them sees are cleared (they may hold
+                    // anything), and so are those that are not finite, which are put on record. Thread r: row r.
+                    if (t == 0 && (kz > p0 || kz - ka != nk - 1 || (P.window > 0 && ka <= p1 - P.window && kz >= P.sinks))) {
                         const int st = (2 * j + 1) % C::NST;
-                        if (!mbar_wait_bounded(bar + B_F + 8 * st, ((2 * j + 1) / C::NST) & 1)) failed = true;
+                        if (!failed && !wait_bar(bar + B_F + 8 * st, ((2 * j + 1) / C::NST) & 1)) failed = true;
                         const int key = K.key(v0 + r);
-                        if (!failed && r < nk && (key > p1 || (P.window > 0 && key <= p0 - P.window && key >= P.sinks))) {
-                            uint4* row = reinterpret_cast<uint4*>(smem + C::OFF_RING + st * C::TILE + r * 128);
-                            for (int c = 0; c < C::CH; ++c)
-    #pragma unroll
-                                for (int i = 0; i < 8; ++i) row[c * (C::CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+                        bool clear = false, spoilt = false;
+                        uint4* row = reinterpret_cast<uint4*>(smem + C::OFF_RING + st * C::TILE + r * 128);
+                        if (!failed && r < nk) {
+                            clear = key > p1 || (P.window > 0 && key <= p0 - P.window && key >= P.sinks);
+                            if (!clear && n_edge < RW_MAX_EDGE) {
+                                for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const uint4 x = row[c * (C::CHUNK / 16) + i];
+                                        spoilt |= not_finite2<T>(x.x) | not_finite2<T>(x.y) | not_finite2<T>(x.z) | not_finite2<T>(x.w);
+                                    }
+                            }
+                            if (clear || spoilt)
+                                for (int c = 0; c < C::CH; ++c)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) row[c * (C::CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
+                        }
+                        const uint32_t bits = __ballot_sync(0xffffffffu, spoilt);
+                        if (n_edge < RW_MAX_EDGE) {
+                            if (lane == 0) {
+                                s_spoilt->e[n_edge].block = j0 + j;
+                                s_spoilt->e[n_edge].keys[warp] = bits;
+                                s_spoilt->n = n_edge + 1;
+                                if (bits) s_spoilt->any = 1;
+                            }
+                            ++n_edge;
                         }
                         fence_proxy_async_smem();
                     }
-                    if (!__all_sync(0xffffffffu, !failed && mbar_wait_bounded(bar + B_S + 8 * t, j & 1))) {
-                        failed = true;
-                        break;
-                    }
+                    if (!__all_sync(0xffffffffu, !failed && wait_bar(bar + B_S + 8 * t, j & 1))) failed = true;
                     fence_after();
-                    float s[RW_BLOCK];
-    #pragma unroll
-                    for (int c = 0; c < 4; ++c) ld32(s_tm + 32 * c, s + 32 * c);
-                    wait_ld();
                     // every row of the tile sees the whole block, or masks: 16 keys at a time
                     const bool full = nk == RW_BLOCK && kz - ka == RW_BLOCK - 1 && kz <= pa &&
                                       (P.window <= 0 || ka > pz - P.window || kz < P.sinks);
-                    if (!full) {
-    #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint32_t see = 16 * c < nk ? seen16(K.key(v0 + 16 * c), p, P.window, P.sinks) : 0u;
-    #pragma unroll
-                            for (int i = 0; i < 16; ++i) s[16 * c + i] = see >> i & 1 ? s[16 * c + i] : -INFINITY;
+                    auto mask = [&](int c, float* x) {      // keys 32 c .. of the block
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int v = 32 * c + 16 * h;
+                            const uint32_t see = v < nk ? seen16(K.key(v0 + v), p, P.window, P.sinks) : 0u;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) x[16 * h + i] = see >> i & 1 ? x[16 * h + i] : -INFINITY;
                         }
-                    }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
-    #pragma unroll
-                    for (int i = 4; i < RW_BLOCK; i += 8)
-    #pragma unroll
-                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], i + 4 + q < RW_BLOCK ? fmaxf(s[i + q], s[i + 4 + q]) : s[i + q]);
-                    const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    const bool need = row_ok && bm > m + 8.f;
-                    if (__any_sync(0xffffffffu, need)) {
-                        const float mn = need ? bm : m;
-                        const float al = need ? ex2_approx(m - mn) : 1.0f;     // 0 from m = -inf
-                        if (j > 0) {   // O is quiet once P V of the previous block is done
-                            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_O + 8 * t, (j - 1) & 1))) {
-                                failed = true;
-                                break;
+                    };
+                    // p = 2^(s - m) at the running maximum, packed, and their sum
+                    uint32_t pk[RW_BLOCK / 2];
+                    float bs = 0.f;
+                    auto weights = [&](auto masked) {
+                        const float ms = m > -INFINITY ? m : 0.f;
+                        const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-ms, -ms);
+                        uint64_t acc[2] = {0, 0};
+                        float x[2][32];
+                        ld32(s_tm, x[0]);
+                        wait_ld();
+#pragma unroll
+                        for (int c = 0; c < RW_BLOCK / 32; ++c) {   // the next chunk's load runs under this one's arithmetic
+                            if (c + 1 < RW_BLOCK / 32) ld32(s_tm + 32 * (c + 1), x[(c + 1) & 1]);
+                            float* y = x[c & 1];
+                            if (masked) mask(c, y);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float x0, x1;
+                                f2_unpack(f2_fma(f2_pack(y[2 * i], y[2 * i + 1]), sc2, nm2), x0, x1);
+                                x0 = ex2_approx(x0);
+                                x1 = ex2_approx(x1);
+                                acc[i & 1] = f2_add(acc[i & 1], f2_pack(x0, x1));
+                                pk[16 * c + i] = pack16<T>(x0, x1);
                             }
-                            fence_after();
-    #pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                ld32(o_tm + c, o);
+                            if (c + 1 < RW_BLOCK / 32) wait_ld();
+                        }
+                        float a0, a1, b0, b1;
+                        f2_unpack(acc[0], a0, a1);
+                        f2_unpack(acc[1], b0, b1);
+                        bs = (a0 + a1) + (b0 + b1);
+                    };
+                    // The maximum moves only when it has to: a sum up to 2^15 bounds every p by 2^15, which fp16 and
+                    // bf16 hold as exactly as smaller ones. Otherwise (and where a row has no maximum yet) the block's
+                    // maximum is found, O and l are rescaled, and the weights taken again.
+                    bool again = true;
+                    if (j > 0) {
+                        if (!failed) {
+                            if (full) weights(std::false_type());
+                            else weights(std::true_type());
+                        }
+                        again = __any_sync(0xffffffffu, row_ok && (!(bs <= 32768.f) || m == -INFINITY));
+                    }
+                    if (again) {
+                        float bm = -INFINITY;
+                        if (!failed) {
+#pragma unroll 1
+                            for (int c = 0; c < RW_BLOCK / 32; ++c) {
+                                float x[32];
+                                ld32(s_tm + 32 * c, x);
                                 wait_ld();
-    #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= al;
-                                st32(o_tm + c, reinterpret_cast<const uint32_t*>(o));
+                                if (!full) mask(c, x);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) bm = fmaxf(bm, x[i]);
+                            }
+                        }
+                        const float mn = fmaxf(m, bm * sc);
+                        const float al = mn > m ? ex2_approx(m - mn) : 1.0f;     // 0 from m = -inf
+                        if (j > 0) {   // O is quiet once P V of the previous block is done
+                            if (!__all_sync(0xffffffffu, !failed && wait_bar(bar + B_O + 8 * t, (j - 1) & 1))) failed = true;
+                            fence_after();
+                            if (!failed) {
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 32) {
+                                    float o[32];
+                                    ld32(o_tm + c, o);
+                                    wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] *= al;
+                                    st32(o_tm + c, reinterpret_cast<const uint32_t*>(o));
+                                }
                             }
                         }
                         l *= al;
                         m = mn;
+                        if (!failed) {
+                            if (full) weights(std::false_type());
+                            else weights(std::true_type());
+                        }
                     }
-                    const float ms = m > -INFINITY ? m : 0.f;
-                    const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(-ms, -ms);
-                    uint64_t a0 = 0, a1 = 0;
-                    uint32_t pk[RW_BLOCK / 2];
-    #pragma unroll
-                    for (int i = 0; i < RW_BLOCK / 2; ++i) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), sc2, nm2), x0, x1);
-                        const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-                        if (i & 1) a1 = f2_add(a1, f2_pack(e0, e1));
-                        else a0 = f2_add(a0, f2_pack(e0, e1));
-                        pk[i] = pack16<T>(e0, e1);
+                    if (!failed) {
+                        st32(s_tm, pk);
+                        st32(s_tm + 32, pk + 32);
+                        l += bs;
+                        wait_st();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar + B_P + 8 * t);
                     }
-                    st32(s_tm, pk);
-                    st32(s_tm + 32, pk + 32);
-                    float x0, x1, y0, y1;
-                    f2_unpack(a0, x0, x1);
-                    f2_unpack(a1, y0, y1);
-                    l += (x0 + x1) + (y0 + y1);
-                    wait_st();
-                    fence_before();
-                    mbar_arrive(bar + B_P + 8 * t);
                 }
-                if (nb > 0 && !failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + B_O + 8 * t, (nb - 1) & 1))) {
+                if (nb > 0 && !failed && !__all_sync(0xffffffffu, wait_bar(bar + B_O + 8 * t, (nb - 1) & 1))) {
                     set_err(P.err, ERR_ROWS_O);
                     failed = true;
                 } else if (failed) {
                     set_err(P.err, ERR_ROWS_SOFTMAX);
                 }
+                fence_after();
+                asm volatile("barrier.cta.sync 1, %0;" ::"r"(128 * ntile) : "memory");   // the record of spoilt keys is complete
                 if (!failed) {
-                    fence_after();
                     const int64_t trow = rt.row0 + rt.tok0 + rtok;
                     const int64_t row = trow * P.H_q + hq;
                     const bool direct = P.n_split == 1;
                     RowEnd e = {1.f, 0.f, 0.f, false};
                     if (direct && row_ok) e = row_end(P, row, m, l);
                     float* part = P.ws + ((size_t)((size_t)tile_idx * per_tile + sub) * (2 * RW_M) + t * RW_M + r) * rows_partial_floats(D);
-                    bool spoiled = false;
-    #pragma unroll
+                    if (nb > 0 && s_spoilt->any)
+                        add_spoilt<T, D>(P, s_spoilt, b, g, trow * P.q_row + (int64_t)hq * P.q_head, p, K, m, o_tm);
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
                         if (nb > 0) {
@@ -602,8 +740,6 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = 0.f;
                         }
-    #pragma unroll
-                        for (int i = 0; i < 32; ++i) spoiled |= !(fabsf(o[i]) < INFINITY);
                         if (!row_ok) continue;
                         if (direct) {
                             if (l == 0.f) {
@@ -639,25 +775,6 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                         } else {
                             part[0] = m;
                             part[1] = l;
-                        }
-                        if (spoiled && l > 0.f) {
-                            float o[D];
-                            row_alone<T, D>(P, b, g, trow * P.q_row + (int64_t)hq * P.q_head, p, K, j0 * RW_BLOCK,
-                                            min(K.total, j1 * RW_BLOCK), m, o, static_cast<const char*>(P.k_base),
-                                            static_cast<const char*>(P.v_base), P.kv_stride);
-                            for (int d = 0; d < D; d += 2) {
-                                if (direct) {
-                                    float x0 = o[d] * e.wo, x1 = o[d + 1] * e.wo;
-                                    if (e.prior) {
-                                        x0 = fmaf(P.O_prior[row * D + d], e.wp, x0);
-                                        x1 = fmaf(P.O_prior[row * D + d + 1], e.wp, x1);
-                                    }
-                                    *reinterpret_cast<uint32_t*>(static_cast<T*>(P.O) + row * D + d) = pack16<T>(x0, x1);
-                                } else {
-                                    part[4 + d] = o[d];
-                                    part[5 + d] = o[d + 1];
-                                }
-                            }
                         }
                     }
                 }
