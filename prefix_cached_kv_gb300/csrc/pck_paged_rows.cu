@@ -11,7 +11,7 @@
 //    share every K and V tile) and walks its keys in blocks of 128. While one tile's softmax runs, the
 //    other tile's MMAs do. TMEM: two S (128 columns each; P of a block overwrites its S as packed 16-bit
 //    values) and two O (D columns each).
-//  * One warp loads Q and a ring of K and V blocks by TMA with 128-byte swizzle, one box per page run (a box
+//  * One warp loads Q and rings of K and of V blocks by TMA with 128-byte swizzle, one box per page run (a box
 //    is the largest power-of-two run of tokens that divides both the page and the block). K is the
 //    K-major B operand of S = Q K^T as it lies; V, stored token by token, is the MN-major B operand of
 //    O += P V, so nothing is transposed.
@@ -22,7 +22,7 @@
 //    rounding like that of the 16-bit output); its fp32 sum takes the unrounded p.
 //  * Keys: with a window, the sinks' boxes and then the window's are laid end to end, so no block is spent
 //    on hidden keys and the pages between are never touched. Only blocks that some row does not see
-//    whole are masked, by a 16-bit mask per row and 16 keys.
+//    whole are masked, by a bit mask per row and 32 keys.
 //  * V rows that no row of the CTA sees (behind the last token, in front of the window) are zeroed in
 //    shared memory, since 0 * NaN would keep what they hold. V rows of partly hidden blocks that are not
 //    finite are cleared too, and added at the end by the rows that see them.
@@ -37,8 +37,8 @@ namespace {
 
 constexpr int RW_M = 128;              // rows of a tile
 constexpr int RW_BLOCK = 128;          // keys of a block
-constexpr int RW_THREADS = 384;        // two softmax warpgroups; MMA warp, load warp and two idle ones
-constexpr int RW_MMA_WARP = 8, RW_LOAD_WARP = 9;
+constexpr int RW_THREADS = 384;        // two softmax warpgroups; MMA warp, load warp, two warps that look V over
+constexpr int RW_MMA_WARP = 8, RW_LOAD_WARP = 9, RW_EDGE_WARP = 10;
 // registers a thread: 168 at launch (384 x 168 <= 65,536); 216 x 256 + 72 x 128 = 384 x 168 after the split
 constexpr int RW_REGS_SOFTMAX = 216, RW_REGS_OTHER = 72;
 
@@ -47,9 +47,10 @@ struct RCfg {
     static constexpr int CH = D / 64;                          // 128-byte chunks of a row
     static constexpr int CHUNK = 128 * 128;                    // bytes of a chunk of 128 rows
     static constexpr int TILE = CH * CHUNK;                    // Q tile, K block or V block
-    static constexpr int NST = D == 128 ? 5 : 8;               // ring stages (a K or a V block each)
+    static constexpr int NK = D == 128 ? 2 : 4, NV = D == 128 ? 3 : 4;   // stages of the K ring and of the V ring
     static constexpr int OFF_RING = 2 * TILE;
-    static constexpr int OFF_BAR = OFF_RING + NST * TILE;
+    static constexpr int OFF_V = OFF_RING + NK * TILE;
+    static constexpr int OFF_BAR = OFF_V + NV * TILE;
     static constexpr int BAR_BYTES = 768;                      // barriers, TMEM address, this CTA's rows, spoilt keys
     static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;    // + alignment slack
     static constexpr int S_COL = 0, O_COL = 256;               // TMEM: S of tile t at 128 t, O at 256 + D t
@@ -211,6 +212,7 @@ struct RowTile {
     int tok0;       // first row of the sequence in this CTA
     int n;          // rows of the sequence
     int row0;       // first row of the sequence among the call's T
+    int len;        // its cached tokens, as given
 };
 
 // The sequence and rows of CTA tile `idx` (tiles of tt rows, the sequences' tiles end to end). One warp.
@@ -218,8 +220,9 @@ __device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt
     int before = 0;
     for (int b0 = 0; b0 < P.B; b0 += 32) {
         const int b = b0 + lane;
-        int r0 = 0, n = 0;
+        int r0 = 0, n = 0, len = 0;
         if (b < P.B) {
+            len = P.kv_len[b];
             r0 = P.cu_rows[b];
             n = max(0, P.cu_rows[b + 1] - r0);
         }
@@ -238,11 +241,12 @@ __device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt
             t.tok0 = (idx - before - __shfl_sync(0xffffffffu, inc - nt, w)) * tt;
             t.n = __shfl_sync(0xffffffffu, n, w);
             t.row0 = __shfl_sync(0xffffffffu, r0, w);
+            t.len = __shfl_sync(0xffffffffu, len, w);
             return t;
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    return RowTile{-1, 0, 0, 0};
+    return RowTile{-1, 0, 0, 0, 0};
 }
 
 // Whether the sequences' tiles are more than the grid was made for: some sequence has more rows than max_rows.
@@ -276,13 +280,21 @@ __device__ __forceinline__ Keys keys_of(int p0, int p1, int window, int sinks, i
     return k;
 }
 
-__device__ __forceinline__ uint32_t low_mask(int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u; }
-// which of keys key .. key + 15 position p sees
-__device__ __forceinline__ uint32_t seen16(int key, int p, int window, int sinks) {
-    uint32_t m = low_mask(p + 1 - key);
-    if (window > 0) m &= ~low_mask(p - window + 1 - key) | low_mask(sinks - key);
-    return m;
+// What a row at position p sees of the keys laid end to end: [0, a) and [b, c). (Where the sinks reach past
+// their own boxes, se = ws and the layout is the keys' own order.)
+struct Seen {
+    int a, b, c;
+};
+__device__ __forceinline__ Seen seen_of(const Keys& k, int p, int window, int sinks) {
+    Seen s;
+    s.c = p + 1 - k.ws + k.se;
+    s.b = window > 0 ? max(0, p - window + 1 - k.ws + k.se) : 0;
+    s.a = window > 0 ? min(sinks, p + 1) : 0;
+    return s;
 }
+__device__ __forceinline__ uint32_t low_mask(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+// which of 32 keys from v on
+__device__ __forceinline__ uint32_t seen32(const Seen& s, int v) { return low_mask(s.a - v) | (low_mask(s.c - v) & ~low_mask(s.b - v)); }
 
 __device__ __forceinline__ int page_of(const PagedAttn& P, int b, int key) {
     const int pg = P.table[(int64_t)b * P.max_pages + key / P.page];
@@ -308,6 +320,7 @@ struct Spoilt {
 template <typename T, int D>
 __device__ __noinline__ void add_spoilt(const PagedAttn& P, const Spoilt* sp, int b, int g, int64_t qoff, int p, Keys K, float m, uint32_t o_tm) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(P.Q) + qoff);
+    const Seen seen = seen_of(K, p, P.window, P.sinks);
     for (int c = 0; c < D; c += 32) {
         float o[32];
         ld32(o_tm + c, o);
@@ -315,8 +328,8 @@ __device__ __noinline__ void add_spoilt(const PagedAttn& P, const Spoilt* sp, in
         for (int e = 0; e < sp->n; ++e)
             for (int i = 0; i < RW_BLOCK; ++i) {
                 if (!(sp->e[e].keys[i >> 5] >> (i & 31) & 1)) continue;
-                const int key = K.key(sp->e[e].block * RW_BLOCK + i);
-                if (p < 0 || !(seen16(key & ~15, p, P.window, P.sinks) >> (key & 15) & 1)) continue;
+                const int v0 = sp->e[e].block * RW_BLOCK + i, key = K.key(v0);
+                if (p < 0 || !(v0 < seen.a || (v0 >= seen.b && v0 < seen.c))) continue;
                 const int64_t pg = page_of(P, b, key);
                 const int slot = key % P.page;
                 const int64_t* st = P.kv_stride;
@@ -351,10 +364,18 @@ __device__ __noinline__ void add_spoilt(const PagedAttn& P, const Spoilt* sp, in
     }
 }
 
-// Whether one of the two values of a packed pair is infinite or NaN.
-template <typename T> __device__ __forceinline__ bool not_finite2(uint32_t u) {
-    const uint32_t e = IsBf16<T>::value ? 0x7f80u : 0x7c00u;
-    return (u & e) == e || ((u >> 16) & e) == e;
+// Whether one of 8 packed values is infinite or NaN: then its product with 0 is NaN, and so is the sum.
+template <typename T> __device__ __forceinline__ bool not_finite8(uint4 x);
+template <> __device__ __forceinline__ bool not_finite8<__half>(uint4 x) {
+    const __half2 z = __float2half2_rn(0.f);
+    const __half2 a = __hfma2(u32_as_h2(x.x), z, __hmul2(u32_as_h2(x.y), z)), b = __hfma2(u32_as_h2(x.z), z, __hmul2(u32_as_h2(x.w), z));
+    return (h2_as_u32(__hadd2(a, b)) & 0x7fff7fffu) != 0;
+}
+template <> __device__ __forceinline__ bool not_finite8<__nv_bfloat16>(uint4 x) {
+    const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+    auto v = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    const __nv_bfloat162 s = __hadd2(__hfma2(v(x.x), z, __hmul2(v(x.y), z)), __hfma2(v(x.z), z, __hmul2(v(x.w), z)));
+    return (*reinterpret_cast<const uint32_t*>(&s) & 0x7fff7fffu) != 0;
 }
 
 // Weights of a row's own attention and of the prior in the result, and the LSE of both.
@@ -383,7 +404,8 @@ __device__ __forceinline__ RowEnd row_end(const PagedAttn& P, int64_t row, float
     return r;
 }
 
-__host__ __device__ constexpr int rows_partial_floats(int D) { return D + 4; }   // m, l, -, -, O
+// Partial of a CTA: m [2][128], l [2][128], O [2][D/4][128] float4 (a warp's rows side by side).
+__host__ __device__ constexpr size_t rows_partial_floats(int D) { return (size_t)2 * RW_M * (D + 2); }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_constant__ PagedAttn P) {
@@ -391,9 +413,9 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t s_base = smem_u32(smem);
-    // barriers: Q of each tile, ring full / empty; of each tile: S ready, P ready (4 warps), O += P V done
-    constexpr int B_Q = 0, B_F = 16, B_E = B_F + 8 * C::NST, B_S = B_E + 8 * C::NST, B_P = B_S + 16, B_O = B_P + 16,
-                  B_DR = B_O + 16, N_BAR = B_DR / 8 + 1;
+    // barriers: Q of each tile; K ring full, empty; V ring full, empty, looked over; of each tile: S ready, P ready (4 warps), O += P V done
+    constexpr int B_Q = 0, B_KF = 16, B_KE = B_KF + 8 * C::NK, B_VF = B_KE + 8 * C::NK, B_VE = B_VF + 8 * C::NV,
+                  B_X = B_VE + 8 * C::NV, B_S = B_X + 8 * C::NV, B_P = B_S + 16, B_O = B_P + 16, B_DR = B_O + 16, N_BAR = B_DR / 8 + 1;
     const uint32_t bar = s_base + C::OFF_BAR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * N_BAR);
     RowTile* s_tile = reinterpret_cast<RowTile*>(smem + C::OFF_BAR + 8 * N_BAR + 16);
@@ -408,7 +430,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     const int g = sub % P.H_kv, split = sub / P.H_kv;
 
     if (tid == 0) {
-        for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i >= B_P && 8 * i < B_P + 16) ? 4 : 1);
+        for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i >= B_P && 8 * i < B_P + 16) ? 4 : (8 * i >= B_X && 8 * i < B_S) ? 2 : 1);
         fence_mbar_init();
         s_spoilt->any = s_spoilt->n = 0;
     }
@@ -437,7 +459,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
 
     if (rt.b >= 0) {
         const int b = rt.b;
-        int len = P.kv_len[b];
+        int len = rt.len;
         if (len > (int64_t)P.max_pages * P.page) {
             if (tid == 0) set_err(P.err, ERR_KV_LEN);
             len = P.max_pages * P.page;
@@ -475,26 +497,30 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                         }
                     };
                     locate(0);
-                    int i = 0;
-                    for (; i < 2 * nb; ++i) {   // K(0), V(0), K(1), V(1), ...
-                        const int j = i >> 1, st = i % C::NST, nk = keys_in(j);
-                        if (i >= C::NST && !__all_sync(0xffffffffu, wait_bar(bar + B_E + 8 * st, (i / C::NST - 1) & 1))) {
-                            failed = true;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(bar + B_F + 8 * st, nk * D * 2);
+                    auto load = [&](int j, const CUtensorMap* tm, int full, int empty, int off, int n) -> bool {
+                        const int st = j % n, nk = keys_in(j);
+                        if (j >= n && !__all_sync(0xffffffffu, wait_bar(bar + empty + 8 * st, (j / n - 1) & 1))) return false;
+                        if (lane == 0) mbar_arrive_expect_tx(bar + full + 8 * st, nk * D * 2);
                         __syncwarp();
                         if (lane * box < nk) {
-                            const uint32_t dst = s_base + C::OFF_RING + st * C::TILE + lane * box * 128;
-                            for (int c = 0; c < C::CH; ++c)
-                                tma5(dst + c * C::CHUNK, (i & 1) ? &P.tm_v : &P.tm_k, 0, tok, c, g, pg, bar + B_F + 8 * st);
+                            const uint32_t dst = s_base + off + st * C::TILE + lane * box * 128;
+                            for (int c = 0; c < C::CH; ++c) tma5(dst + c * C::CHUNK, tm, 0, tok, c, g, pg, bar + full + 8 * st);
                         }
-                        if ((i & 1) && j + 1 < nb) locate(j + 1);
+                        return true;
+                    };
+                    int jk = 0, jv = 0;      // blocks whose K, V were issued
+                    for (; jv < nb; ++jv) {
+                        if (!load(jk, &P.tm_k, B_KF, B_KE, C::OFF_RING, C::NK)) break;
+                        ++jk;
+                        if (!load(jv, &P.tm_v, B_VF, B_VE, C::OFF_V, C::NV)) break;
+                        if (jv + 1 < nb) locate(jv + 1);
                     }
-                    if (failed && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
+                    if (jv < nb && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
                     // the copies in flight land before the CTA can end, whatever the other warps do
-                    for (int q = max(0, i - C::NST); q < i; ++q)
-                        if (!__all_sync(0xffffffffu, wait_bar(bar + B_F + 8 * (q % C::NST), (q / C::NST) & 1))) break;
+                    for (int j = max(0, jk - C::NK); j < jk; ++j)
+                        if (!__all_sync(0xffffffffu, wait_bar(bar + B_KF + 8 * (j % C::NK), (j / C::NK) & 1))) break;
+                    for (int j = max(0, jv - C::NV); j < jv; ++j)
+                        if (!__all_sync(0xffffffffu, wait_bar(bar + B_VF + 8 * (j % C::NV), (j / C::NV) & 1))) break;
                 }
             } else if (warp == RW_MMA_WARP) {
                 // ------------------------------------------------------------ MMAs
@@ -506,23 +532,23 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 constexpr uint32_t ID_PV = idesc_16(FMT, D, 1), ID_S = idesc_16(FMT, RW_BLOCK, 0);
                 const uint64_t q_desc = desc_sw128(s_base, 16);
                 const uint64_t k_desc = desc_sw128(s_base + C::OFF_RING, 16);
-                const uint64_t v_desc = desc_sw128(s_base + C::OFF_RING, C::CHUNK);
+                const uint64_t v_desc = desc_sw128(s_base + C::OFF_V, C::CHUNK);
                 auto wait = [&](int off, int phase) {
                     if (!failed && !__all_sync(0xffffffffu, wait_bar(bar + off, phase & 1))) failed = true;
                     return !failed;
                 };
                 auto issue_S = [&](int t, int j) {   // S_t = Q_t K(j)^T
-                    const int st = (2 * j) % C::NST;
+                    const int st = j % C::NK;
                     const uint32_t id = j + 1 < nbu ? ID_S : idesc_16(FMT, nk_last, 0);
                     const uint64_t qd = q_desc + static_cast<uint64_t>((t * C::TILE) >> 4), kd = k_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
 #pragma unroll
                     for (int c = 0; c < C::CH; ++c)
                         mma_ss4(tm + C::S_COL + 128 * t, qd + c * (C::CHUNK >> 4), kd + c * (C::CHUNK >> 4), id, c > 0);
                     commit(bar + B_S + 8 * t);
-                    if (t == ntu - 1) commit(bar + B_E + 8 * st);
+                    if (t == ntu - 1) commit(bar + B_KE + 8 * st);
                 };
                 auto issue_PV = [&](int t, int j) {  // O_t += P_t V(j)
-                    const int st = (2 * j + 1) % C::NST;
+                    const int st = j % C::NV;
                     const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::TILE) >> 4);
                     const uint32_t d = tm + C::O_COL + D * t, a = tm + C::S_COL + 128 * t;
                     if (j + 1 < nbu || nk_last == RW_BLOCK) {
@@ -532,18 +558,17 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                             mma_ts(d, a + 8 * u, vd + static_cast<uint64_t>(u * (2048 >> 4)), ID_PV, j > 0 || u > 0);
                     }
                     commit(bar + B_O + 8 * t);
-                    if (t == ntu - 1) commit(bar + B_E + 8 * st);
+                    if (t == ntu - 1) commit(bar + B_VE + 8 * st);
                 };
-                if (nbu > 0 && wait(B_F, 0)) {
+                if (nbu > 0 && wait(B_KF, 0)) {
                     for (int t = 0; t < ntu; ++t)
                         if (wait(B_Q + 8 * t, 0)) issue_S(t, 0);
                     for (int j = 0; j < nbu && !failed; ++j) {
-                        const int iv = 2 * j + 1, ik = 2 * j + 2;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (t >= ntu) break;
-                            if (t == 0 && !(wait(B_F + 8 * (iv % C::NST), iv / C::NST) &&
-                                            (j + 1 == nbu || wait(B_F + 8 * (ik % C::NST), ik / C::NST)))) break;
+                            if (t == 0 && !(wait(B_VF + 8 * (j % C::NV), j / C::NV) && wait(B_X + 8 * (j % C::NV), j / C::NV) &&
+                                            (j + 1 == nbu || wait(B_KF + 8 * ((j + 1) % C::NK), (j + 1) / C::NK)))) break;
                             if (!wait(B_P + 8 * t, j)) break;
                             fence_after();
                             issue_PV(t, j);
@@ -554,6 +579,66 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 if (failed && lane == 0) set_err(P.err, ERR_ROWS_MMA);
                 commit(bar + B_DR);      // no MMA writes TMEM any more when the CTA gives it back
                 __all_sync(0xffffffffu, wait_bar(bar + B_DR, 0));
+            } else {
+                // -------------------------------------------------------- V blocks looked over (the two warps left)
+                // Where a block is partly hidden from the CTA's rows, V rows that none of them sees are cleared (they
+                // may hold anything), and so are those that are not finite, which are put on record. A warp takes 64 V
+                // rows, 8 lanes of 16 bytes a row and chunk. Other blocks are passed on as they are.
+                const int w = warp - RW_EDGE_WARP;
+                int n_edge = 0;
+                for (int j = 0; j < nb && !failed; ++j) {
+                    const int st = j % C::NV, v0 = (j0 + j) * RW_BLOCK, nk = keys_in(j);
+                    const int ka = K.key(v0), kz = K.key(v0 + nk - 1);
+                    if (!__all_sync(0xffffffffu, wait_bar(bar + B_VF + 8 * st, (j / C::NV) & 1))) {
+                        failed = true;
+                        break;
+                    }
+                    if (kz > p0 || kz - ka != nk - 1 || (P.window > 0 && ka <= p1 - P.window && kz >= P.sinks)) {
+                        bool cleared = false;
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = 64 * w + 32 * h + lane, key = K.key(v0 + r);
+                            const uint32_t clear = __ballot_sync(0xffffffffu, r < nk && (key > p1 || (P.window > 0 && key <= p0 - P.window && key >= P.sinks)));
+                            const uint32_t live = __ballot_sync(0xffffffffu, r < nk) & ~clear;
+                            uint8_t* rows = smem + C::OFF_V + st * C::TILE + (64 * w + 32 * h) * 128 + lane * 16;
+                            uint32_t spoilt = 0;
+                            if (live && n_edge < RW_MAX_EDGE) {
+                                uint32_t bad = 0;          // bit i: this lane's piece of row 4 i + lane / 8
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                                    for (int c = 0; c < C::CH; ++c)
+                                        bad |= static_cast<uint32_t>(not_finite8<T>(*reinterpret_cast<const uint4*>(rows + c * C::CHUNK + i * 512))) << i;
+                                if (__any_sync(0xffffffffu, bad)) {
+                                    for (int i = 0; i < 8; ++i) {
+                                        const uint32_t f = __ballot_sync(0xffffffffu, bad >> i & 1);
+                                        for (int q = 0; q < 4; ++q) spoilt |= (f >> (8 * q) & 0xffu ? 1u : 0u) << (4 * i + q);
+                                    }
+                                    spoilt &= live;
+                                }
+                            }
+                            if (n_edge < RW_MAX_EDGE && lane == 0) {
+                                s_spoilt->e[n_edge].block = j0 + j;
+                                s_spoilt->e[n_edge].keys[2 * w + h] = spoilt;
+                                s_spoilt->n = n_edge + 1;
+                                if (spoilt) s_spoilt->any = 1;
+                            }
+                            if (clear | spoilt) {
+                                for (int i = 0; i < 8; ++i)
+                                    if ((clear | spoilt) >> (4 * i + (lane >> 3)) & 1)
+                                        for (int c = 0; c < C::CH; ++c) *reinterpret_cast<uint4*>(rows + c * C::CHUNK + i * 512) = make_uint4(0, 0, 0, 0);
+                                cleared = true;
+                            }
+                        }
+                        if (n_edge < RW_MAX_EDGE) ++n_edge;
+                        if (cleared) fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(bar + B_X + 8 * st);
+                }
+                if (failed && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
+                // the record is complete, for either tile
+                asm volatile("barrier.cta.arrive 1, 192;" ::: "memory");
+                if (ntile == 2) asm volatile("barrier.cta.arrive 2, 192;" ::: "memory");
             }
         } else {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RW_REGS_SOFTMAX));
@@ -569,60 +654,31 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
                 const uint32_t s_tm = tmem + C::S_COL + 128 * t + lane_base, o_tm = tmem + C::O_COL + D * t + lane_base;
                 const float sc = P.scale_log2;
+                const Seen seen = seen_of(K, p, P.window, P.sinks);
                 float m = -INFINITY, l = 0.f;
-                int n_edge = 0;
                 // A wait that runs out only marks the warp: it goes on, without work, to the barrier at the end.
                 for (int j = 0; j < nb; ++j) {
                     const int v0 = (j0 + j) * RW_BLOCK, nk = keys_in(j);
                     const int ka = K.key(v0), kz = K.key(v0 + nk - 1);
-                    // Partly hidden from the CTA's rows: V rows that none of them sees are cleared (they may hold
-                    // anything), and so are those that are not finite, which are put on record. Thread r: row r.
-                    if (t == 0 && (kz > p0 || kz - ka != nk - 1 || (P.window > 0 && ka <= p1 - P.window && kz >= P.sinks))) {
-                        const int st = (2 * j + 1) % C::NST;
-                        if (!failed && !wait_bar(bar + B_F + 8 * st, ((2 * j + 1) / C::NST) & 1)) failed = true;
-                        const int key = K.key(v0 + r);
-                        bool clear = false, spoilt = false;
-                        uint4* row = reinterpret_cast<uint4*>(smem + C::OFF_RING + st * C::TILE + r * 128);
-                        if (!failed && r < nk) {
-                            clear = key > p1 || (P.window > 0 && key <= p0 - P.window && key >= P.sinks);
-                            if (!clear && n_edge < RW_MAX_EDGE) {
-                                for (int c = 0; c < C::CH; ++c)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const uint4 x = row[c * (C::CHUNK / 16) + i];
-                                        spoilt |= not_finite2<T>(x.x) | not_finite2<T>(x.y) | not_finite2<T>(x.z) | not_finite2<T>(x.w);
-                                    }
-                            }
-                            if (clear || spoilt)
-                                for (int c = 0; c < C::CH; ++c)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) row[c * (C::CHUNK / 16) + i] = make_uint4(0, 0, 0, 0);
-                        }
-                        const uint32_t bits = __ballot_sync(0xffffffffu, spoilt);
-                        if (n_edge < RW_MAX_EDGE) {
-                            if (lane == 0) {
-                                s_spoilt->e[n_edge].block = j0 + j;
-                                s_spoilt->e[n_edge].keys[warp] = bits;
-                                s_spoilt->n = n_edge + 1;
-                                if (bits) s_spoilt->any = 1;
-                            }
-                            ++n_edge;
-                        }
-                        fence_proxy_async_smem();
-                    }
                     if (!__all_sync(0xffffffffu, !failed && wait_bar(bar + B_S + 8 * t, j & 1))) failed = true;
                     fence_after();
                     // every row of the tile sees the whole block, or masks: 16 keys at a time
                     const bool full = nk == RW_BLOCK && kz - ka == RW_BLOCK - 1 && kz <= pa &&
                                       (P.window <= 0 || ka > pz - P.window || kz < P.sinks);
-                    auto mask = [&](int c, float* x) {      // keys 32 c .. of the block
+                    // per 32 keys: bits of those the row sees; and whether the warp's rows see all of them, or none
+                    uint32_t see[RW_BLOCK / 32];
+                    uint32_t part = 0, none = 0;
+                    if (!full) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int v = 32 * c + 16 * h;
-                            const uint32_t see = v < nk ? seen16(K.key(v0 + v), p, P.window, P.sinks) : 0u;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x[16 * h + i] = see >> i & 1 ? x[16 * h + i] : -INFINITY;
+                        for (int c = 0; c < RW_BLOCK / 32; ++c) {
+                            see[c] = seen32(seen, v0 + 32 * c);
+                            if (__all_sync(0xffffffffu, see[c] == 0)) none |= 1u << c;
+                            else if (!__all_sync(0xffffffffu, see[c] == ~0u || !row_ok)) part |= 1u << c;
                         }
+                    }
+                    auto mask = [&](int c, float* x) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = see[c] & (1u << i) ? x[i] : -INFINITY;
                     };
                     // p = 2^(s - m) at the running maximum, packed, and their sum
                     uint32_t pk[RW_BLOCK / 2];
@@ -638,15 +694,20 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                         for (int c = 0; c < RW_BLOCK / 32; ++c) {   // the next chunk's load runs under this one's arithmetic
                             if (c + 1 < RW_BLOCK / 32) ld32(s_tm + 32 * (c + 1), x[(c + 1) & 1]);
                             float* y = x[c & 1];
-                            if (masked) mask(c, y);
+                            if (masked && (none >> c & 1)) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float x0, x1;
-                                f2_unpack(f2_fma(f2_pack(y[2 * i], y[2 * i + 1]), sc2, nm2), x0, x1);
-                                x0 = ex2_approx(x0);
-                                x1 = ex2_approx(x1);
-                                acc[i & 1] = f2_add(acc[i & 1], f2_pack(x0, x1));
-                                pk[16 * c + i] = pack16<T>(x0, x1);
+                                for (int i = 0; i < 16; ++i) pk[16 * c + i] = 0;
+                            } else {
+                                if (masked && (part >> c & 1)) mask(c, y);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float x0, x1;
+                                    f2_unpack(f2_fma(f2_pack(y[2 * i], y[2 * i + 1]), sc2, nm2), x0, x1);
+                                    x0 = ex2_approx(x0);
+                                    x1 = ex2_approx(x1);
+                                    acc[i & 1] = f2_add(acc[i & 1], f2_pack(x0, x1));
+                                    pk[16 * c + i] = pack16<T>(x0, x1);
+                                }
                             }
                             if (c + 1 < RW_BLOCK / 32) wait_ld();
                         }
@@ -669,14 +730,20 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     if (again) {
                         float bm = -INFINITY;
                         if (!failed) {
-#pragma unroll 1
+#pragma unroll
                             for (int c = 0; c < RW_BLOCK / 32; ++c) {
+                                if (none >> c & 1) continue;
                                 float x[32];
                                 ld32(s_tm + 32 * c, x);
                                 wait_ld();
-                                if (!full) mask(c, x);
+                                if (part >> c & 1) mask(c, x);
+                                float b0 = fmaxf(x[0], x[1]), b1 = fmaxf(x[2], x[3]);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) bm = fmaxf(bm, x[i]);
+                                for (int i = 4; i < 32; i += 4) {
+                                    b0 = fmaxf(b0, fmaxf(x[i], x[i + 1]));
+                                    b1 = fmaxf(b1, fmaxf(x[i + 2], x[i + 3]));
+                                }
+                                bm = fmaxf(bm, fmaxf(b0, b1));
                             }
                         }
                         const float mn = fmaxf(m, bm * sc);
@@ -720,38 +787,36 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     set_err(P.err, ERR_ROWS_SOFTMAX);
                 }
                 fence_after();
-                asm volatile("barrier.cta.sync 1, %0;" ::"r"(128 * ntile) : "memory");   // the record of spoilt keys is complete
+                // the record of spoilt keys is complete
+                asm volatile("barrier.cta.sync %0, 192;" ::"r"(1 + t) : "memory");
                 if (!failed) {
                     const int64_t trow = rt.row0 + rt.tok0 + rtok;
-                    const int64_t row = trow * P.H_q + hq;
+                    const int row = static_cast<int>(trow * P.H_q + hq);      // (T H_q < 2^27)
                     const bool direct = P.n_split == 1;
                     RowEnd e = {1.f, 0.f, 0.f, false};
                     if (direct && row_ok) e = row_end(P, row, m, l);
-                    float* part = P.ws + ((size_t)((size_t)tile_idx * per_tile + sub) * (2 * RW_M) + t * RW_M + r) * rows_partial_floats(D);
+                    float* part = P.ws + ((size_t)tile_idx * per_tile + sub) * rows_partial_floats(D);
+                    // the warp's 32 result rows, staged over the tile's Q (which no MMA reads any more)
+                    uint8_t* stage = smem + t * C::TILE + (warp & 3) * 32 * (D * 2);
                     if (nb > 0 && s_spoilt->any)
                         add_spoilt<T, D>(P, s_spoilt, b, g, trow * P.q_row + (int64_t)hq * P.q_head, p, K, m, o_tm);
-#pragma unroll 1
+#pragma unroll 2
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
                         if (nb > 0) {
                             ld32(o_tm + c, o);
                             wait_ld();
-                        } else {
-    #pragma unroll
+                        }
+                        if (l == 0.f) {     // nothing seen (and O unwritten where the CTA has no keys)
+#pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = 0.f;
                         }
-                        if (!row_ok) continue;
                         if (direct) {
-                            if (l == 0.f) {
-    #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                            }
-                            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.O) + row * D + c);
-                            const float4* pr = reinterpret_cast<const float4*>(P.O_prior + row * D + c);
-    #pragma unroll
+                            const float4* pr = reinterpret_cast<const float4*>(P.O_prior + (int64_t)row * D + c);
+#pragma unroll
                             for (int i = 0; i < 32; i += 8) {
                                 float x[8];
-    #pragma unroll
+#pragma unroll
                                 for (int q = 0; q < 8; ++q) x[q] = o[i + q] * e.wo;
                                 if (e.prior) {
                                     const float4 a = pr[i / 4], c4 = pr[i / 4 + 1];
@@ -760,22 +825,33 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                                     x[4] = fmaf(c4.x, e.wp, x[4]); x[5] = fmaf(c4.y, e.wp, x[5]);
                                     x[6] = fmaf(c4.z, e.wp, x[6]); x[7] = fmaf(c4.w, e.wp, x[7]);
                                 }
-                                dst[i / 8] = make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]), pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
+                                *reinterpret_cast<uint4*>(stage + lane * (D * 2) + (((c + i) / 8 ^ lane) & (D / 8 - 1)) * 16) =
+                                    make_uint4(pack16<T>(x[0], x[1]), pack16<T>(x[2], x[3]), pack16<T>(x[4], x[5]), pack16<T>(x[6], x[7]));
                             }
-                        } else {
-    #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4*>(part + 4 + c + i) = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                                                      : make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        } else {   // [D/4][128 rows] float4
+                            float4* po = reinterpret_cast<float4*>(part + 4 * RW_M) + ((size_t)t * (D / 4) + c / 4) * RW_M + r;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) po[(i / 4) * RW_M] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                         }
                     }
-                    if (row_ok) {
-                        if (direct) {
-                            if (P.LSE) P.LSE[row] = e.lse;
-                        } else {
-                            part[0] = m;
-                            part[1] = l;
+                    if (direct) {
+                        // whole rows out, 512 contiguous bytes of neighbouring heads an instruction
+                        __syncwarp();
+                        constexpr int CR = D / 8, RPI = 32 / CR;      // 16-byte pieces a row, rows an instruction
+                        const uint32_t ok = __ballot_sync(0xffffffffu, row_ok);
+                        const int piece = lane & (CR - 1);
+#pragma unroll
+                        for (int i = 0; i < 32; i += RPI) {
+                            const int rr = i + lane / CR;
+                            const int64_t dst = __shfl_sync(0xffffffffu, row, rr);   // (widened)
+                            if (ok >> rr & 1)
+                                *reinterpret_cast<uint4*>(static_cast<T*>(P.O) + dst * D + piece * 8) =
+                                    *reinterpret_cast<const uint4*>(stage + rr * (D * 2) + ((piece ^ rr) & (CR - 1)) * 16);
                         }
+                        if (row_ok && P.LSE) P.LSE[row] = e.lse;
+                    } else {
+                        part[t * RW_M + r] = m;
+                        part[2 * RW_M + t * RW_M + r] = l;
                     }
                 }
             }
@@ -788,60 +864,60 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
-// Joins the n_split partials of each row: a warp per row, lanes over D (a float4 each).
+// Joins the n_split partials: a CTA per tile of 128 rows and 32 columns, a thread per row.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_rows_join_kernel(const __grid_constant__ PagedAttn P) {
-    constexpr int LP = D / 4;
+__global__ void __launch_bounds__(RW_M) paged_rows_join_kernel(const __grid_constant__ PagedAttn P) {
     pdl_wait();
     pdl_release();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, r = threadIdx.x;
     const int tpt = RW_M / P.G, tt = 2 * tpt;
     const int tile_idx = blockIdx.x / P.H_kv, g = blockIdx.x % P.H_kv;
+    const int t = blockIdx.y & 1, c0 = (blockIdx.y >> 1) * 32;
     const RowTile rt = find_tile(P, tile_idx, tt, lane);
     if (rt.b < 0) return;
-    const int rows_here = min(rt.n - rt.tok0, tt);
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 2 * RW_M; r += gridDim.y * 8) {
-        const int t = r / RW_M, rr = r % RW_M;
-        const int rtok = t * tpt + rr / P.G;
-        if (rr >= tpt * P.G || rtok >= rows_here) continue;
-        const int64_t trow = rt.row0 + rt.tok0 + rtok;
-        if (trow < 0 || trow >= P.T) continue;
-        const int64_t row = trow * P.H_q + g * P.G + rr % P.G;
-        auto part = [&](int s) {
-            return P.ws + ((size_t)((size_t)tile_idx * P.H_kv * P.n_split + s * P.H_kv + g) * (2 * RW_M) + r) * rows_partial_floats(D);
-        };
-        float M = -INFINITY;
-        for (int s = lane; s < P.n_split; s += 32) M = fmaxf(M, part(s)[0]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int rtok = t * tpt + r / P.G;
+    const int64_t trow = rt.row0 + rt.tok0 + rtok;
+    if (r >= tpt * P.G || rtok >= min(rt.n - rt.tok0, tt) || trow < 0 || trow >= P.T) return;
+    const int64_t row = trow * P.H_q + g * P.G + r % P.G;
+    auto part = [&](int s) { return P.ws + ((size_t)tile_idx * P.H_kv * P.n_split + (size_t)s * P.H_kv + g) * rows_partial_floats(D); };
+    float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-        for (int s = 0; s < P.n_split; ++s) {
-            const float* p = part(s);
-            const float2 ml = *reinterpret_cast<const float2*>(p);
-            const float w = ml.x > -INFINITY ? ex2_approx(ml.x - M) : 1.f;   // (a part without keys holds zeros)
-            L = fmaf(w, ml.y, L);
-            if (lane < LP) {
-                const float4 v = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
-                acc.x = fmaf(w, v.x, acc.x);
-                acc.y = fmaf(w, v.y, acc.y);
-                acc.z = fmaf(w, v.z, acc.z);
-                acc.w = fmaf(w, v.w, acc.w);
-            }
+    for (int s = 0; s < P.n_split; ++s) M = fmaxf(M, part(s)[t * RW_M + r]);
+    float4 acc[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int s = 0; s < P.n_split; ++s) {
+        const float* p = part(s);
+        const float m = p[t * RW_M + r];
+        const float w = m > -INFINITY ? ex2_approx(m - M) : 1.f;   // (a part without keys holds zeros)
+        L = fmaf(w, p[2 * RW_M + t * RW_M + r], L);
+        const float4* po = reinterpret_cast<const float4*>(p + 4 * RW_M) + ((size_t)t * (D / 4) + c0 / 4) * RW_M + r;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float4 v = po[c * RW_M];
+            acc[c].x = fmaf(w, v.x, acc[c].x);
+            acc[c].y = fmaf(w, v.y, acc[c].y);
+            acc[c].z = fmaf(w, v.z, acc[c].z);
+            acc[c].w = fmaf(w, v.w, acc[c].w);
         }
-        const RowEnd e = row_end(P, row, M, L);
-        if (lane < LP) {
-            float4 x = make_float4(acc.x * e.wo, acc.y * e.wo, acc.z * e.wo, acc.w * e.wo);
-            if (e.prior) {
-                const float4 a = *reinterpret_cast<const float4*>(P.O_prior + row * D + 4 * lane);
-                x.x = fmaf(a.x, e.wp, x.x); x.y = fmaf(a.y, e.wp, x.y);
-                x.z = fmaf(a.z, e.wp, x.z); x.w = fmaf(a.w, e.wp, x.w);
-            }
-            *reinterpret_cast<uint2*>(static_cast<T*>(P.O) + row * D + 4 * lane) = make_uint2(pack16<T>(x.x, x.y), pack16<T>(x.z, x.w));
-        }
-        if (lane == 0 && P.LSE) P.LSE[row] = e.lse;
     }
+    const RowEnd e = row_end(P, row, M, L);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.O) + row * D + c0);
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+        float4 x = acc[c], y = acc[c + 1];
+        x = make_float4(x.x * e.wo, x.y * e.wo, x.z * e.wo, x.w * e.wo);
+        y = make_float4(y.x * e.wo, y.y * e.wo, y.z * e.wo, y.w * e.wo);
+        if (e.prior) {
+            const float4* pr = reinterpret_cast<const float4*>(P.O_prior + row * D + c0 + 4 * c);
+            const float4 a = pr[0], b = pr[1];
+            x.x = fmaf(a.x, e.wp, x.x); x.y = fmaf(a.y, e.wp, x.y); x.z = fmaf(a.z, e.wp, x.z); x.w = fmaf(a.w, e.wp, x.w);
+            y.x = fmaf(b.x, e.wp, y.x); y.y = fmaf(b.y, e.wp, y.y); y.z = fmaf(b.z, e.wp, y.z); y.w = fmaf(b.w, e.wp, y.w);
+        }
+        dst[c / 2] = make_uint4(pack16<T>(x.x, x.y), pack16<T>(x.z, x.w), pack16<T>(y.x, y.y), pack16<T>(y.z, y.w));
+    }
+    if (c0 == 0 && P.LSE) P.LSE[row] = e.lse;
 }
 
 template <typename T, int D>
@@ -862,8 +938,8 @@ cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, D>, p);
     if (e != cudaSuccess || p.n_split == 1) return e;
-    cfg.gridDim = dim3(p.row_tiles * p.H_kv, 8);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(p.row_tiles * p.H_kv, 2 * (D / 32));
+    cfg.blockDim = dim3(RW_M);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, paged_rows_join_kernel<T, D>, p);
 }
@@ -895,7 +971,7 @@ size_t paged_rows_plan(PagedAttn& p, int D, int sms) {
     const int64_t most = bound / (4 * RW_BLOCK);
     if (ns > most) ns = most;
     p.n_split = ns < 1 ? 1 : static_cast<int>(ns);
-    return p.n_split == 1 ? 0 : (size_t)p.row_tiles * p.H_kv * p.n_split * 2 * RW_M * rows_partial_floats(D) * sizeof(float);
+    return p.n_split == 1 ? 0 : (size_t)p.row_tiles * p.H_kv * p.n_split * rows_partial_floats(D) * sizeof(float);
 }
 
 cudaError_t launch_paged_rows(PagedAttn& p, int D, cudaStream_t st) {
