@@ -82,7 +82,7 @@ struct PagedAttn {
     int* err;
     // one-token kernel
     int heads_per_group, n_groups;   // q heads of a kv head that share a work item, and items per kv head
-    int split;                       // 1: equal ranges of tiles over the CTAs, joined by a second kernel
+    int mode;                        // how the call is cut
     int n_ctas;
     // row kernel
     int n_split, row_tiles, box;     // key splits, row tiles of the grid, tokens of a TMA box

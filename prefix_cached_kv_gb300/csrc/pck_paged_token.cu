@@ -9,30 +9,39 @@
 // bounds it and the kernel's business is to keep loads in flight on every SM whatever the lengths:
 //  * A unit is a cache tile of 16 tokens of one kv head (a page is a multiple of 16, so a unit never
 //    leaves its page). The units of all items (sequence, kv head, group of q heads) laid end to end
-//    are cut into equal ranges, one per CTA, from the lengths on the device (one block scan per
-//    CTA), so a ragged batch, one long sequence and many short ones all load every SM evenly, and
-//    a captured graph follows the lengths it finds.
-//  * One CTA per SM; each warp streams every NW-th unit of the range through a ring of its own
-//    (two TMA tile loads a unit, 128-byte swizzle, evict-first: read once). Lane i of a warp
-//    resolves the i-th of its next 32 units (sequence, tile, page number) at once, so page-table
-//    latency is paid once in 32 units and off the critical path; rings run on across items.
+//    are cut into equal ranges from the lengths on the device (one block scan per CTA), so a ragged
+//    batch, one long sequence and many short ones all load every SM evenly, and a captured graph
+//    follows the lengths it finds. Few items (at most TK_FEW_ITEMS per SM): a range per CTA, whose warps
+//    take every NW-th unit and join through shared memory; neighbouring warps then read neighbouring
+//    tiles, and an item has few pieces. Many: a range per warp, because a change of item (its q, its end)
+//    then stalls one of the SM's eight streams and not all of them.
+//  * One CTA per SM; each warp streams its units through a ring of its own (two TMA tile loads a unit,
+//    128-byte swizzle, evict-first: read once). Lane i of a warp resolves the i-th of its next 32 units
+//    (sequence, tile, page number) at once, so page-table latency is paid once in 32 units and off the
+//    critical path; rings run on across items.
 //  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads as columns; the running
 //    maximum moves only when a score passes it by 8 (log2), so every p <= 2^8; p goes into
 //    O^T += V^T p^T as a 16-bit hi + lo pair (two MMAs into one accumulator), which keeps ~22 bits
 //    (16 for bf16) of p: the result's own rounding is then the only visible one, and these MMAs are
 //    hidden behind the loads.
-//  * At the end of an item the CTA's warps join through shared memory. An item that lies within
-//    one CTA's range is finished there; one that crosses CTAs leaves a partial [m, l, O] per CTA,
-//    at most two per CTA, and a second, programmatically launched kernel joins them.
-//  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA of its own and
-//    nothing is joined: one launch.
+//  * An item that lies within one range is finished there; one that crosses ranges leaves a partial [m, l, O]
+//    per range, at most two per range, and a second, programmatically launched kernel joins them.
+//  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA whose warps take its
+//    units in turn and join through shared memory: one launch.
 #include "pck_paged.cuh"
 
 namespace pck {
 namespace {
 
 constexpr int TK_DIRECT_UNITS = 32;    // 512 tokens
-constexpr int TK_MIN_UNITS = 16;       // units per CTA at least, when ranges are cut
+constexpr int TK_FEW_ITEMS = 2;        // items per SM up to which a range is a CTA's
+// How a call is cut.
+enum { TK_ITEM, TK_CTA, TK_WARP };     // an item per CTA; ranges per CTA; ranges per warp
+// Units per range at least (two per warp, or what a warp's start is worth).
+__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_CTA ? 16 : 8; }
+// What an item costs beside its units (its q, its end), in units: ranges are cut by units + this per item, so that a
+// range of many short items does not take long after the others.
+__host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_CTA ? 24 : 16; }
 constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
 
 template <int D>
@@ -59,6 +68,7 @@ template <> struct Elem<__half> {
     }
     static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) { split_hi_lo(x0, x1, hi, lo); }
     static __device__ __forceinline__ uint32_t pack(float x0, float x1) { return h2_as_u32(__floats2half2_rn(x0, x1)); }
+    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
 };
 template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -72,6 +82,7 @@ template <> struct Elem<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
     static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
         hi = pack(x0, x1);
         lo = pack(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
@@ -126,41 +137,58 @@ __device__ __forceinline__ int clamp_len(const PagedAttn& P, int b, bool report)
 // NaN, from a NaN score), which weight 1 passes on.
 __device__ __forceinline__ float join_weight(float m, float M) { return m > -INFINITY ? ex2_approx(m - M) : 1.f; }
 
-// Writes row (t, hq): O = acc / l merged with the prior, and the LSE. Called by each thread for its
-// elements d, d + 1; `first` also writes the LSE.
+// Weights of a row's own attention and of the prior in the result, and the LSE of both.
+struct RowEnd {
+    float wo, wp, lse;
+    bool prior;
+};
+__device__ __forceinline__ RowEnd row_end(const PagedAttn& P, int64_t row, float m, float l) {
+    RowEnd r;
+    const bool none = l == 0.f;
+    r.wo = none ? 0.f : 1.0f / l;
+    r.wp = 0.f;
+    r.lse = none ? -INFINITY : (m + log2f(l)) * PG_LN2;
+    r.prior = false;
+    if (P.O_prior) {
+        const float lp = P.LSE_prior[row];
+        if (lp != -INFINITY) {
+            const float mx = fmaxf(r.lse, lp);
+            const float wn = expf(r.lse - mx), wp = expf(lp - mx), sum = wn + wp;
+            r.wo *= wn / sum;
+            r.wp = wp / sum;
+            r.lse = mx + logf(sum);
+            r.prior = true;
+        }
+    }
+    return r;
+}
+
+// Elements d, d + 1 of row (t, hq), and (first) its LSE.
 template <typename T>
 __device__ __forceinline__ void finish2(const PagedAttn& P, int t, int hq, int D, int d, float a0, float a1, float m, float l,
                                         bool first) {
     const int64_t row = (int64_t)t * P.H_q + hq;
-    const bool none = l == 0.f;
-    const float inv = none ? 0.f : 1.0f / l;
-    float lse = none ? -INFINITY : (m + log2f(l)) * PG_LN2;
-    a0 *= inv;
-    a1 *= inv;
-    if (P.O_prior) {
-        const float lp = P.LSE_prior[row];
-        if (lp != -INFINITY) {
-            const float mx = fmaxf(lse, lp);
-            const float wn = expf(lse - mx), wp = expf(lp - mx), sum = wn + wp;
-            const float2 op = *reinterpret_cast<const float2*>(P.O_prior + row * D + d);
-            a0 = none ? op.x : (a0 * wn + op.x * wp) / sum;
-            a1 = none ? op.y : (a1 * wn + op.y * wp) / sum;
-            lse = mx + logf(sum);
-        }
+    const RowEnd r = row_end(P, row, m, l);
+    a0 *= r.wo;
+    a1 *= r.wo;
+    if (r.prior) {
+        const float2 op = *reinterpret_cast<const float2*>(P.O_prior + row * D + d);
+        a0 = fmaf(op.x, r.wp, a0);
+        a1 = fmaf(op.y, r.wp, a1);
     }
     *reinterpret_cast<uint32_t*>(static_cast<T*>(P.O) + row * D + d) = Elem<T>::pack(a0, a1);
-    if (first && P.LSE) P.LSE[row] = lse;
+    if (first && P.LSE) P.LSE[row] = r.lse;
 }
 
-// Partial of a CTA (two slots per CTA): [heads][D + 4] floats: m, l, -, -, O (not normalised).
+// Partial of a range (two slots per range): [heads][D + 4] floats: m, l, -, -, O (not normalised).
 __host__ __device__ constexpr int slot_floats(int D, int heads) { return heads * (D + 4); }
 
-// A split item's descriptor, written by the CTA in which it begins (pieces = 0: none).
+// A split item's descriptor, written by the range in which it begins (pieces = 0: none).
 struct JoinDesc {
     int b, x, pieces, pad;
 };
 
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, int MODE>
 __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const __grid_constant__ PagedAttn P) {
     using C = TCfg<D>;
     constexpr int NW = C::NW, ST = C::ST, KS = D / 16, NT = NW * 32;
@@ -184,14 +212,19 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
     pdl_wait();
     pdl_release();
 
-    // ---- this CTA's range of units
+    // ---- the range of units of this warp (BY_WARP) or CTA
     const int Hg = P.H_kv * P.n_groups;
     const int B = P.B;
+    const int heads = P.heads_per_group;
+    constexpr bool SPLIT = MODE != TK_ITEM, BY_WARP = MODE == TK_WARP;
+    constexpr int TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
+    const int worker = BY_WARP ? warp * gridDim.x + blockIdx.x : blockIdx.x;    // few workers spread over the SMs
+    int workers = BY_WARP ? gridDim.x * NW : gridDim.x;
+    JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * workers * slot_floats(D, heads));
     int64_t u0, u1;            // units of all items end to end
     int64_t U = 0;
-    int ncta = gridDim.x;
     int b_first = 0;
-    if (P.split) {
+    if (SPLIT) {
         // units before each sequence (per kv head and group): a scan over the lengths
         const int per = (B + NT - 1) / NT;
         int sum = 0;
@@ -219,19 +252,29 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
         }
         if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
         __syncthreads();
-        U = (int64_t)pre[B] * Hg;
-        // at least TK_MIN_UNITS units a CTA
+        U = ((int64_t)pre[B] + (int64_t)TK_ITEM_UNITS * B) * Hg;      // the items' whole weight
         const int64_t most = (U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
-        if (most < ncta) ncta = static_cast<int>(most);
-        if ((int)blockIdx.x >= ncta) {
-            if (tid == 0) {
-                JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * gridDim.x * slot_floats(D, P.heads_per_group));
-                jd[blockIdx.x].pieces = 0;
-            }
+        if (most < workers) workers = static_cast<int>(most);
+        if (worker >= workers) {
+            if (BY_WARP ? lane == 0 : tid == 0) jd[worker].pieces = 0;
             return;
         }
-        u0 = U * blockIdx.x / ncta;
-        u1 = U * (blockIdx.x + 1) / ncta;
+        // the unit at which weight w falls; weights behind an item's units fall on its end
+        auto unit_at = [&](int64_t w) -> int64_t {
+            const int v = static_cast<int>(w / Hg);
+            int lo = 0, hi = B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] + TK_ITEM_UNITS * mid <= v) lo = mid;
+                else hi = mid - 1;
+            }
+            const int n = pre[lo + 1] - pre[lo], nw = n + TK_ITEM_UNITS;
+            const int64_t rem = w - ((int64_t)pre[lo] + (int64_t)TK_ITEM_UNITS * lo) * Hg;
+            const int64_t x = rem / nw;
+            return (int64_t)pre[lo] * Hg + x * n + min((int64_t)n, rem - x * nw);
+        };
+        u0 = unit_at(U * worker / workers);
+        u1 = worker + 1 < workers ? unit_at(U * (worker + 1) / workers) : (int64_t)pre[B] * Hg;
     } else {
         b_first = blockIdx.x / Hg;
         const int n = span_of(clamp_len(P, b_first, true), P.window, P.sinks).n;
@@ -243,13 +286,16 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
         u0 = (int64_t)(blockIdx.x - b_first * Hg) * n;
         u1 = u0 + n;
     }
-    const int nseq = P.split ? B : 1;   // sequences in pre[]
+    const int nseq = SPLIT ? B : 1;     // sequences in pre[]
 
-    // ---- a warp's units: u0 + warp + k NW. Lane i resolves unit k0 + i: coordinates of its loads.
+    // ---- a warp's units: u0 + k of its own range, u0 + warp + k NW of its CTA's. Lane i resolves unit k0 + i: coordinates of its
+    // loads.
+    const int64_t uf = BY_WARP ? u0 : u0 + warp;
+    constexpr int STEP = BY_WARP ? 1 : NW;
     const uint64_t pol = l2_evict_first();
     int pl_tok = 0, pl_head = 0, pl_page = 0;
     auto resolve = [&](int k0) {
-        const int64_t u = u0 + warp + (int64_t)(k0 + lane) * NW;
+        const int64_t u = uf + (int64_t)(k0 + lane) * STEP;
         if (u < u1) {
             const int v = static_cast<int>(u / Hg);
             int lo = 0, hi = nseq - 1;      // the sequence with pre[b] <= v < pre[b + 1]
@@ -277,7 +323,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
             }
         }
     };
-    const int nk = static_cast<int>(u1 - u0 > warp ? (u1 - u0 - warp + NW - 1) / NW : 0);   // units of this warp
+    const int nk = static_cast<int>(u1 > uf ? (u1 - uf + STEP - 1) / STEP : 0);   // units of this warp
     int kp = 0;                          // next unit to load
     auto produce = [&]() {
         if (kp >= nk) return;
@@ -310,9 +356,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
             else hi = mid - 1;
         }
     }
-    const int heads = P.heads_per_group;
-    JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * gridDim.x * slot_floats(D, heads));
-    bool crosses = false;                // an item begins here and goes on in the next CTA
+    bool crosses = false;                // an item begins here and goes on in the next range
     while (u < u1) {
         while ((int64_t)pre[bi + 1] * Hg <= u) ++bi;
         const int b = b_first + bi;
@@ -320,7 +364,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
         const int64_t first_of_b = (int64_t)pre[bi] * Hg;
         const int x = static_cast<int>((u - first_of_b) / n);
         const int64_t a = first_of_b + (int64_t)x * n, e = a + n;   // the item's units
-        const int64_t pe = e < u1 ? e : u1;                         // end of this CTA's piece
+        const int64_t pe = e < u1 ? e : u1;                         // end of this range's piece
         const int g = x / P.n_groups, grp = x - g * P.n_groups;
         const int hq0 = g * P.G + grp * heads;
         const int nq = min(heads, P.G - grp * heads);
@@ -353,7 +397,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
                 for (int i = 0; i < 4; ++i) o[nb][s][i] = 0.f;
         }
         for (; k < nk; ++k) {
-            const int64_t uk = u0 + warp + (int64_t)k * NW;
+            const int64_t uk = uf + (int64_t)k * STEP;
             if (uk >= pe) break;
             const int j = static_cast<int>(uk - a);
             const int tile = j < sp.ns ? j : j - sp.ns + sp.w0;
@@ -460,87 +504,121 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
             __syncwarp();
             produce();
         }
-        // ---- the CTA's warps join: maxima and sums first, then O in two halves of D per column block
+        // the rows' sums, in every lane of a head's eight
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float s = l[nb][i];
-                s += __shfl_xor_sync(0xffffffffu, s, 4);
-                s += __shfl_xor_sync(0xffffffffu, s, 8);
-                s += __shfl_xor_sync(0xffffffffu, s, 16);
-                if (lane < 4) {
-                    s_m[warp * 16 + nb * 8 + 2 * lane + i] = m[nb][i];
-                    s_l[warp * 16 + nb * 8 + 2 * lane + i] = s;
-                }
+                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 4);
+                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 8);
+                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 16);
             }
-        __syncthreads();
         const bool whole = a >= u0 && e <= u1;
-        const int slot = a < u0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1;
-        float* part = P.ws + (size_t)slot * slot_floats(D, heads);
-        if (a >= u0 && e > u1) crosses = true;
-        if (tid == 0 && P.split && a >= u0 && e > u1) {
-            // the item's last unit e - 1 lies in CTA ((e ncta) - 1) / U
-            const int last = static_cast<int>((e * ncta - 1) / U);
-            jd[blockIdx.x] = JoinDesc{b, x, last - (int)blockIdx.x + 1, 0};
+        float* part = P.ws + (size_t)(a < u0 ? 2 * worker : 2 * worker + 1) * slot_floats(D, heads);
+        if (SPLIT && a >= u0 && e > u1) {
+            crosses = true;
+            // the item's last unit, of weight w, lies in the last range that begins at w or before
+            const int64_t w = e - 1 + (int64_t)TK_ITEM_UNITS * ((int64_t)bi * Hg + x);
+            const int last = static_cast<int>(((w + 1) * workers - 1) / U);
+            if (BY_WARP ? lane == 0 : tid == 0) jd[worker] = JoinDesc{b, x, last - worker + 1, 0};
         }
+        if (BY_WARP) {
+            // the warp's own: the result, or a partial. Lane: heads 2 (lane % 4) + i, elements lane / 4 + 8 q.
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float al[2];
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float M = -INFINITY;
+                for (int i = 0; i < 2; ++i) {
+                    const int lh = nb * 8 + 2 * (lane & 3) + i;
+                    if (lh >= nq) continue;
+                    if (whole) {
+                        const int64_t row = (int64_t)b * P.H_q + hq0 + lh;
+                        const RowEnd r = row_end(P, row, m[nb][i], l[nb][i]);
+                        T* out = static_cast<T*>(P.O) + row * D + (lane >> 2);
+                        const float* op = P.O_prior + row * D + (lane >> 2);
 #pragma unroll
-                for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * (lane & 3) + i]);
-                al[i] = join_weight(m[nb][i], M);
-            }
+                        for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float* row = jbuf + (warp * 8 + 2 * (lane & 3)) * C::JROW + (lane >> 2);
+                            for (int q = 0; q < 2; ++q) {
+                                float v = o[nb][s][2 * q + i] * r.wo;
+                                if (r.prior) v = fmaf(op[16 * s + 8 * q], r.wp, v);
+                                out[16 * s + 8 * q] = Elem<T>::from(v);
+                            }
+                        if (lane < 4 && P.LSE) P.LSE[row] = r.lse;
+                    } else {
+                        float* pr = part + lh * (D + 4);
 #pragma unroll
-                for (int s = 0; s < KS / 2; ++s) {
-                    const float (&v)[4] = o[nb][hf * (KS / 2) + s];
-                    row[16 * s] = v[0] * al[0];
-                    row[C::JROW + 16 * s] = v[1] * al[1];
-                    row[16 * s + 8] = v[2] * al[0];
-                    row[C::JROW + 16 * s + 8] = v[3] * al[1];
+                        for (int s = 0; s < KS; ++s)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) pr[4 + 16 * s + 8 * q + (lane >> 2)] = o[nb][s][2 * q + i];
+                        if (lane < 4) *reinterpret_cast<float2*>(pr) = make_float2(m[nb][i], l[nb][i]);
+                    }
                 }
-                __syncthreads();
-                for (int i = tid; i < 8 * (D / 4); i += NT) {   // (head, pair of elements)
-                    const int h = i / (D / 4), d = 2 * (i - h * (D / 4));
-                    const int lh = nb * 8 + h;
-                    if (lh < nq) {
-                        float M = -INFINITY, L = 0.f;
+        } else {
+            // the CTA's warps join: maxima and sums first, then O in two halves of D per column block
 #pragma unroll
-                        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
-                        float a0 = 0.f, a1 = 0.f;
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int w = 0; w < NW; ++w) {
-                            const float mw = s_m[w * 16 + lh];
-                            L += s_l[w * 16 + lh] * join_weight(mw, M);
-                            const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * 8 + h) * C::JROW + d);
-                            a0 += f.x;
-                            a1 += f.y;
-                        }
-                        const int dd = hf * (D / 2) + d;
-                        if (whole) {
-                            finish2<T>(P, b, hq0 + lh, D, dd, a0, a1, M, L, dd == 0);
-                        } else {
-                            float* pr = part + lh * (D + 4);
-                            *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
-                            if (dd == 0) {
-                                pr[0] = M;
-                                pr[1] = L;
+                for (int i = 0; i < 2; ++i)
+                    if (lane < 4) {
+                        s_m[warp * 16 + nb * 8 + 2 * lane + i] = m[nb][i];
+                        s_l[warp * 16 + nb * 8 + 2 * lane + i] = l[nb][i];
+                    }
+            __syncthreads();
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float al[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * (lane & 3) + i]);
+                    al[i] = join_weight(m[nb][i], M);
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float* row = jbuf + (warp * 8 + 2 * (lane & 3)) * C::JROW + (lane >> 2);
+#pragma unroll
+                    for (int s = 0; s < KS / 2; ++s) {
+                        const float (&v)[4] = o[nb][hf * (KS / 2) + s];
+                        row[16 * s] = v[0] * al[0];
+                        row[C::JROW + 16 * s] = v[1] * al[1];
+                        row[16 * s + 8] = v[2] * al[0];
+                        row[C::JROW + 16 * s + 8] = v[3] * al[1];
+                    }
+                    __syncthreads();
+                    for (int i = tid; i < 8 * (D / 4); i += NT) {   // (head, pair of elements)
+                        const int h = i / (D / 4), d = 2 * (i - h * (D / 4));
+                        const int lh = nb * 8 + h;
+                        if (lh < nq) {
+                            float M = -INFINITY, L = 0.f;
+#pragma unroll
+                            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
+                            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                            for (int w = 0; w < NW; ++w) {
+                                const float mw = s_m[w * 16 + lh];
+                                L += s_l[w * 16 + lh] * join_weight(mw, M);
+                                const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * 8 + h) * C::JROW + d);
+                                a0 += f.x;
+                                a1 += f.y;
+                            }
+                            const int dd = hf * (D / 2) + d;
+                            if (!SPLIT || whole) {
+                                finish2<T>(P, b, hq0 + lh, D, dd, a0, a1, M, L, dd == 0);
+                            } else {
+                                float* pr = part + lh * (D + 4);
+                                *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
+                                if (dd == 0) *reinterpret_cast<float2*>(pr) = make_float2(M, L);
                             }
                         }
                     }
+                    __syncthreads();
                 }
-                __syncthreads();
             }
         }
         u = pe;
     }
-    if (P.split && tid == 0 && !crosses) jd[blockIdx.x].pieces = 0;
+    if (SPLIT && !crosses && (BY_WARP ? lane == 0 : tid == 0)) jd[worker].pieces = 0;
     if (failed) {
         set_err(P.err, ERR_PAGED_TOKEN);
         for (k = k_failed; k < kp; ++k)   // copies still in flight, waited for with the same limit
@@ -548,30 +626,30 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
     }
 }
 
-// Joins the partials of one split item and one q head: CTA (c, h) takes the item that begins in
-// CTA c of the attention launch. NT / (D/4) pieces at a time, one float4 of the row a thread.
+// Joins the partials of a split item: CTA (c, h, w) takes the one that begins in range w gridDim.x + c, if any, q head h
+// of it; 256 / (D/4) pieces at a time, one float4 of the row a thread.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_constant__ PagedAttn P) {
     constexpr int LP = D / 4, NP = 256 / LP;
     __shared__ float4 s_acc[NP][LP];
     pdl_wait();
     pdl_release();
-    const int c = blockIdx.x, h = blockIdx.y;
+    const int h = blockIdx.y, c = blockIdx.z * gridDim.x + blockIdx.x;
     const int heads = P.heads_per_group;
-    const JoinDesc jd = reinterpret_cast<const JoinDesc*>(P.ws + (size_t)2 * P.n_ctas * slot_floats(D, heads))[c];
-    if (jd.pieces == 0) return;
-    const int g = jd.x / P.n_groups, grp = jd.x - g * P.n_groups;
+    const JoinDesc d = reinterpret_cast<const JoinDesc*>(P.ws + (size_t)2 * gridDim.x * gridDim.z * slot_floats(D, heads))[c];
+    if (d.pieces == 0) return;
+    const int g = d.x / P.n_groups, grp = d.x - g * P.n_groups;
     if (grp * heads + h >= P.G) return;
     const int hq = g * P.G + grp * heads + h;
     const int tid = threadIdx.x, pp = tid / LP, q = tid - pp * LP;
     // piece i: slot 2 c + 1 for the first, 2 (c + i) for the others
     auto part = [&](int i) { return P.ws + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_floats(D, heads) + h * (D + 4); };
     float M = -INFINITY;
-    for (int i = tid & 31; i < jd.pieces; i += 32) M = fmaxf(M, part(i)[0]);
+    for (int i = tid & 31; i < d.pieces; i += 32) M = fmaxf(M, part(i)[0]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
-    for (int i = tid & 31; i < jd.pieces; i += 32) {
+    for (int i = tid & 31; i < d.pieces; i += 32) {
         const float2 ml = *reinterpret_cast<const float2*>(part(i));
         L += ml.y * join_weight(ml.x, M);
     }
@@ -580,11 +658,10 @@ __global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_cons
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (pp < NP) {
 #pragma unroll 4
-        for (int i = pp; i < jd.pieces; i += NP) {
+        for (int i = pp; i < d.pieces; i += NP) {
             const float* p = part(i);
-            const float mi = p[0];
             const float4 v = *reinterpret_cast<const float4*>(p + 4 + 4 * q);
-            const float w = join_weight(mi, M);
+            const float w = join_weight(p[0], M);
             acc.x = fmaf(w, v.x, acc.x);
             acc.y = fmaf(w, v.y, acc.y);
             acc.z = fmaf(w, v.z, acc.z);
@@ -600,17 +677,16 @@ __global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_cons
             const float4 v = s_acc[i][tid];
             a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
         }
-        finish2<T>(P, jd.b, hq, D, 4 * tid, a.x, a.y, M, L, tid == 0);
-        finish2<T>(P, jd.b, hq, D, 4 * tid + 2, a.z, a.w, M, L, false);
+        finish2<T>(P, d.b, hq, D, 4 * tid, a.x, a.y, M, L, tid == 0);
+        finish2<T>(P, d.b, hq, D, 4 * tid + 2, a.z, a.w, M, L, false);
     }
 }
 
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, int MODE>
 cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
     using C = TCfg<D>;
-    const int smem = C::SMEM_BASE + 4 * ((p.split ? p.B : 1) + 1);
     static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
-    const cudaError_t e0 = cudaFuncSetAttribute(paged_token_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e0 = cudaFuncSetAttribute(paged_token_kernel<T, D, NB, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 C::SMEM_BASE + 4 * (TK_MAX_B + 1));
     if (e0 != cudaSuccess) return e0;
     cudaLaunchAttribute at[1];
@@ -619,26 +695,31 @@ cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_ctas);
     cfg.blockDim = dim3(C::NW * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = C::SMEM_BASE + 4 * ((MODE != TK_ITEM ? p.B : 1) + 1);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token_kernel<T, D, NB>, p);
-    if (e != cudaSuccess || !p.split) return e;
-    cfg.gridDim = dim3(p.n_ctas, p.heads_per_group);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token_kernel<T, D, NB, MODE>, p);
+    if (e != cudaSuccess || MODE == TK_ITEM) return e;
+    cfg.gridDim = dim3(p.n_ctas, p.heads_per_group, MODE == TK_WARP ? C::NW : 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, paged_token_join_kernel<T, D>, p);
+}
+
+template <typename T, int D, int NB>
+cudaError_t launch_s(PagedAttn& p, cudaStream_t st) {
+    return p.mode == TK_WARP ? launch_t<T, D, NB, TK_WARP>(p, st) : p.mode == TK_CTA ? launch_t<T, D, NB, TK_CTA>(p, st) : launch_t<T, D, NB, TK_ITEM>(p, st);
 }
 
 template <typename T>
 cudaError_t launch_d(PagedAttn& p, int D, cudaStream_t st) {
     const bool two = p.heads_per_group > 8;
     switch (D) {
-        case 64: return two ? launch_t<T, 64, 2>(p, st) : launch_t<T, 64, 1>(p, st);
-        case 128: return two ? launch_t<T, 128, 2>(p, st) : launch_t<T, 128, 1>(p, st);
-        case 192: return launch_t<T, 192, 1>(p, st);
-        case 256: return launch_t<T, 256, 1>(p, st);
+        case 64: return two ? launch_s<T, 64, 2>(p, st) : launch_s<T, 64, 1>(p, st);
+        case 128: return two ? launch_s<T, 128, 2>(p, st) : launch_s<T, 128, 1>(p, st);
+        case 192: return launch_s<T, 192, 1>(p, st);
+        case 256: return launch_s<T, 256, 1>(p, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -647,7 +728,7 @@ cudaError_t launch_d(PagedAttn& p, int D, cudaStream_t st) {
 
 bool paged_token_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 
-// How a call is cut; fills heads_per_group, n_groups, split and n_ctas, and returns the workspace
+// How a call is cut; fills heads_per_group, n_groups, mode and n_ctas, and returns the workspace
 // bytes. Up to 8 q heads (16 at D <= 128) share a work item and one read of the kv head; more are
 // split evenly into several items.
 size_t paged_token_plan(PagedAttn& p, int D, int sms) {
@@ -659,10 +740,11 @@ size_t paged_token_plan(PagedAttn& p, int D, int sms) {
         const int64_t w = ((int64_t)p.window + PG_SUB - 1) / PG_SUB + 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;
         if (w < bound) bound = w;
     }
-    p.split = bound > TK_DIRECT_UNITS;
     const int64_t items = (int64_t)p.B * p.H_kv * p.n_groups;
-    p.n_ctas = p.split ? sms : static_cast<int>(items);
-    return p.split ? (size_t)2 * p.n_ctas * slot_floats(D, p.heads_per_group) * sizeof(float) + p.n_ctas * sizeof(JoinDesc) : 0;
+    p.mode = bound <= TK_DIRECT_UNITS ? TK_ITEM : items <= (int64_t)TK_FEW_ITEMS * sms ? TK_CTA : TK_WARP;
+    p.n_ctas = p.mode == TK_ITEM ? static_cast<int>(items) : sms;
+    const size_t ranges = p.mode == TK_ITEM ? 0 : (size_t)p.n_ctas * (p.mode == TK_CTA ? 1 : D <= 128 ? TCfg<128>::NW : TCfg<256>::NW);
+    return ranges * (2 * slot_floats(D, p.heads_per_group) * sizeof(float) + sizeof(JoinDesc));
 }
 
 cudaError_t launch_paged_token(PagedAttn& p, int D, cudaStream_t st) {

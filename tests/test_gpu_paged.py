@@ -171,6 +171,15 @@ def test_token_window(ctx, dtype, W, sinks):
     _attend_case(ctx, lens, 7, 1, 64, 32, dtype, W, sinks, prior=True, nhd=True)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 2, 64), (32, 2, 64), (16, 4, 128), (64, 4, 128), (20, 4, 192), (9, 3, 256), (128, 4, 128)])
+def test_token_many_items(ctx, dtype, H_q, H_kv, D):
+    """More items than a few per SM: a range per warp, with whole items, items cut once and items over many ranges."""
+    lens = [(37 * i * i) % 700 for i in range(180)] + [9000, 0, 1, 2500]
+    _attend_case(ctx, lens, H_q, H_kv, D, 16, dtype)
+    _attend_case(ctx, lens, H_q, H_kv, D, 32, dtype, W=300, sinks=5, prior=True, nhd=True, seed=4, width=600)
+
+
 def test_token_hidden_keys_hold_anything(ctx):
     """Behind the window, in front of the last token and in unneeded pages: NaN, infinities, the lowest value, and table
     entries that are no pages."""
