@@ -267,9 +267,40 @@ def _rows(t, out, weight):
     """pck_rows of t [T, H, D] (None: no rows of this kind)."""
     if t is None:
         return None
-    o = (0, 0) if out is None else out.stride()
-    return RowsT(t.data_ptr(), None if out is None else out.data_ptr(), t.shape[1], t.stride(0), t.stride(1), o[0], o[1],
-                 None if weight is None else weight.data_ptr())
+    i = t.stride()
+    w = None if weight is None else weight.data_ptr()
+    if out is None:
+        return RowsT(t.data_ptr(), None, t.shape[1], i[0], i[1], 0, 0, w)
+    o = out.stride()
+    return RowsT(t.data_ptr(), out.data_ptr(), t.shape[1], i[0], i[1], o[0], o[1], w)
+
+
+# The checks of a call's usual arguments, in one pass without names: what fails here goes through the named
+# checks, which say what is wrong.
+def _rows_fit(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.stride()[2] == 1 and t.device == device
+
+
+def _dense_fit(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
+
+
+def _side_fits(t, out, weight, dtype, T, D, device, norm):
+    """Rows [T, H, D] with their output and norm weight, or none of the three."""
+    if t is None:
+        return out is None and weight is None
+    sh = t.shape
+    return (len(sh) == 3 and sh[0] == T and sh[2] == D and t.dtype is dtype and t.stride()[2] == 1 and t.device == device
+            and (out is None or _rows_fit(out, dtype, sh, device))
+            and (weight is None or norm and weight.dtype is dtype and weight.shape == (D,) and weight.is_contiguous()
+                 and weight.device == device))
+
+
+try:   # the current stream of a device as a number, without the Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _rotary(cos_sin, interleaved, positions):
@@ -315,6 +346,7 @@ class PagedCache:
         self.n_pages, self.H_kv, self.page_size, self.D = k.shape
         self.c = PagedCacheT(k.data_ptr(), v.data_ptr(), _PAGED_DT[k.dtype], self.H_kv, self.D, self.page_size,
                              self.n_pages, *k.stride()[:3], *v.stride()[:3])
+        self.ref = ctypes.byref(self.c)
         self._ws = {}   # workspace bytes by the sizes of a call
 
 
@@ -538,12 +570,11 @@ class Context:
     # ---- paged tail
     def _launch(self, fn, stream, *args):
         """fn(context, *args, stream) on the given stream, or the current one of the context's device."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        rc = fn(self.h, *args, s.cuda_stream)
+        rc = fn(self.h, *args, _raw_stream(self.device.index) if stream is None else stream.cuda_stream)
         if rc != OK:
             raise PckError(rc, self.last_error())
 
-    def _empty(self, stream, *shape, dtype):
+    def _empty(self, stream, shape, dtype):
         """A new tensor that the call writes on `stream` (None: the current one) and the caller uses on its own."""
         if stream is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
@@ -553,24 +584,25 @@ class Context:
         return t
 
     def _batch(self, cache, table, kv_len, cu_rows, T, max_rows):
-        B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-        if table.dim() != 2 or B < 0:
-            raise ValueError("kv_len must be [B] and table [B, max_pages]")
-        W = table.shape[1]
-        _need(kv_len, "kv_len", torch.int32, (B,))
-        _need(table, "table", torch.int32, (B, W))
+        dev = self.device
+        B, W = kv_len.shape[0] if kv_len.dim() == 1 else -1, table.shape[-1] if table.dim() == 2 else -1
+        if not (cache.device == dev and _dense_fit(kv_len, torch.int32, (B,), dev) and _dense_fit(table, torch.int32, (B, W), dev)
+                and (T == B if cu_rows is None else _dense_fit(cu_rows, torch.int32, (B + 1,), dev))):
+            if table.dim() != 2 or B < 0:
+                raise ValueError("kv_len must be [B] and table [B, max_pages]")
+            _need(kv_len, "kv_len", torch.int32, (B,))
+            _need(table, "table", torch.int32, (B, W))
+            if cu_rows is None:
+                if T != B:
+                    raise ValueError(f"{T} rows for {B} sequences: cu_rows is needed")
+            else:
+                _need(cu_rows, "cu_rows", torch.int32, (B + 1,))
+            if cache.device != dev:
+                raise ValueError(f"cache: must be on the CUDA device {dev}, not {cache.device}")
+            _on(dev, kv_len=kv_len, table=table, cu_rows=cu_rows)
         if cu_rows is None:
-            if T != B:
-                raise ValueError(f"{T} rows for {B} sequences: cu_rows is needed")
-            max_rows = 1
-        else:
-            _need(cu_rows, "cu_rows", torch.int32, (B + 1,))
-            max_rows = T if max_rows is None else max_rows
-        if cache.device != self.device:
-            raise ValueError(f"cache: must be on the CUDA device {self.device}, not {cache.device}")
-        _on(self.device, kv_len=kv_len, table=table, cu_rows=cu_rows)
-        return PagedBatchT(B, T, None if cu_rows is None else cu_rows.data_ptr(), kv_len.data_ptr(), table.data_ptr(), W,
-                           max_rows)
+            return PagedBatchT(B, T, None, kv_len.data_ptr(), table.data_ptr(), W, 1)
+        return PagedBatchT(B, T, cu_rows.data_ptr(), kv_len.data_ptr(), table.data_ptr(), W, T if max_rows is None else max_rows)
 
     def qk_norm_rope(self, Q, K, positions=None, cos_sin=None, norm=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, Q_out=None, K_out=None, stream=None):
@@ -581,35 +613,44 @@ class Context:
         if one is None or one.dim() != 3:
             raise ValueError("Q [T, H_q, D], K [T, H_kv, D] or both must be given")
         T, _, D = one.shape
-        if one.dtype not in _ROWS_DT:
-            raise ValueError(f"dtype {one.dtype}, expected float32, float16 or bfloat16")
+        dt, dev = one.dtype, self.device
+        if dt not in _ROWS_DT:
+            raise ValueError(f"dtype {dt}, expected float32, float16 or bfloat16")
         norm = (q_weight is not None or k_weight is not None) if norm is None else bool(norm)
-        for t, o, w, n in ((Q, Q_out, q_weight, "Q"), (K, K_out, k_weight, "K")):
-            if t is None:
-                if o is not None or w is not None:
-                    raise ValueError(f"{n}_out or a weight without {n}")
-                continue
-            if t.dim() != 3:
-                raise ValueError(f"{n} must be [T, H, D]")
-            _need(t, n, one.dtype, (T, t.shape[1], D), strided=True)
-            if o is not None:
-                _need(o, n + "_out", one.dtype, t.shape, strided=True)
-            if w is not None:
-                _need(w, n + "_weight", one.dtype, (D,))
-        if not norm and (q_weight is not None or k_weight is not None):
-            raise ValueError("a weight without the norm")
-        _check_rope(cos_sin, positions, T)
-        if cos_sin is not None and positions is None:
-            raise ValueError("cos_sin without positions")
-        _on(self.device, Q=Q, K=K, Q_out=Q_out, K_out=K_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-            positions=positions)
+        if not (_side_fits(Q, Q_out, q_weight, dt, T, D, dev, norm) and _side_fits(K, K_out, k_weight, dt, T, D, dev, norm)
+                and self._rope_fits(cos_sin, positions, T, True)):
+            for t, o, w, n in ((Q, Q_out, q_weight, "Q"), (K, K_out, k_weight, "K")):
+                if t is None:
+                    if o is not None or w is not None:
+                        raise ValueError(f"{n}_out or a weight without {n}")
+                    continue
+                if t.dim() != 3:
+                    raise ValueError(f"{n} must be [T, H, D]")
+                _need(t, n, dt, (T, t.shape[1], D), strided=True)
+                if o is not None:
+                    _need(o, n + "_out", dt, t.shape, strided=True)
+                if w is not None:
+                    _need(w, n + "_weight", dt, (D,))
+            if not norm and (q_weight is not None or k_weight is not None):
+                raise ValueError("a weight without the norm")
+            _check_rope(cos_sin, positions, T)
+            if cos_sin is not None and positions is None:
+                raise ValueError("cos_sin without positions")
+            _on(dev, Q=Q, K=K, Q_out=Q_out, K_out=K_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                positions=positions)
         if Q is not None and Q_out is None:
-            Q_out = self._empty(stream, *Q.shape, dtype=Q.dtype)
+            Q_out = self._empty(stream, Q.shape, dt)
         if K is not None and K_out is None:
-            K_out = self._empty(stream, *K.shape, dtype=K.dtype)
-        self._launch(self.lib.pck_qk_norm_rope, stream, _ROWS_DT[one.dtype], T, D, _ref(_rows(Q, Q_out, q_weight)),
-                     _ref(_rows(K, K_out, k_weight)), int(norm), eps, _ref(_rotary(cos_sin, interleaved, positions)))
+            K_out = self._empty(stream, K.shape, dt)
+        self._launch(self.lib.pck_qk_norm_rope, stream, _ROWS_DT[dt], T, D, _ref(_rows(Q, Q_out, q_weight)),
+                     _ref(_rows(K, K_out, k_weight)), norm, eps, _ref(_rotary(cos_sin, interleaved, positions)))
         return Q_out, K_out
+
+    def _rope_fits(self, cos_sin, positions, T, need_positions):
+        if cos_sin is None:
+            return positions is None
+        return (cos_sin.dim() == 2 and _dense_fit(cos_sin, torch.float32, cos_sin.shape, self.device)
+                and (not need_positions if positions is None else _dense_fit(positions, torch.int32, (T,), self.device)))
 
     def paged_append(self, cache, table, kv_len, K, V, Q=None, cu_rows=None, cos_sin=None, positions=None, norm=None,
                      q_weight=None, k_weight=None, eps=1e-6, interleaved=False, Q_out=None, stream=None):
@@ -618,34 +659,39 @@ class Context:
         same pass. positions: None takes the cache positions. Returns Q_out (None without Q)."""
         if K.dim() != 3 or K.shape[1:] != (cache.H_kv, cache.D):
             raise ValueError(f"K must be [T, {cache.H_kv}, {cache.D}]")
-        T, D, dt = K.shape[0], cache.D, K.dtype
+        T, D, dt, dev = K.shape[0], cache.D, K.dtype, self.device
         if dt != cache.dtype and dt != torch.float32:
             raise ValueError(f"K: dtype {dt}, expected {cache.dtype} or float32")
-        _need(K, "K", dt, K.shape, strided=True)
-        _need(V, "V", dt, K.shape, strided=True)
-        if Q is not None:
-            if Q.dim() != 3:
-                raise ValueError("Q must be [T, H_q, D]")
-            _need(Q, "Q", dt, (T, Q.shape[1], D), strided=True)
-            if Q_out is not None:
-                _need(Q_out, "Q_out", dt, Q.shape, strided=True)
-        elif Q_out is not None or q_weight is not None:
-            raise ValueError("Q_out or q_weight without Q")
         norm = (q_weight is not None or k_weight is not None) if norm is None else bool(norm)
-        for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                if not norm:
-                    raise ValueError("a weight without the norm")
-                _need(w, n, dt, (D,))
-        _check_rope(cos_sin, positions, T)
+        fits = (_rows_fit(K, dt, K.shape, dev) and _rows_fit(V, dt, K.shape, dev)
+                and _side_fits(Q, Q_out, q_weight, dt, T, D, dev, norm)
+                and (k_weight is None or norm and _dense_fit(k_weight, dt, (D,), dev))
+                and self._rope_fits(cos_sin, positions, T, False))
+        if not fits:
+            _need(K, "K", dt, K.shape, strided=True)
+            _need(V, "V", dt, K.shape, strided=True)
+            if Q is not None:
+                if Q.dim() != 3:
+                    raise ValueError("Q must be [T, H_q, D]")
+                _need(Q, "Q", dt, (T, Q.shape[1], D), strided=True)
+                if Q_out is not None:
+                    _need(Q_out, "Q_out", dt, Q.shape, strided=True)
+            elif Q_out is not None or q_weight is not None:
+                raise ValueError("Q_out or q_weight without Q")
+            for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+                if w is not None:
+                    if not norm:
+                        raise ValueError("a weight without the norm")
+                    _need(w, n, dt, (D,))
+            _check_rope(cos_sin, positions, T)
         batch = self._batch(cache, table, kv_len, cu_rows, T, None)
-        _on(self.device, K=K, V=V, Q=Q, Q_out=Q_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-            positions=positions)
+        if not fits:
+            _on(dev, K=K, V=V, Q=Q, Q_out=Q_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, positions=positions)
         if Q is not None and Q_out is None:
-            Q_out = self._empty(stream, *Q.shape, dtype=dt)
-        self._launch(self.lib.pck_paged_append, stream, _ref(cache.c), _ref(batch), _ROWS_DT[dt],
+            Q_out = self._empty(stream, Q.shape, dt)
+        self._launch(self.lib.pck_paged_append, stream, cache.ref, _ref(batch), _ROWS_DT[dt],
                      _ref(_rows(Q, Q_out, q_weight)), _ref(_rows(K, None, k_weight)), _ref(_rows(V, None, None)),
-                     int(norm), eps, _ref(_rotary(cos_sin, interleaved, positions)))
+                     norm, eps, _ref(_rotary(cos_sin, interleaved, positions)))
         return Q_out
 
     def paged_attend(self, cache, table, kv_len, Q, cu_rows=None, max_rows=None, window=0, sinks=0, prior=None, O=None,
@@ -655,38 +701,45 @@ class Context:
         cu_rows, else 1). Outputs and the workspace are allocated when not given. Returns (O, LSE)."""
         if Q.dim() != 3 or Q.shape[2] != cache.D:
             raise ValueError(f"Q must be [T, H_q, {cache.D}]")
-        T, H_q, D = Q.shape
-        _need(Q, "Q", cache.dtype, Q.shape, strided=True)
-        if O is not None:
-            _need(O, "O", cache.dtype, Q.shape)
-        if LSE is not None:
-            _need(LSE, "LSE", torch.float32, (T, H_q))
+        T, H_q, _ = shape = Q.shape
+        dt, dev = cache.dtype, self.device
         Op, Lp = (None, None) if prior is None else prior
-        if prior is not None:
-            _need(Op, "prior O", torch.float32, Q.shape)
-            _need(Lp, "prior LSE", torch.float32, (T, H_q))
+        fits = (_rows_fit(Q, dt, shape, dev) and (O is None or _dense_fit(O, dt, shape, dev))
+                and (LSE is None or _dense_fit(LSE, torch.float32, (T, H_q), dev))
+                and (prior is None or _dense_fit(Op, torch.float32, shape, dev) and _dense_fit(Lp, torch.float32, (T, H_q), dev)))
+        if not fits:
+            _need(Q, "Q", dt, shape, strided=True)
+            if O is not None:
+                _need(O, "O", dt, shape)
+            if LSE is not None:
+                _need(LSE, "LSE", torch.float32, (T, H_q))
+            if prior is not None:
+                _need(Op, "prior O", torch.float32, shape)
+                _need(Lp, "prior LSE", torch.float32, (T, H_q))
         batch = self._batch(cache, table, kv_len, cu_rows, T, max_rows)
-        _on(self.device, Q=Q, O=O, LSE=LSE, prior_O=Op, prior_LSE=Lp, workspace=workspace)
+        if not fits or workspace is not None:
+            _on(dev, Q=Q, O=O, LSE=LSE, prior_O=Op, prior_LSE=Lp, workspace=workspace)
+        bref = ctypes.byref(batch)
         key = (batch.B, T, batch.max_pages, batch.max_rows, cu_rows is None, H_q, window, sinks, self.h.value)
         need = cache._ws.get(key)
         if need is None:
             n = ctypes.c_size_t()
-            self._rc(self.lib.pck_paged_workspace(self.h, _ref(cache.c), _ref(batch), H_q, window, sinks, _ref(n)))
+            self._rc(self.lib.pck_paged_workspace(self.h, cache.ref, bref, H_q, window, sinks, ctypes.byref(n)))
             if len(cache._ws) >= 256:
                 cache._ws.clear()
             need = cache._ws[key] = n.value
         if workspace is None:
-            workspace = self._empty(stream, need, dtype=torch.uint8) if need else None
+            workspace = self._empty(stream, need, torch.uint8) if need else None
         elif not workspace.is_contiguous():
             raise ValueError("workspace: must be contiguous")
         if O is None:
-            O = self._empty(stream, T, H_q, D, dtype=cache.dtype)
+            O = self._empty(stream, shape, dt)
         if LSE is None and want_lse:
-            LSE = self._empty(stream, T, H_q, dtype=torch.float32)
-        self._launch(self.lib.pck_paged_attend, stream, _ref(cache.c), _ref(batch), H_q, Q.data_ptr(), Q.stride(0),
-                     Q.stride(1), window, sinks, None if Op is None else Op.data_ptr(),
-                     None if Lp is None else Lp.data_ptr(), O.data_ptr(), None if LSE is None else LSE.data_ptr(),
-                     None if workspace is None else workspace.data_ptr(),
+            LSE = self._empty(stream, (T, H_q), torch.float32)
+        st = Q.stride()
+        self._launch(self.lib.pck_paged_attend, stream, cache.ref, bref, H_q, Q.data_ptr(), st[0], st[1], window, sinks,
+                     None if Op is None else Op.data_ptr(), None if Lp is None else Lp.data_ptr(), O.data_ptr(),
+                     None if LSE is None else LSE.data_ptr(), None if workspace is None else workspace.data_ptr(),
                      0 if workspace is None else workspace.numel() * workspace.element_size())
         return O, LSE
 

@@ -20,13 +20,17 @@ namespace pck {
 namespace {
 
 constexpr int NR_THREADS = 256;
+// Heads whose loads a lane has in flight, and blocks per SM (64 registers): 16,384 tokens of 72 heads in 106.7 us; one
+// head 111, four heads 115 (3 blocks); five blocks spill (138).
+constexpr int NR_HEADS = 2;
+template <typename TI> __host__ __device__ constexpr int nr_blocks() { return sizeof(TI) == 4 ? 3 : 4; }   // fp32 rows take 80 registers
 
 template <typename T>
-struct Vec8;   // 8 elements as fp32
+struct Vec8;   // 8 elements: as they lie in memory (Raw), and as fp32
 template <>
 struct Vec8<__half> {
-    static __device__ __forceinline__ void load(const __half* p, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
+    typedef uint4 Raw;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -47,8 +51,8 @@ struct Vec8<__half> {
 };
 template <>
 struct Vec8<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
+    typedef uint4 Raw;
+    static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -68,8 +72,11 @@ struct Vec8<__nv_bfloat16> {
 };
 template <>
 struct Vec8<float> {
-    static __device__ __forceinline__ void load(const float* p, float (&x)[8]) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    struct Raw {
+        float4 a, b;
+    };
+    static __device__ __forceinline__ void unpack(const Raw& r, float (&x)[8]) {
+        const float4 a = r.a, b = r.b;
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
@@ -81,7 +88,7 @@ struct Vec8<float> {
 
 // L: lanes per row. TI: type of the rows read (and of q written); TC: type of the cache (append).
 template <typename TI, typename TC, int L>
-__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(const __grid_constant__ RopeParams P) {
     constexpr int SUBS = NR_THREADS / L;
     pdl_wait();      // inputs may come from the previous kernel of the stream
     pdl_release();
@@ -149,71 +156,87 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const __grid_cons
         }
     }
 
-#pragma unroll 2
-    for (int hh = h0; hh < Ht; hh += P.spt) {
-        const int cls = hh < P.q.H ? 0 : hh < P.q.H + P.k.H ? 1 : 2;
-        const RowsArg& A = cls == 0 ? P.q : cls == 1 ? P.k : P.v;
-        const int h = hh - (cls == 0 ? 0 : cls == 1 ? P.q.H : P.q.H + P.k.H);
-        const TI* src = static_cast<const TI*>(A.in) + (int64_t)t * A.in_row + (int64_t)h * A.in_head;
-        float x[8], y[8];
+    typedef typename Vec8<TI>::Raw Raw;
+    auto at = [&](const void* p, int64_t off) { return static_cast<const TI*>(p) + off; };
+    // NR_HEADS heads at a time, all of their loads in flight before the first is used
+    for (int hb = h0; hb < Ht; hb += NR_HEADS * P.spt) {
+        Raw r0[NR_HEADS], r1[NR_HEADS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-        if (active) {
-            Vec8<TI>::load(src + 8 * s0, x);
-            Vec8<TI>::load(src + 8 * s1, y);
-        }
-        if (A.norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, L);
-            const float r = rsqrtf(ss / P.D + P.eps);
-            if (A.w && active) {
-                float w0[8], w1[8];
-                Vec8<TI>::load(static_cast<const TI*>(A.w) + 8 * s0, w0);
-                Vec8<TI>::load(static_cast<const TI*>(A.w) + 8 * s1, w1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = x[i] * r * w0[i];
-                    y[i] = y[i] * r * w1[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= r;
-                    y[i] *= r;
-                }
+        for (int k = 0; k < NR_HEADS; ++k) {
+            const int hh = hb + k * P.spt;
+            r0[k] = r1[k] = Raw{};
+            if (hh < Ht && active) {
+                const int cls = hh < P.q.H ? 0 : hh < P.q.H + P.k.H ? 1 : 2;
+                const RowsArg& A = cls == 0 ? P.q : cls == 1 ? P.k : P.v;
+                const int h = hh - (cls == 0 ? 0 : cls == 1 ? P.q.H : P.q.H + P.k.H);
+                const TI* src = at(A.in, (int64_t)t * A.in_row + (int64_t)h * A.in_head);
+                r0[k] = *reinterpret_cast<const Raw*>(src + 8 * s0);
+                r1[k] = *reinterpret_cast<const Raw*>(src + 8 * s1);
             }
         }
-        if (rot && cls != 2) {
-            if (P.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
-                    x[2 * i] = a * co[i] - b * si[i];
-                    x[2 * i + 1] = b * co[i] + a * si[i];
-                    y[2 * i] = c * co[4 + i] - d * si[4 + i];
-                    y[2 * i + 1] = d * co[4 + i] + c * si[4 + i];
-                }
-            } else {
+        for (int k = 0; k < NR_HEADS; ++k) {
+            const int hh = hb + k * P.spt;
+            if (hh >= Ht) break;
+            const int cls = hh < P.q.H ? 0 : hh < P.q.H + P.k.H ? 1 : 2;
+            const RowsArg& A = cls == 0 ? P.q : cls == 1 ? P.k : P.v;
+            const int h = hh - (cls == 0 ? 0 : cls == 1 ? P.q.H : P.q.H + P.k.H);
+            float x[8], y[8];
+            Vec8<TI>::unpack(r0[k], x);
+            Vec8<TI>::unpack(r1[k], y);
+            if (A.norm) {
+                float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = x[i], b = y[i];
-                    x[i] = a * co[i] - b * si[i];
-                    y[i] = b * co[i] + a * si[i];
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, L);
+                const float r = rsqrtf(ss * P.inv_d + P.eps);
+                if (A.w && active) {
+                    float w0[8], w1[8];
+                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(at(A.w, 8 * s0)), w0);
+                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(at(A.w, 8 * s1)), w1);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = x[i] * r * w0[i];
+                        y[i] = y[i] * r * w1[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] *= r;
+                        y[i] *= r;
+                    }
                 }
             }
-        }
-        if (!active) continue;
-        if (P.append && cls != 0) {
-            TC* dst = static_cast<TC*>(A.out) + (cls == 1 ? kbase : vbase) + (int64_t)h * A.out_head;
-            Vec8<TC>::store(dst + 8 * s0, x);
-            Vec8<TC>::store(dst + 8 * s1, y);
-        } else {
-            TI* dst = static_cast<TI*>(A.out) + (int64_t)t * A.out_row + (int64_t)h * A.out_head;
-            Vec8<TI>::store(dst + 8 * s0, x);
-            Vec8<TI>::store(dst + 8 * s1, y);
+            if (rot && cls != 2) {
+                if (P.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
+                        x[2 * i] = a * co[i] - b * si[i];
+                        x[2 * i + 1] = b * co[i] + a * si[i];
+                        y[2 * i] = c * co[4 + i] - d * si[4 + i];
+                        y[2 * i + 1] = d * co[4 + i] + c * si[4 + i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float a = x[i], b = y[i];
+                        x[i] = a * co[i] - b * si[i];
+                        y[i] = b * co[i] + a * si[i];
+                    }
+                }
+            }
+            if (!active) continue;
+            if (P.append && cls != 0) {
+                TC* dst = static_cast<TC*>(A.out) + (cls == 1 ? kbase : vbase) + (int64_t)h * A.out_head;
+                Vec8<TC>::store(dst + 8 * s0, x);
+                Vec8<TC>::store(dst + 8 * s1, y);
+            } else {
+                TI* dst = static_cast<TI*>(A.out) + (int64_t)t * A.out_row + (int64_t)h * A.out_head;
+                Vec8<TI>::store(dst + 8 * s0, x);
+                Vec8<TI>::store(dst + 8 * s1, y);
+            }
         }
     }
 }
@@ -221,12 +244,14 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const __grid_cons
 template <typename TI, typename TC, int L>
 cudaError_t launch_l(RopeParams p, int sms, cudaStream_t st) {
     constexpr int SUBS = NR_THREADS / L;
-    // Subwarps per token: as few as still give every SM its 2048 threads twice over, at least one
-    // warp's worth (neighbouring heads of a token share a warp's wide accesses).
+    // Subwarps per token: as few as still give every SM 2048 threads, at least one warp's worth (neighbouring heads
+    // of a token share a warp's wide accesses). At 16,384 tokens of 72 heads: 106.7 us, with twice as many 108.7, with
+    // four times 135.
     const int Ht = p.q.H + p.k.H + p.v.H;
     int spt = 32 / L;
-    while (spt < SUBS && spt < Ht && (int64_t)p.T * spt < (int64_t)sms * (4096 / L)) spt *= 2;
+    while (spt < SUBS && spt < Ht && (int64_t)p.T * spt < (int64_t)sms * (2048 / L)) spt *= 2;
     p.spt = spt;
+    p.inv_d = 1.0f / p.D;
     const int tpb = SUBS / spt;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -10,6 +10,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pck.h"
 #include "pck_common.cuh"
 
@@ -42,7 +44,7 @@ struct RowsArg {
 struct RopeParams {
     RowsArg q, k, v;                 // v: append only (copied), H = 0 otherwise
     int T, D, R, interleaved;
-    float eps;
+    float eps, inv_d;
     const float* cos_sin;            // [n_pos, R]: R/2 cosines, R/2 sines
     int n_pos;
     const int32_t* positions;        // [T] or nullptr (append: the row's cache position)
@@ -77,7 +79,7 @@ struct PagedAttn {
     int window, sinks;
     int max_rows;                    // bound on a sequence's rows
     float scale_log2;                // tau * log2(e)
-    int dtype;
+    int dtype, device;
     float* ws;                       // partials, then the join descriptors
     int* err;
     // one-token kernel
@@ -108,6 +110,18 @@ struct CtxView {
 CtxView ctx_view(pck_ctx* c);
 int ctx_fail(pck_ctx* c, int code, const char* fmt, ...);
 void ctx_count_query(pck_ctx* c);
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per kernel and device. (Two threads may both do it: it is
+// the same setting.)
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes, int device) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -316,6 +316,7 @@ int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     p.scale_log2 = PG_LOG2E / sqrtf(static_cast<float>(D));
     p.ws = static_cast<float*>(workspace);
     p.err = v.dev_err;
+    p.device = v.device;
     p.k_base = cache->K;
     p.v_base = cache->V;
     const int64_t strides[6] = {cache->k_page, cache->k_head, cache->k_token, cache->v_page, cache->v_head, cache->v_token};

@@ -686,8 +686,7 @@ template <typename T, int D, int NB, int MODE>
 cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
     using C = TCfg<D>;
     static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
-    const cudaError_t e0 = cudaFuncSetAttribute(paged_token_kernel<T, D, NB, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                C::SMEM_BASE + 4 * (TK_MAX_B + 1));
+    const cudaError_t e0 = allow_smem<paged_token_kernel<T, D, NB, MODE>>(C::SMEM_BASE + 4 * (TK_MAX_B + 1), p.device);
     if (e0 != cudaSuccess) return e0;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
