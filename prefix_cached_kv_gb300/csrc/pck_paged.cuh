@@ -84,6 +84,7 @@ struct PagedAttn {
     int* err;
     // one-token kernel
     int heads_per_group, n_groups;   // q heads of a kv head that share a work item, and items per kv head
+    int cols;                        // columns of a work item: rows x heads
     int mode;                        // how the call is cut
     int n_ctas;
     // row kernel
@@ -93,9 +94,11 @@ struct PagedAttn {
 };
 
 bool paged_token_dim_ok(int D);
+bool paged_token_rows_ok(int G, int max_rows, int D);     // ragged rows few enough for the one-token kernel
 constexpr int paged_token_box_rows() { return PG_SUB; }   // tokens of a TMA tile load
 size_t paged_token_plan(PagedAttn& p, int D, int sms);    // how the call is cut; its workspace in bytes
 cudaError_t launch_paged_token(PagedAttn& p, int D, cudaStream_t st);
+cudaError_t launch_paged_token_bf16(PagedAttn& p, int D, cudaStream_t st);
 bool paged_rows_dim_ok(int D);
 int paged_rows_box(int page);             // tokens of a TMA box
 int paged_rows_tok_per_tile(int G);

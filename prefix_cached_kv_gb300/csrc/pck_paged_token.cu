@@ -1,753 +1,37 @@
-// pck_paged_token.cu -- attention of one new token per sequence over a paged KV cache, split over
-// the cache's length and joined.
-//
-// Per sequence b (n = kv_len[b] keys, the new token's own among them) and q head h of kv head g:
-//   s_j = tau q_h . k_j,  O = sum_j 2^(s_j' - m) v_j / l,  LSE = (m + log2 l) ln 2   (s' = s log2 e)
-// over the visible keys: all n, or with a window W the last W and the first `sinks`.
-//
-// Every K and V byte is read once and used for G = H_q / H_kv heads: 4 G flop per 4 bytes, so HBM
-// bounds it and the kernel's business is to keep loads in flight on every SM whatever the lengths:
-//  * A unit is a cache tile of 16 tokens of one kv head (a page is a multiple of 16, so a unit never
-//    leaves its page). The units of all items (sequence, kv head, group of q heads) laid end to end
-//    are cut into equal ranges from the lengths on the device (one block scan per CTA), so a ragged
-//    batch, one long sequence and many short ones all load every SM evenly, and a captured graph
-//    follows the lengths it finds. Few items (at most TK_FEW_ITEMS per SM): a range per CTA, whose warps
-//    take every NW-th unit and join through shared memory; neighbouring warps then read neighbouring
-//    tiles, and an item has few pieces. Many: a range per warp, because a change of item (its q, its end)
-//    then stalls one of the SM's eight streams and not all of them.
-//  * One CTA per SM; each warp streams its units through a ring of its own (two TMA tile loads a unit,
-//    128-byte swizzle, evict-first: read once). Lane i of a warp resolves the i-th of its next 32 units
-//    (sequence, tile, page number) at once, so page-table latency is paid once in 32 units and off the
-//    critical path; rings run on across items.
-//  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads as columns; the running
-//    maximum moves only when a score passes it by 8 (log2), so every p <= 2^8; p goes into
-//    O^T += V^T p^T as a 16-bit hi + lo pair (two MMAs into one accumulator), which keeps ~22 bits
-//    (16 for bf16) of p: the result's own rounding is then the only visible one, and these MMAs are
-//    hidden behind the loads.
-//  * An item that lies within one range is finished there; one that crosses ranges leaves a partial [m, l, O]
-//    per range, at most two per range, and a second, programmatically launched kernel joins them.
-//  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA whose warps take its
-//    units in turn and join through shared memory: one launch.
-#include "pck_paged.cuh"
+// pck_paged_token.cu -- one-token attention over a paged cache: how a call is cut, and the fp16 kernels.
+#include "pck_paged_token_impl.cuh"
 
 namespace pck {
-namespace {
-
-constexpr int TK_DIRECT_UNITS = 32;    // 512 tokens
-constexpr int TK_FEW_ITEMS = 2;        // items per SM up to which a range is a CTA's
-// How a call is cut.
-enum { TK_ITEM, TK_CTA, TK_WARP };     // an item per CTA; ranges per CTA; ranges per warp
-// Units per range at least (two per warp, or what a warp's start is worth).
-__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_CTA ? 16 : 8; }
-// What an item costs beside its units (its q, its end), in units: ranges are cut by units + this per item, so that a
-// range of many short items does not take long after the others.
-__host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_CTA ? 24 : 16; }
-constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
-
-template <int D>
-struct TCfg {
-    static constexpr int NW = D <= 128 ? 8 : 4;                   // warps per CTA
-    static constexpr int UNIT = PG_SUB * D * 2;                   // bytes of a K (or V) unit
-    static constexpr int STAGE = 2 * UNIT;
-    static constexpr int ST = D <= 64 ? 6 : D == 192 ? 4 : 3;     // stages of a warp's ring
-    static constexpr int RING = NW * ST * STAGE;
-    static constexpr int JROW = D / 2 + 4;                        // floats of a join row (half of D, padded)
-    static constexpr int JOIN = NW * 8 * JROW * 4;
-    static constexpr int OFF_JOIN = RING;
-    static constexpr int OFF_ML = OFF_JOIN + JOIN;                // [NW][16] m, then l
-    static constexpr int OFF_BAR = OFF_ML + NW * 16 * 2 * 4;
-    static constexpr int OFF_SCAN = OFF_BAR + NW * ST * 8 + 8;
-    static constexpr int OFF_PRE = OFF_SCAN + 64 * 4;             // prefix of units per sequence [B + 1]
-    static constexpr int SMEM_BASE = OFF_PRE + 1024;              // + alignment slack; + 4 (B + 1)
-};
-
-template <typename T> struct Elem;
-template <> struct Elem<__half> {
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        mma16816(c, a, b0, b1);
-    }
-    static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) { split_hi_lo(x0, x1, hi, lo); }
-    static __device__ __forceinline__ uint32_t pack(float x0, float x1) { return h2_as_u32(__floats2half2_rn(x0, x1)); }
-    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-};
-template <> struct Elem<__nv_bfloat16> {
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static __device__ __forceinline__ uint32_t pack(float x0, float x1) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
-    static __device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-        hi = pack(x0, x1);
-        lo = pack(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
-    }
-};
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* tm, int tok, int head, int page, uint32_t bar, uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
-        ::"r"(dst), "l"(tm), "r"(0), "r"(tok), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(pol) : "memory");
-}
-
-// The units (cache tiles of 16 tokens) that one sequence's row reads: tiles [0, ns) hold the sinks,
-// then come tiles [w0, w0 + n - ns). A sequence without keys has one unit with nothing visible.
-struct Span {
-    int n, ns, w0;
-};
-__device__ __forceinline__ Span span_of(int len, int window, int sinks) {
-    Span s;
-    const int end = (len + PG_SUB - 1) / PG_SUB;
-    s.ns = 0;
-    s.w0 = 0;
-    if (window > 0 && len > window) {
-        s.w0 = (len - window) / PG_SUB;
-        s.ns = min((min(sinks, len) + PG_SUB - 1) / PG_SUB, s.w0);
-    }
-    s.n = max(1, s.ns + end - s.w0);
-    return s;
-}
-
-__device__ __forceinline__ int clamp_len(const PagedAttn& P, int b, bool report) {
-    int len = P.kv_len[b];
-    const int64_t most = (int64_t)P.max_pages * P.page;
-    if (len > most) {
-        if (report) set_err(P.err, ERR_KV_LEN);
-        len = static_cast<int>(most);
-    }
-    return max(len, 0);
-}
-
-// Weight of a part with maximum m in a join at M. A part without a visible key has m = -inf and sums of 0 (or
-// NaN, from a NaN score), which weight 1 passes on.
-__device__ __forceinline__ float join_weight(float m, float M) { return m > -INFINITY ? ex2_approx(m - M) : 1.f; }
-
-// Weights of a row's own attention and of the prior in the result, and the LSE of both.
-struct RowEnd {
-    float wo, wp, lse;
-    bool prior;
-};
-__device__ __forceinline__ RowEnd row_end(const PagedAttn& P, int64_t row, float m, float l) {
-    RowEnd r;
-    const bool none = l == 0.f;
-    r.wo = none ? 0.f : 1.0f / l;
-    r.wp = 0.f;
-    r.lse = none ? -INFINITY : (m + log2f(l)) * PG_LN2;
-    r.prior = false;
-    if (P.O_prior) {
-        const float lp = P.LSE_prior[row];
-        if (lp != -INFINITY) {
-            const float mx = fmaxf(r.lse, lp);
-            const float wn = expf(r.lse - mx), wp = expf(lp - mx), sum = wn + wp;
-            r.wo *= wn / sum;
-            r.wp = wp / sum;
-            r.lse = mx + logf(sum);
-            r.prior = true;
-        }
-    }
-    return r;
-}
-
-// Elements d, d + 1 of row (t, hq), and (first) its LSE.
-template <typename T>
-__device__ __forceinline__ void finish2(const PagedAttn& P, int t, int hq, int D, int d, float a0, float a1, float m, float l,
-                                        bool first) {
-    const int64_t row = (int64_t)t * P.H_q + hq;
-    const RowEnd r = row_end(P, row, m, l);
-    a0 *= r.wo;
-    a1 *= r.wo;
-    if (r.prior) {
-        const float2 op = *reinterpret_cast<const float2*>(P.O_prior + row * D + d);
-        a0 = fmaf(op.x, r.wp, a0);
-        a1 = fmaf(op.y, r.wp, a1);
-    }
-    *reinterpret_cast<uint32_t*>(static_cast<T*>(P.O) + row * D + d) = Elem<T>::pack(a0, a1);
-    if (first && P.LSE) P.LSE[row] = r.lse;
-}
-
-// Partial of a range (two slots per range): [heads][D + 4] floats: m, l, -, -, O (not normalised).
-__host__ __device__ constexpr int slot_floats(int D, int heads) { return heads * (D + 4); }
-
-// A split item's descriptor, written by the range in which it begins (pieces = 0: none).
-struct JoinDesc {
-    int b, x, pieces, pad;
-};
-
-template <typename T, int D, int NB, int MODE>
-__global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const __grid_constant__ PagedAttn P) {
-    using C = TCfg<D>;
-    constexpr int NW = C::NW, ST = C::ST, KS = D / 16, NT = NW * 32;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t s_base = smem_u32(smem);
-    float* jbuf = reinterpret_cast<float*>(smem + C::OFF_JOIN);
-    float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
-    float* s_l = s_m + NW * 16;
-    int* s_scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
-    int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t ring = s_base + warp * ST * C::STAGE;
-    const uint32_t bar = s_base + C::OFF_BAR + warp * ST * 8;
-    if (lane == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, 1);
-        fence_mbar_init();
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_k) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_v) : "memory");
-    }
-    pdl_wait();
-    pdl_release();
-
-    // ---- the range of units of this warp (BY_WARP) or CTA
-    const int Hg = P.H_kv * P.n_groups;
-    const int B = P.B;
-    const int heads = P.heads_per_group;
-    constexpr bool SPLIT = MODE != TK_ITEM, BY_WARP = MODE == TK_WARP;
-    constexpr int TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
-    const int worker = BY_WARP ? warp * gridDim.x + blockIdx.x : blockIdx.x;    // few workers spread over the SMs
-    int workers = BY_WARP ? gridDim.x * NW : gridDim.x;
-    JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * workers * slot_floats(D, heads));
-    int64_t u0, u1;            // units of all items end to end
-    int64_t U = 0;
-    int b_first = 0;
-    if (SPLIT) {
-        // units before each sequence (per kv head and group): a scan over the lengths
-        const int per = (B + NT - 1) / NT;
-        int sum = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < B) sum += span_of(clamp_len(P, b, blockIdx.x == 0), P.window, P.sinks).n;
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        int base = 0;
-        for (int w = 0; w < warp; ++w) base += s_scan[w];
-        int run = base + inc - sum;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < B) {
-                pre[b] = run;
-                run += span_of(clamp_len(P, b, false), P.window, P.sinks).n;
-            }
-        }
-        if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
-        __syncthreads();
-        U = ((int64_t)pre[B] + (int64_t)TK_ITEM_UNITS * B) * Hg;      // the items' whole weight
-        const int64_t most = (U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
-        if (most < workers) workers = static_cast<int>(most);
-        if (worker >= workers) {
-            if (BY_WARP ? lane == 0 : tid == 0) jd[worker].pieces = 0;
-            return;
-        }
-        // the unit at which weight w falls; weights behind an item's units fall on its end
-        auto unit_at = [&](int64_t w) -> int64_t {
-            const int v = static_cast<int>(w / Hg);
-            int lo = 0, hi = B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] + TK_ITEM_UNITS * mid <= v) lo = mid;
-                else hi = mid - 1;
-            }
-            const int n = pre[lo + 1] - pre[lo], nw = n + TK_ITEM_UNITS;
-            const int64_t rem = w - ((int64_t)pre[lo] + (int64_t)TK_ITEM_UNITS * lo) * Hg;
-            const int64_t x = rem / nw;
-            return (int64_t)pre[lo] * Hg + x * n + min((int64_t)n, rem - x * nw);
-        };
-        u0 = unit_at(U * worker / workers);
-        u1 = worker + 1 < workers ? unit_at(U * (worker + 1) / workers) : (int64_t)pre[B] * Hg;
-    } else {
-        b_first = blockIdx.x / Hg;
-        const int n = span_of(clamp_len(P, b_first, true), P.window, P.sinks).n;
-        if (tid == 0) {
-            pre[0] = 0;
-            pre[1] = n;
-        }
-        __syncthreads();
-        u0 = (int64_t)(blockIdx.x - b_first * Hg) * n;
-        u1 = u0 + n;
-    }
-    const int nseq = SPLIT ? B : 1;     // sequences in pre[]
-
-    // ---- a warp's units: u0 + k of its own range, u0 + warp + k NW of its CTA's. Lane i resolves unit k0 + i: coordinates of its
-    // loads.
-    const int64_t uf = BY_WARP ? u0 : u0 + warp;
-    constexpr int STEP = BY_WARP ? 1 : NW;
-    const uint64_t pol = l2_evict_first();
-    int pl_tok = 0, pl_head = 0, pl_page = 0;
-    auto resolve = [&](int k0) {
-        const int64_t u = uf + (int64_t)(k0 + lane) * STEP;
-        if (u < u1) {
-            const int v = static_cast<int>(u / Hg);
-            int lo = 0, hi = nseq - 1;      // the sequence with pre[b] <= v < pre[b + 1]
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] <= v) lo = mid;
-                else hi = mid - 1;
-            }
-            const int b = b_first + lo;
-            const int n = pre[lo + 1] - pre[lo];
-            const int64_t rem = u - (int64_t)pre[lo] * Hg;
-            const int x = static_cast<int>(rem / n), j = static_cast<int>(rem - (int64_t)x * n);
-            const int len = clamp_len(P, b, false);
-            const Span s = span_of(len, P.window, P.sinks);
-            const int tile = j < s.ns ? j : j - s.ns + s.w0;
-            const int tok = tile * PG_SUB;
-            const int pi = tok / P.page;
-            pl_tok = tok - pi * P.page;
-            pl_head = x / P.n_groups;
-            pl_page = 0;
-            if (len > 0) {
-                const int pg = P.table[(int64_t)b * P.max_pages + pi];
-                if (pg < 0 || pg >= P.n_pages) set_err(P.err, ERR_PAGE_ID);   // and page 0 is read instead
-                else pl_page = pg;
-            }
-        }
-    };
-    const int nk = static_cast<int>(u1 > uf ? (u1 - uf + STEP - 1) / STEP : 0);   // units of this warp
-    int kp = 0;                          // next unit to load
-    auto produce = [&]() {
-        if (kp >= nk) return;
-        if ((kp & 31) == 0) resolve(kp);
-        const int tok = __shfl_sync(0xffffffffu, pl_tok, kp & 31);
-        const int head = __shfl_sync(0xffffffffu, pl_head, kp & 31);
-        const int page = __shfl_sync(0xffffffffu, pl_page, kp & 31);
-        const int st = kp % ST;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar + 8 * st, C::STAGE);
-            tma_5d(ring + st * C::STAGE, &P.tm_k, tok, head, page, bar + 8 * st, pol);
-            tma_5d(ring + st * C::STAGE + C::UNIT, &P.tm_v, tok, head, page, bar + 8 * st, pol);
-        }
-        ++kp;
-    };
-    for (int i = 0; i < ST; ++i) produce();
-
-    // ---- items of the range, in order
-    bool failed = false;
-    int k_failed = 0;                    // the unit whose copy never landed
-    int k = 0;                           // next unit to consume
-    int64_t u = u0;                      // first unit of the current piece
-    int bi = 0;                          // index into pre[] of the current sequence
-    {
-        const int v = static_cast<int>(u0 / Hg);
-        int hi = nseq - 1;
-        while (bi < hi) {
-            const int mid = (bi + hi + 1) >> 1;
-            if (pre[mid] <= v) bi = mid;
-            else hi = mid - 1;
-        }
-    }
-    bool crosses = false;                // an item begins here and goes on in the next range
-    while (u < u1) {
-        while ((int64_t)pre[bi + 1] * Hg <= u) ++bi;
-        const int b = b_first + bi;
-        const int n = pre[bi + 1] - pre[bi];
-        const int64_t first_of_b = (int64_t)pre[bi] * Hg;
-        const int x = static_cast<int>((u - first_of_b) / n);
-        const int64_t a = first_of_b + (int64_t)x * n, e = a + n;   // the item's units
-        const int64_t pe = e < u1 ? e : u1;                         // end of this range's piece
-        const int g = x / P.n_groups, grp = x - g * P.n_groups;
-        const int hq0 = g * P.G + grp * heads;
-        const int nq = min(heads, P.G - grp * heads);
-        const int len = clamp_len(P, b, false);
-        const Span sp = span_of(len, P.window, P.sinks);
-        const int lo_key = P.window > 0 && len > P.window ? len - P.window : 0;   // first key of the window
-
-        // q as the B operand: head (column) lane / 4, elements 16 s + 2 (lane % 4) and + 8
-        uint32_t qf[NB][KS][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const int col = nb * 8 + (lane >> 2);
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const T*>(P.Q) + (int64_t)b * P.q_row +
-                                                                  (int64_t)(hq0 + col) * P.q_head) + (lane & 3);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                qf[nb][s][0] = col < nq ? q[8 * s] : 0u;
-                qf[nb][s][1] = col < nq ? q[8 * s + 4] : 0u;
-            }
-        }
-        float o[NB][KS][4];
-        float m[NB][2], l[NB][2];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            m[nb][0] = m[nb][1] = -INFINITY;
-            l[nb][0] = l[nb][1] = 0.f;
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nb][s][i] = 0.f;
-        }
-        for (; k < nk; ++k) {
-            const int64_t uk = uf + (int64_t)k * STEP;
-            if (uk >= pe) break;
-            const int j = static_cast<int>(uk - a);
-            const int tile = j < sp.ns ? j : j - sp.ns + sp.w0;
-            const int st = k % ST;
-            const uint32_t ks = ring + st * C::STAGE, vs = ks + C::UNIT;
-            if (!failed && !__all_sync(0xffffffffu, mbar_wait_bounded(bar + 8 * st, (k / ST) & 1))) {
-                failed = true;
-                k_failed = k;
-            }
-            if (failed) continue;
-            // visible keys of the tile: token t of it is key key0 + t
-            const int key0 = tile * PG_SUB;
-            const bool full = key0 + PG_SUB <= len && (key0 >= lo_key || key0 + PG_SUB <= P.sinks);
-            auto seen = [&](int t) { return key0 + t < len && (key0 + t >= lo_key || key0 + t < P.sinks); };
-            if (!full) {
-                // hidden V rows may hold anything (also NaN, which 0 * v would keep): zero them
-                for (int t = 0; t < PG_SUB; ++t)
-                    if (!seen(t))
-                        for (int c = lane; c < D / 8; c += 32)
-                            *reinterpret_cast<uint4*>(smem + (vs - s_base) + (c >> 3) * (PG_SUB * 128) + t * 128 + (c & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            // S^T = K q^T
-            float s4[NB][4];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s4[nb][i] = 0.f;
-            {
-                const int r = lane & 15, half = lane >> 4;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int c = 2 * s + half;
-                    uint32_t af[4];
-                    ldsm_x4(ks + (c >> 3) * (PG_SUB * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), af);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) Elem<T>::mma(s4[nb], af, qf[nb][s][0], qf[nb][s][1]);
-                }
-            }
-            // lane: tokens lane / 4 and + 8, heads 2 (lane % 4) and + 1 of each column block
-            const int t0 = lane >> 2;
-            bool up = false;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = s4[nb][i] * P.scale_log2;
-                    if (!full && !seen(t0 + (i >> 1) * 8)) v = -INFINITY;
-                    s4[nb][i] = v;
-                    up |= !(v <= m[nb][i & 1] + 8.f);   // (a NaN too)
-                }
-            if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(s4[nb][i], s4[nb][i + 2]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mx, m[nb][i]);
-                        const float al = m[nb][i] > -INFINITY ? ex2_approx(m[nb][i] - mx) : 0.f;
-                        m[nb][i] = mx;
-                        l[nb][i] *= al;
-#pragma unroll
-                        for (int s = 0; s < KS; ++s) {
-                            o[nb][s][i] *= al;
-                            o[nb][s][i + 2] *= al;
-                        }
-                    }
-            }
-            // p, its sum, and its transpose (tokens as k) as hi + lo B fragments
-            uint32_t ph[NB][2], plo[NB][2];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = ex2_approx(s4[nb][2 * r] - (m[nb][0] > -INFINITY ? m[nb][0] : 0.f));
-                    const float p1 = ex2_approx(s4[nb][2 * r + 1] - (m[nb][1] > -INFINITY ? m[nb][1] : 0.f));
-                    l[nb][0] += p0;
-                    l[nb][1] += p1;
-                    uint32_t hi, lo;
-                    Elem<T>::split(p0, p1, hi, lo);
-                    ph[nb][r] = movmatrix_trans(hi);
-                    plo[nb][r] = movmatrix_trans(lo);
-                }
-            // O^T += V^T p^T
-            {
-                const int r = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int c = 2 * s + half;
-                    uint32_t af[4];
-                    ldsm_x4_t(vs + (c >> 3) * (PG_SUB * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), af);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        Elem<T>::mma(o[nb][s], af, ph[nb][0], ph[nb][1]);
-                        Elem<T>::mma(o[nb][s], af, plo[nb][0], plo[nb][1]);
-                    }
-                }
-            }
-            __syncwarp();
-            produce();
-        }
-        // the rows' sums, in every lane of a head's eight
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 4);
-                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 8);
-                l[nb][i] += __shfl_xor_sync(0xffffffffu, l[nb][i], 16);
-            }
-        const bool whole = a >= u0 && e <= u1;
-        float* part = P.ws + (size_t)(a < u0 ? 2 * worker : 2 * worker + 1) * slot_floats(D, heads);
-        if (SPLIT && a >= u0 && e > u1) {
-            crosses = true;
-            // the item's last unit, of weight w, lies in the last range that begins at w or before
-            const int64_t w = e - 1 + (int64_t)TK_ITEM_UNITS * ((int64_t)bi * Hg + x);
-            const int last = static_cast<int>(((w + 1) * workers - 1) / U);
-            if (BY_WARP ? lane == 0 : tid == 0) jd[worker] = JoinDesc{b, x, last - worker + 1, 0};
-        }
-        if (BY_WARP) {
-            // the warp's own: the result, or a partial. Lane: heads 2 (lane % 4) + i, elements lane / 4 + 8 q.
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int lh = nb * 8 + 2 * (lane & 3) + i;
-                    if (lh >= nq) continue;
-                    if (whole) {
-                        const int64_t row = (int64_t)b * P.H_q + hq0 + lh;
-                        const RowEnd r = row_end(P, row, m[nb][i], l[nb][i]);
-                        T* out = static_cast<T*>(P.O) + row * D + (lane >> 2);
-                        const float* op = P.O_prior + row * D + (lane >> 2);
-#pragma unroll
-                        for (int s = 0; s < KS; ++s)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                float v = o[nb][s][2 * q + i] * r.wo;
-                                if (r.prior) v = fmaf(op[16 * s + 8 * q], r.wp, v);
-                                out[16 * s + 8 * q] = Elem<T>::from(v);
-                            }
-                        if (lane < 4 && P.LSE) P.LSE[row] = r.lse;
-                    } else {
-                        float* pr = part + lh * (D + 4);
-#pragma unroll
-                        for (int s = 0; s < KS; ++s)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) pr[4 + 16 * s + 8 * q + (lane >> 2)] = o[nb][s][2 * q + i];
-                        if (lane < 4) *reinterpret_cast<float2*>(pr) = make_float2(m[nb][i], l[nb][i]);
-                    }
-                }
-        } else {
-            // the CTA's warps join: maxima and sums first, then O in two halves of D per column block
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (lane < 4) {
-                        s_m[warp * 16 + nb * 8 + 2 * lane + i] = m[nb][i];
-                        s_l[warp * 16 + nb * 8 + 2 * lane + i] = l[nb][i];
-                    }
-            __syncthreads();
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float al[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * (lane & 3) + i]);
-                    al[i] = join_weight(m[nb][i], M);
-                }
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float* row = jbuf + (warp * 8 + 2 * (lane & 3)) * C::JROW + (lane >> 2);
-#pragma unroll
-                    for (int s = 0; s < KS / 2; ++s) {
-                        const float (&v)[4] = o[nb][hf * (KS / 2) + s];
-                        row[16 * s] = v[0] * al[0];
-                        row[C::JROW + 16 * s] = v[1] * al[1];
-                        row[16 * s + 8] = v[2] * al[0];
-                        row[C::JROW + 16 * s + 8] = v[3] * al[1];
-                    }
-                    __syncthreads();
-                    for (int i = tid; i < 8 * (D / 4); i += NT) {   // (head, pair of elements)
-                        const int h = i / (D / 4), d = 2 * (i - h * (D / 4));
-                        const int lh = nb * 8 + h;
-                        if (lh < nq) {
-                            float M = -INFINITY, L = 0.f;
-#pragma unroll
-                            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
-                            float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-                            for (int w = 0; w < NW; ++w) {
-                                const float mw = s_m[w * 16 + lh];
-                                L += s_l[w * 16 + lh] * join_weight(mw, M);
-                                const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * 8 + h) * C::JROW + d);
-                                a0 += f.x;
-                                a1 += f.y;
-                            }
-                            const int dd = hf * (D / 2) + d;
-                            if (!SPLIT || whole) {
-                                finish2<T>(P, b, hq0 + lh, D, dd, a0, a1, M, L, dd == 0);
-                            } else {
-                                float* pr = part + lh * (D + 4);
-                                *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
-                                if (dd == 0) *reinterpret_cast<float2*>(pr) = make_float2(M, L);
-                            }
-                        }
-                    }
-                    __syncthreads();
-                }
-            }
-        }
-        u = pe;
-    }
-    if (SPLIT && !crosses && (BY_WARP ? lane == 0 : tid == 0)) jd[worker].pieces = 0;
-    if (failed) {
-        set_err(P.err, ERR_PAGED_TOKEN);
-        for (k = k_failed; k < kp; ++k)   // copies still in flight, waited for with the same limit
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + 8 * (k % ST), (k / ST) & 1))) break;
-    }
-}
-
-// Joins the partials of a split item: CTA (c, h, w) takes the one that begins in range w gridDim.x + c, if any, q head h
-// of it; 256 / (D/4) pieces at a time, one float4 of the row a thread.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_constant__ PagedAttn P) {
-    constexpr int LP = D / 4, NP = 256 / LP;
-    __shared__ float4 s_acc[NP][LP];
-    pdl_wait();
-    pdl_release();
-    const int h = blockIdx.y, c = blockIdx.z * gridDim.x + blockIdx.x;
-    const int heads = P.heads_per_group;
-    const JoinDesc d = reinterpret_cast<const JoinDesc*>(P.ws + (size_t)2 * gridDim.x * gridDim.z * slot_floats(D, heads))[c];
-    if (d.pieces == 0) return;
-    const int g = d.x / P.n_groups, grp = d.x - g * P.n_groups;
-    if (grp * heads + h >= P.G) return;
-    const int hq = g * P.G + grp * heads + h;
-    const int tid = threadIdx.x, pp = tid / LP, q = tid - pp * LP;
-    // piece i: slot 2 c + 1 for the first, 2 (c + i) for the others
-    auto part = [&](int i) { return P.ws + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_floats(D, heads) + h * (D + 4); };
-    float M = -INFINITY;
-    for (int i = tid & 31; i < d.pieces; i += 32) M = fmaxf(M, part(i)[0]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int i = tid & 31; i < d.pieces; i += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(part(i));
-        L += ml.y * join_weight(ml.x, M);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (pp < NP) {
-#pragma unroll 4
-        for (int i = pp; i < d.pieces; i += NP) {
-            const float* p = part(i);
-            const float4 v = *reinterpret_cast<const float4*>(p + 4 + 4 * q);
-            const float w = join_weight(p[0], M);
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
-        }
-        s_acc[pp][q] = acc;
-    }
-    __syncthreads();
-    if (tid < LP) {
-        float4 a = s_acc[0][tid];
-#pragma unroll
-        for (int i = 1; i < NP; ++i) {
-            const float4 v = s_acc[i][tid];
-            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-        }
-        finish2<T>(P, d.b, hq, D, 4 * tid, a.x, a.y, M, L, tid == 0);
-        finish2<T>(P, d.b, hq, D, 4 * tid + 2, a.z, a.w, M, L, false);
-    }
-}
-
-template <typename T, int D, int NB, int MODE>
-cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
-    using C = TCfg<D>;
-    static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
-    const cudaError_t e0 = allow_smem<paged_token_kernel<T, D, NB, MODE>>(C::SMEM_BASE + 4 * (TK_MAX_B + 1), p.device);
-    if (e0 != cudaSuccess) return e0;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_ctas);
-    cfg.blockDim = dim3(C::NW * 32);
-    cfg.dynamicSmemBytes = C::SMEM_BASE + 4 * ((MODE != TK_ITEM ? p.B : 1) + 1);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token_kernel<T, D, NB, MODE>, p);
-    if (e != cudaSuccess || MODE == TK_ITEM) return e;
-    cfg.gridDim = dim3(p.n_ctas, p.heads_per_group, MODE == TK_WARP ? C::NW : 1);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, paged_token_join_kernel<T, D>, p);
-}
-
-template <typename T, int D, int NB>
-cudaError_t launch_s(PagedAttn& p, cudaStream_t st) {
-    return p.mode == TK_WARP ? launch_t<T, D, NB, TK_WARP>(p, st) : p.mode == TK_CTA ? launch_t<T, D, NB, TK_CTA>(p, st) : launch_t<T, D, NB, TK_ITEM>(p, st);
-}
-
-template <typename T>
-cudaError_t launch_d(PagedAttn& p, int D, cudaStream_t st) {
-    const bool two = p.heads_per_group > 8;
-    switch (D) {
-        case 64: return two ? launch_s<T, 64, 2>(p, st) : launch_s<T, 64, 1>(p, st);
-        case 128: return two ? launch_s<T, 128, 2>(p, st) : launch_s<T, 128, 1>(p, st);
-        case 192: return launch_s<T, 192, 1>(p, st);
-        case 256: return launch_s<T, 256, 1>(p, st);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
-}  // namespace
 
 bool paged_token_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 
-// How a call is cut; fills heads_per_group, n_groups, mode and n_ctas, and returns the workspace
+// Columns (rows x q heads of a kv head) that a work item can have.
+static int token_cols(int D) { return D <= 128 ? 16 : 8; }
+bool paged_token_rows_ok(int G, int max_rows, int D) { return paged_token_dim_ok(D) && (int64_t)G * max_rows <= token_cols(D); }
+
+// How a call is cut; fills heads_per_group, n_groups, cols, mode and n_ctas, and returns the workspace
 // bytes. Up to 8 q heads (16 at D <= 128) share a work item and one read of the kv head; more are
-// split evenly into several items.
+// split evenly into several items. A few rows of a sequence share it as well.
 size_t paged_token_plan(PagedAttn& p, int D, int sms) {
-    const int most = D <= 128 ? 16 : 8;
-    p.n_groups = (p.G + most - 1) / most;
+    const int most = token_cols(D);
+    const int rows = p.cu_rows ? p.max_rows : 1;
+    p.n_groups = (p.G * rows + most - 1) / most;       // 1 with more than one row
     p.heads_per_group = (p.G + p.n_groups - 1) / p.n_groups;
+    p.cols = p.heads_per_group * rows;
     int64_t bound = ((int64_t)p.max_pages * p.page + PG_SUB - 1) / PG_SUB;   // units of one item
     if (p.window > 0) {
-        const int64_t w = ((int64_t)p.window + PG_SUB - 1) / PG_SUB + 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;
+        const int64_t w = ((int64_t)p.window + rows + PG_SUB - 1) / PG_SUB + 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;
         if (w < bound) bound = w;
     }
     const int64_t items = (int64_t)p.B * p.H_kv * p.n_groups;
     p.mode = bound <= TK_DIRECT_UNITS ? TK_ITEM : items <= (int64_t)TK_FEW_ITEMS * sms ? TK_CTA : TK_WARP;
     p.n_ctas = p.mode == TK_ITEM ? static_cast<int>(items) : sms;
     const size_t ranges = p.mode == TK_ITEM ? 0 : (size_t)p.n_ctas * (p.mode == TK_CTA ? 1 : D <= 128 ? TCfg<128>::NW : TCfg<256>::NW);
-    return ranges * (2 * slot_floats(D, p.heads_per_group) * sizeof(float) + sizeof(JoinDesc));
+    return ranges * (2 * slot_floats(D, p.cols) * sizeof(float) + sizeof(JoinDesc));
 }
 
 cudaError_t launch_paged_token(PagedAttn& p, int D, cudaStream_t st) {
-    return p.dtype == PCK_DT_F16 ? launch_d<__half>(p, D, st) : launch_d<__nv_bfloat16>(p, D, st);
+    return p.dtype == PCK_DT_F16 ? launch_d<__half>(p, D, st) : launch_paged_token_bf16(p, D, st);
 }
 
 }  // namespace pck

@@ -18,7 +18,7 @@ def _cu(news):
 
 
 def _case(ctx, lens, news, H_q, H_kv, D, page, dtype, W=0, sinks=0, prior=False, nhd=False, seed=1, pad=0, scale=1.0, width=None,
-          max_rows=None):
+          max_rows=None, split_p=False):
     need_gpu()
     pg = ref.Pages(seed, lens, H_kv, D, page, dtype, nhd=nhd, width=width)
     T = sum(news)
@@ -35,7 +35,7 @@ def _case(ctx, lens, news, H_q, H_kv, D, page, dtype, W=0, sinks=0, prior=False,
     kw = dict(cu_rows=_cu(news), window=W, sinks=sinks, prior=pr, max_rows=max_rows)
     ctx.paged_attend(c, pg.table, pg.lens, Q, O=O, LSE=L, **kw)
     want = ref.attend(pg.k, pg.v, pg.table, lens, news, Q[:T], W, sinks, None if pr is None else (pr[0][:T], pr[1][:T]))
-    ref.check_attend(O[:T], L[:T], want, dtype, ref.P_ONCE[dtype], f"lens {lens[:4]} news {news[:4]} D {D} W {W}")
+    ref.check_attend(O[:T], L[:T], want, dtype, (ref.P_SPLIT if split_p else ref.P_ONCE)[dtype], f"lens {lens[:4]} news {news[:4]} D {D} W {W}")
     assert (O[T:] == 5).all() and (L[T:] == 6).all()       # rows behind the last sequence, left as they were
     O2, L2 = ctx.paged_attend(c, pg.table, pg.lens, Q, **kw)
     assert torch.equal(O[:T], O2[:T]) and torch.equal(L[:T], L2[:T])
@@ -74,6 +74,18 @@ def test_few_rows_over_a_long_cache(ctx, dtype, lens, news, H_q, H_kv, D, page, 
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("H_q,H_kv,D,rows", [(4, 1, 64, 4), (8, 2, 128, 2), (6, 2, 128, 5), (4, 1, 128, 1), (8, 8, 128, 16), (8, 2, 192, 2),
+                                             (2, 1, 256, 4), (3, 3, 256, 7)])
+def test_a_few_rows(ctx, dtype, H_q, H_kv, D, rows):   # noqa: F811
+    """Rows that share the one-token kernel's columns: a CTA per item, a range per CTA, a range per warp."""
+    few = [min(rows, n) for n in (1, 2, rows, rows, 0, rows)]
+    for lens, news in (([1, 17, 500, 33, 0, 2], few), ([1, 17, 5000, 33, 9, 2], few), ([(31 * i * i) % 900 for i in range(330)], [i % (rows + 1) for i in range(330)])):
+        lens = [max(n, m) if i % 3 else n for i, (n, m) in enumerate(zip(lens, news))]     # some rows in front of their cache
+        for kw in (dict(), dict(W=40, sinks=5, prior=True, nhd=True, pad=2), dict(W=1, sinks=0)):
+            _case(ctx, lens, news, H_q, H_kv, D, 16, dtype, max_rows=rows, split_p=True, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
 def test_rows_large_scores(ctx, dtype):   # noqa: F811
     """Scores in the hundreds, and scores that grow along the cache so that every block moves the maximum."""
     _case(ctx, [700], [500], 4, 2, 128, 16, dtype, scale=20.0)
@@ -86,7 +98,8 @@ def test_rows_large_scores(ctx, dtype):   # noqa: F811
         ref.check_attend(O, L, ref.attend(pg.k, pg.v, pg.table, [1500], [rows], Q), dtype, ref.P_ONCE[dtype])
 
 
-@pytest.mark.parametrize("rows,width,W,sinks", [(300, None, 0, 0), (20, 3000, 0, 0), (300, None, 60, 5), (20, 3000, 600, 2)])
+@pytest.mark.parametrize("rows,width,W,sinks", [(300, None, 0, 0), (20, 3000, 0, 0), (300, None, 60, 5), (20, 3000, 600, 2), (8, None, 0, 0),
+                                                (8, None, 20, 5), (8, 3000, 700, 2)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_a_value_that_is_not_finite_stays_with_the_rows_that_see_it(ctx, rows, width, W, sinks, bad):   # noqa: F811
     """V (or K) of one token is not finite: rows that do not see it are as if it were not there."""
@@ -96,12 +109,12 @@ def test_a_value_that_is_not_finite_stays_with_the_rows_that_see_it(ctx, rows, w
     c = binding.PagedCache(pg.k, pg.v)
     at = torch.arange(n - rows, n, device="cuda")
     for which in ("v", "k"):
-        for j in (n - rows + 13, n - 30, n - 7, 1):
+        for j in (max(n - rows, n - rows + 13 if rows > 13 else n - 3), n - 30, n - 7, 1):
             t = getattr(pg, which)
             page, slot = int(pg.table[0, j // 16]), j % 16
             old = t[page, :, slot].clone()
             t[page, :, slot, 3] = bad
-            O, L = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu([rows]), window=W, sinks=sinks)
+            O, L = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu([rows]), max_rows=rows, window=W, sinks=sinks)
             t[page, :, slot] = old
             see = at >= j
             if W:
@@ -150,11 +163,12 @@ def test_rows_out_of_range_are_reported(ctx):   # noqa: F811
         assert "code 8" in code(c, t, pg.lens, Q, cu_rows=cu)
     assert "code 10" in code(c, pg.table, pg.lens + 500, Q, cu_rows=cu)
     assert "code 10" in code(c, pg.table, pg.lens, Q, cu_rows=cu, max_rows=10)
+    assert "code 10" in code(c, pg.table, pg.lens, Q, cu_rows=cu, max_rows=4)
     O2, L2 = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=cu)
     assert torch.equal(O, O2) and torch.equal(L, L2)
     with pytest.raises(binding.PckError) as e:
         d = torch.zeros((3, 1, 16, 256), dtype=F16, device="cuda")
-        ctx.paged_attend(binding.PagedCache(d, d), pg.table, pg.lens, _rand(1, 320, 2, 256, dtype=F16), cu_rows=cu)
+        ctx.paged_attend(binding.PagedCache(d, d), pg.table, pg.lens, _rand(1, 320, 2, 256, dtype=F16), cu_rows=cu, max_rows=5)
     assert e.value.code == binding.EUNSUPPORTED
     with pytest.raises(binding.PckError) as e:
         ctx.paged_attend(c, pg.table, pg.lens, _rand(1, 320, 2 * 129, 64, dtype=F16), cu_rows=cu)
