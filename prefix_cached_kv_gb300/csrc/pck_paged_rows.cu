@@ -978,9 +978,10 @@ size_t paged_rows_plan(PagedAttn& p, int D, int sms) {
     // at most, whatever the sequences' shares
     p.row_tiles = static_cast<int>(std::min<int64_t>(p.T / tt + p.B, (int64_t)p.B * ((p.max_rows + tt - 1) / tt)));
     p.box = paged_rows_box(p.page);
-    // Keys are split when the row tiles leave SMs idle: as many splits as fill them once, each of at least
-    // 4 blocks of the longest cache the table can hold.
-    const int64_t ctas = std::min<int64_t>((p.T + tt - 1) / tt, p.row_tiles) * p.H_kv;
+    // Keys are split when the row tiles leave SMs idle: as many splits as fill them once, each of at least 4 blocks
+    // of the longest cache the table can hold. The tiles are taken as those of full ones, or one per sequence.
+    const int64_t tiles = std::max<int64_t>((p.T + tt - 1) / tt, std::min(p.B, p.T));
+    const int64_t ctas = std::min<int64_t>(tiles, p.row_tiles) * p.H_kv;
     int64_t bound = (int64_t)p.max_pages * p.page;
     if (p.window > 0) {
         const int64_t w = (int64_t)p.window + tt + p.sinks + 2 * p.box;
