@@ -17,6 +17,8 @@ its own roofline fraction.
 ``--impl reference`` times the CPU oracle (test infrastructure) on all the host cores on the
 same workload and prints the same line with ``"impl": "reference"``. ``--profile ROW`` runs each
 kernel of one row once, at a size meant for an Nsight Compute capture, and prints nothing else.
+``--rows paged`` reports the paged-tail operators (head norms with rotary positions, append, attention
+over pages) over the cases of perf/operators.py instead.
 """
 import os
 
@@ -563,7 +565,46 @@ def row_prefill(ctx, torch, pk, reps=10, fmt=0):
             "frac_tensor_bf16_peak": round(tf / pk["bf16"], 4), "gflop_per_layer": round(flops_layer / 1e9, 3)}
 
 
+def paged_case(name):
+    """A case of perf/operators.py with the framework's calls: the module and the case."""
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.own = True
+    return mod, [c for c in mod.listed() if name is None or c["name"] == name]
+
+
+def row_paged(ctx, torch, pk, calls=12):
+    """The paged-tail operators over the cases of perf/operators.py: device time per call in a captured graph of 12
+    calls that rotate over three states, against the larger of the bytes' and the operations' time at the measured peaks.
+    (States of the largest cases are larger than L2; the smallest are launch-bound whatever the cache holds.)"""
+    mod, cases = paged_case(None)
+    out = {}
+    for c in cases:
+        states = [mod.prepare(c, k) for k in range(3)]
+        for s in states:
+            mod.run(s)
+        torch.cuda.synchronize()
+        g = graph_of(torch, lambda: [mod.run(states[i % 3]) for i in range(calls)])
+        for _ in range(3):
+            g.replay()
+        us = statistics.median(time_replays(torch, g, 1) for _ in range(9)) / calls * 1e3
+        w = mod.work(c)
+        floor = max(w["bytes"] / pk["hbm"] / 1e3, w["flops"] / pk["bf16"] / 1e6)
+        out[c["name"]] = {"us": round(us, 2), "floor_us": round(floor, 2), "frac_of_floor": round(floor / us, 3)}
+        del g, states
+        torch.cuda.empty_cache()
+    mod._ctx().sync()
+    return out
+
+
 # ------------------------------------------------------------------ single launches for Nsight Compute
+
+# profile rows of the paged tail: cases of perf/operators.py
+PAGED_PROFILES = {"norm_rope": "norm_rope long prompt", "paged_append": "append ragged prompts",
+                  "paged_token": "token, ragged batch, prefix", "paged_rows": "prompts, window and sinks"}
+
 
 def profile_row(row, ctx, torch):
     """Run each kernel of one row twice (the first launch sets kernel attributes; capture the
@@ -571,7 +612,8 @@ def profile_row(row, ctx, torch):
     64-session fp16 M=1 batch; sparse = a 16-session pck_query_sparse_batch (scoring, selection,
     gather decode, merge); quant = one cartridge layer's K and V (354 MB in); warm = the same
     layer's records dequantised to fp16; prefill = one batched-Q layer (fp16 prefix);
-    prefill_mlx = the same over an mlx4g32 prefix."""
+    prefill_mlx = the same over an mlx4g32 prefix; norm_rope, paged_append, paged_token and paged_rows = one call of
+    that paged-tail operator."""
     from prefix_cached_kv_gb300 import binding, synth
     if row == "fp16":
         H, N, D, R = 8, 2048, 128, 64
@@ -616,6 +658,10 @@ def profile_row(row, ctx, torch):
         Ks = torch.randn((H_kv, S, D), device="cuda").half()
         Vs = torch.randn((H_kv, S, D), device="cuda").half()
         fn = lambda: ctx.query_fused("pp", 0, Q, Ks, Vs)
+    elif row in PAGED_PROFILES:
+        mod, (case,) = paged_case(PAGED_PROFILES[row])
+        state = mod.prepare(case, 0)
+        fn = lambda: mod.run(state)
     else:
         raise SystemExit(f"unknown profile row {row}")
     torch.cuda.synchronize()
@@ -790,9 +836,11 @@ def main():
     ap.add_argument("--warmup", type=int, default=20)
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--rows", default="all",
-                    help="all | comma list of main,fp16,dims,sparse,prefill,prefill_mlx,cartridge (main = the headline line)")
+                    help="all | comma list of main,fp16,dims,sparse,prefill,prefill_mlx,cartridge (main = the headline line), "
+                         "and paged (not in all): the paged-tail operators")
     ap.add_argument("--profile", default=None,
-                    help="fp16 | sparse | quant | warm | prefill | prefill_mlx: one capture-sized run of that row")
+                    help="fp16 | sparse | quant | warm | prefill | prefill_mlx | norm_rope | paged_append | paged_token | "
+                         "paged_rows: one capture-sized run of that row")
     args = ap.parse_args()
     if args.impl == "reference":
         run_reference(args)
@@ -836,6 +884,8 @@ def main():
         rows["N3_batched_q_mlx4g32"] = row_prefill(ctx, torch, pk, fmt=1)
     if "cartridge" in want:
         rows["A1_A3_N2_cartridge"] = row_cartridge(ctx, torch, pk)
+    if "paged" in want:
+        rows["paged_tail"] = row_paged(ctx, torch, pk)
     ctx.close()
     if rank() != 0:
         return
