@@ -315,7 +315,7 @@ typedef struct pck_paged_cache {
  * last ones of its kv_len[b] cached tokens: row i of its n rows stands at cache position
  * kv_len[b] - n + i, and token p of the cache lies in page table[b][p / page_size], slot
  * p % page_size. Table entries that no visible token needs are not read. cu_rows NULL: one row per
- * sequence (T == B). Rows with a negative cache position (a padded sequence of length 0) see and
+ * sequence (T == B). max_pages * page_size is at most 2^30. Rows with a negative cache position (a padded sequence of length 0) see and
  * store nothing. */
 typedef struct pck_paged_batch {
     int B, T;

@@ -420,7 +420,11 @@ int ctx_fail(pck_ctx* c, int code, const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    return fail(c, code, "%s", buf);
+    try {
+        return fail(c, code, "%s", buf);
+    } catch (...) {     // no memory for the text
+        return code;
+    }
 }
 
 void ctx_count_query(pck_ctx* c) { ++c->queries; }

@@ -126,6 +126,9 @@ inline cudaError_t allow_smem(int bytes, int device) {
     return e;
 }
 
+// Orders this thread's earlier view of memory (ordinary loads and stores) before its later TMA accesses.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

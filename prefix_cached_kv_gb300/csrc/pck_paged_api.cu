@@ -27,6 +27,8 @@ struct DeviceScope {
     }
 };
 
+constexpr int MAX_TOKENS = 1 << 30;     // of one sequence, by the table's width; windows and sinks are cut to it
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool stride_ok(int64_t s, int64_t extent, int elems) { return extent <= 1 || (s > 0 && s % elems == 0 && s < (int64_t(1) << 36)); }
 
@@ -86,7 +88,7 @@ int check_batch(pck_ctx* c, const pck_paged_batch* b, int page_size) {
     if (b->B > PCK_PAGED_MAX_BATCH) return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d above %d", b->B, PCK_PAGED_MAX_BATCH);
     if (b->B == 0 || b->T == 0) return PCK_OK;
     if (!b->kv_len || !b->table) return ctx_fail(c, PCK_EINVAL, "NULL kv_len or table");
-    if (b->max_pages < 1 || (int64_t)b->max_pages * page_size >= (int64_t(1) << 31))
+    if (b->max_pages < 1 || (int64_t)b->max_pages * page_size > MAX_TOKENS)
         return ctx_fail(c, PCK_EINVAL, "max_pages=%d out of range", b->max_pages);
     if (b->max_rows < 1) return ctx_fail(c, PCK_EINVAL, "max_rows=%d", b->max_rows);
     if (!b->cu_rows && b->T != b->B)
@@ -175,14 +177,14 @@ int attend_shape(pck_ctx* c, const pck_paged_cache* k, const pck_paged_batch* b,
     p.page = k->page_size;
     p.max_pages = b->max_pages;
     p.n_pages = static_cast<int>(k->n_pages);
-    p.window = window;
-    p.sinks = sinks;
+    p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
+    p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
     p.cu_rows = b->cu_rows;
     p.max_rows = b->max_rows < b->T ? b->max_rows : b->T;
     p.dtype = k->dtype;
-    if ((int64_t)b->B * (((int64_t)b->max_pages * k->page_size + PG_SUB - 1) / PG_SUB + 1) >= (int64_t(1) << 31))
+    if ((int64_t)b->B * (((int64_t)b->max_pages * k->page_size + PG_SUB - 1) / PG_SUB + 64) >= (int64_t(1) << 31))
         return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld tokens", b->B, (long long)b->max_pages * k->page_size);
-    if ((int64_t)b->T * H_q >= (int64_t(1) << 31) / 16) return ctx_fail(c, PCK_EUNSUPPORTED, "T=%d, H_q=%d", b->T, H_q);
+    if ((int64_t)b->T * H_q >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EUNSUPPORTED, "T=%d, H_q=%d", b->T, H_q);
     return PCK_OK;
 }
 

@@ -219,44 +219,61 @@ struct RowTile {
     int len;        // its cached tokens, as given
 };
 
-// The sequence and rows of CTA tile `idx` (tiles of tt rows, the sequences' tiles end to end). One warp.
-__device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt, int lane) {
-    int before = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-        const int b = b0 + lane;
-        int r0 = 0, n = 0, len = 0;
-        if (b < P.B) {
-            len = P.kv_len[b];
-            r0 = P.cu_rows[b];
-            n = max(0, P.cu_rows[b + 1] - r0);
-        }
-        const int nt = (n + tt - 1) / tt;
-        int inc = nt;
+// The sequence and rows of CTA tile `idx` (tiles of tt rows, the sequences' tiles end to end). One warp; PER sequences a
+// lane at a time. (Row counts that make no sense, from a cu_rows that does not ascend, give some tile or none: the
+// caller checks every index that follows from it.)
+template <int PER>
+__device__ __forceinline__ RowTile find_tile_by(const PagedAttn& P, int idx, int tt, int lane) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32 * PER) {
+        const int bl = b0 + lane * PER;
+        int cu[PER + 1], len[PER];
+#pragma unroll
+        for (int i = 0; i <= PER; ++i) cu[i] = P.cu_rows[min(bl + i, P.B)];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) len[i] = PER == 1 && bl + i < P.B ? P.kv_len[bl + i] : 0;   // many: loaded once found
+        int64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sum += (max(0, cu[i + 1] - cu[i]) + (int64_t)tt - 1) / tt;
+        int64_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
         const unsigned hit = __ballot_sync(0xffffffffu, idx < before + inc);
         if (hit) {
             const int w = __ffs(hit) - 1;
-            RowTile t;
-            t.b = b0 + w;
-            t.tok0 = (idx - before - __shfl_sync(0xffffffffu, inc - nt, w)) * tt;
-            t.n = __shfl_sync(0xffffffffu, n, w);
-            t.row0 = __shfl_sync(0xffffffffu, r0, w);
-            t.len = __shfl_sync(0xffffffffu, len, w);
+            RowTile t = {-1, 0, 0, 0, 0};
+            if (lane == w) {
+                int64_t at = idx - before - (inc - sum);     // tile of the lane's sequences
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int n = max(0, cu[i + 1] - cu[i]);
+                    const int64_t nt = (n + (int64_t)tt - 1) / tt;
+                    if (t.b < 0 && at < nt) t = RowTile{bl + i, static_cast<int>(at * tt), n, cu[i], PER == 1 ? len[i] : P.kv_len[bl + i]};
+                    at -= nt;
+                }
+            }
+            t.b = __shfl_sync(0xffffffffu, t.b, w);
+            t.tok0 = __shfl_sync(0xffffffffu, t.tok0, w);
+            t.n = __shfl_sync(0xffffffffu, t.n, w);
+            t.row0 = __shfl_sync(0xffffffffu, t.row0, w);
+            t.len = __shfl_sync(0xffffffffu, t.len, w);
             return t;
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
     return RowTile{-1, 0, 0, 0, 0};
 }
+__device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt, int lane) {
+    return P.B <= 32 ? find_tile_by<1>(P, idx, tt, lane) : find_tile_by<8>(P, idx, tt, lane);
+}
 
 // Whether the sequences' tiles are more than the grid was made for: some sequence has more rows than max_rows.
 __device__ __forceinline__ bool too_many_rows(const PagedAttn& P, int tt, int lane) {
     int64_t total = 0;
-    for (int b = lane; b < P.B; b += 32) total += (max(0, P.cu_rows[b + 1] - P.cu_rows[b]) + tt - 1) / tt;
+    for (int b = lane; b < P.B; b += 32) total += (max(0, P.cu_rows[b + 1] - P.cu_rows[b]) + (int64_t)tt - 1) / tt;
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     return total > P.row_tiles;
@@ -450,6 +467,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     }
     pdl_wait();
     pdl_release();
+    fence_proxy_async_all();     // the pages may have been written by the kernel before, and are read by TMA
     if (warp == RW_LOAD_WARP) {
         const RowTile t = find_tile(P, tile_idx, tt, lane);
         if (lane == 0) *s_tile = t;
@@ -468,6 +486,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
             if (tid == 0) set_err(P.err, ERR_KV_LEN);
             len = P.max_pages * P.page;
         }
+        len = max(len, 0);
         const int rows_here = min(rt.n - rt.tok0, tt);          // rows (tokens) of this CTA
         const int ntile = rows_here > tpt ? 2 : 1;
         const int p0 = len - rt.n + rt.tok0, p1 = p0 + rows_here - 1;
@@ -655,7 +674,8 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 // -------------------------------------------------------- softmax: row r of tile t
                 const int t = warp >> 2, r = (warp & 3) * 32 + lane;
                 const int rtok = t * tpt + r / G;                     // token of the CTA
-                const bool row_ok = r < tpt * G && rtok < rows_here && rt.row0 + rt.tok0 + rtok < P.T && rt.row0 >= 0;
+                const int64_t trow = (int64_t)rt.row0 + rt.tok0 + rtok;
+                const bool row_ok = r < tpt * G && rtok < rows_here && trow >= 0 && trow < P.T;
                 const int p = row_ok ? p0 + rtok : -1;
                 const int hq = g * G + r % G;
                 // positions of the tile's first and last rows
@@ -809,8 +829,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 // the record of spoilt keys is complete
                 asm volatile("barrier.cta.sync %0, 192;" ::"r"(1 + t) : "memory");
                 if (!failed) {
-                    const int64_t trow = rt.row0 + rt.tok0 + rtok;
-                    const int row = static_cast<int>(trow * P.H_q + hq);      // (T H_q < 2^27)
+                    const int row = static_cast<int>(trow * P.H_q + hq);      // (T H_q < 2^31)
                     const bool direct = P.n_split == 1;
                     RowEnd e = {1.f, 0.f, 0.f, false};
                     if (direct && row_ok) e = row_end(P, row, m, l);
@@ -895,7 +914,7 @@ __global__ void __launch_bounds__(RW_M) paged_rows_join_kernel(const __grid_cons
     const RowTile rt = find_tile(P, tile_idx, tt, lane);
     if (rt.b < 0) return;
     const int rtok = t * tpt + r / P.G;
-    const int64_t trow = rt.row0 + rt.tok0 + rtok;
+    const int64_t trow = (int64_t)rt.row0 + rt.tok0 + rtok;
     if (r >= tpt * P.G || rtok >= min(rt.n - rt.tok0, tt) || trow < 0 || trow >= P.T) return;
     const int64_t row = trow * P.H_q + g * P.G + r % P.G;
     auto part = [&](int s) { return P.ws + ((size_t)tile_idx * P.H_kv * P.n_split + (size_t)s * P.H_kv + g) * rows_partial_floats(D); };
@@ -976,7 +995,7 @@ int paged_rows_tok_per_tile(int G) { return RW_M / G; }
 size_t paged_rows_plan(PagedAttn& p, int D, int sms) {
     const int tt = 2 * (RW_M / p.G);
     // at most, whatever the sequences' shares
-    p.row_tiles = static_cast<int>(std::min<int64_t>(p.T / tt + p.B, (int64_t)p.B * ((p.max_rows + tt - 1) / tt)));
+    p.row_tiles = static_cast<int>(std::min<int64_t>(p.T / tt + std::min(p.B, p.T), (int64_t)p.B * ((p.max_rows + tt - 1) / tt)));
     p.box = paged_rows_box(p.page);
     // Keys are split when the row tiles leave SMs idle: as many splits as fill them once, each of at least 4 blocks
     // of the longest cache the table can hold. The tiles are taken as those of full ones, or one per sequence.

@@ -155,7 +155,7 @@ __device__ __forceinline__ RowSpan rows_of(const PagedAttn& P, int b, bool repor
         if (report) set_err(P.err, ERR_KV_LEN);
         r.n = P.max_rows;
     }
-    if (r.n < 0 || r.r0 < 0 || r.r0 + r.n > P.T) r.n = 0;
+    if (r.n < 0 || r.r0 < 0 || r.r0 > P.T - r.n) r.n = 0;
     return r;
 }
 
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
     }
     pdl_wait();
     pdl_release();
+    fence_proxy_async_all();     // the pages may have been written by the kernel before, and are read by TMA
 
     // ---- the range of units of this warp (BY_WARP) or CTA
     const int Hg = P.H_kv * P.n_groups;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
             pl_tok = tok - pi * P.page;
             pl_head = x / P.n_groups;
             pl_page = 0;
-            if (len > 0 && rows > 0) {
+            if (len > 0 && rows > 0 && pi < P.max_pages) {
                 const int pg = P.table[(int64_t)b * P.max_pages + pi];
                 if (pg < 0 || pg >= P.n_pages) set_err(P.err, ERR_PAGE_ID);   // and page 0 is read instead
                 else pl_page = pg;

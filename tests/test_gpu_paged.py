@@ -2,6 +2,7 @@
 append, attention of one row per sequence, and a run of them together behind a resident prefix."""
 import ctypes
 import math
+import os
 
 import pytest
 import torch
@@ -12,6 +13,7 @@ from tests.gpu_util import need_gpu
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
 i32 = torch.int32
 
@@ -413,3 +415,37 @@ def test_other_streams_and_two_graphs_at_once(ctx):
     O, L = ctx.paged_attend(k["c"], k["pg"].table, k["n"], q, stream=side)
     side.synchronize()
     ref.check_attend(O, L, ref.attend(k["pg"].k, k["pg"].v, k["pg"].table, lens, [1] * len(lens), q), BF16, ref.P_SPLIT[BF16])
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose very first paged calls are captured (their kernels are loaded then), replayed against eager ones."""
+    import subprocess
+    import sys
+    need_gpu()
+    code = """
+import torch
+from prefix_cached_kv_gb300 import binding
+ctx = binding.Context(0)
+k, v = (torch.randn((9, 2, 16, 64), device="cuda").half() for _ in range(2))
+c = binding.PagedCache(k, v)
+x = torch.randn((3, 8, 64), device="cuda").half()
+tab = torch.arange(9, device="cuda", dtype=torch.int32).view(1, 9).expand(3, 9).contiguous()
+n = torch.tensor([100, 17, 140], dtype=torch.int32, device="cuda")
+wide = torch.cat((tab, tab.new_full((3, 200), -1)), 1)
+cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+def calls():
+    q, _ = ctx.qk_norm_rope(x[:, :4], None, norm=True)
+    return [q] + [t for w in (tab, wide) for kw in (dict(), dict(cu_rows=cu, max_rows=1), dict(cu_rows=cu)) for t in ctx.paged_attend(c, w, n, q, **kw)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(out, calls()):
+    assert torch.equal(a, b)
+ctx.sync()
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr[-2000:]

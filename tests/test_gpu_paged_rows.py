@@ -225,3 +225,76 @@ def test_prompt_in_a_graph_with_other_lengths(ctx):   # noqa: F811
             t = sum(m)
             ref.check_attend(O[:t], L[:t], ref.attend(pg.k, pg.v, pg.table, a, m, Q[:t]), F16, ref.P_ONCE[F16])
     ctx.sync()
+
+
+def test_row_counts_that_make_no_sense(ctx):   # noqa: F811
+    """cu_rows that does not ascend, points outside the rows, or wraps: nothing outside O and LSE is touched, and sound
+    calls are right afterwards."""
+    pg, c, Q, O, L = _case(ctx, [400, 100], [300, 20], 4, 2, 64, 16, F16)
+    big = 2 ** 31 - 1
+    buf = torch.full((3, 320, 4, 64), 3.0, dtype=F16, device="cuda")
+    lse = torch.full((3, 320, 4), 4.0, device="cuda")
+    kk = pg.k.clone()
+    for cu in ([0, 320, 300], [300, 0, 320], [-5, 100, 320], [0, big, 20], [-big - 1, big, 320], [310, 320, 900], [big, big, big], [0, 5, -big]):
+        t = torch.tensor(cu, dtype=i32, device="cuda")
+        for mr in (None, 4):
+            ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=t, max_rows=mr, O=buf[1], LSE=lse[1])
+            ctx.paged_append(c, pg.table, pg.lens - 400, Q[:, :2], Q[:, 2:], cu_rows=t)
+            try:
+                ctx.sync()
+            except binding.PckError:
+                pass
+    for ln in (-1, -big - 1, big):
+        ctx.paged_attend(c, pg.table, torch.full_like(pg.lens, ln), Q, cu_rows=_cu([300, 20]), O=buf[1], LSE=lse[1])
+        ctx.paged_attend(c, pg.table, torch.full_like(pg.lens, ln), Q[:2], O=buf[1, :2], LSE=lse[1, :2])
+        ctx.paged_append(c, pg.table, torch.full_like(pg.lens, ln), Q[:2, :2], Q[:2, 2:])
+        try:
+            ctx.sync()
+        except binding.PckError:
+            pass
+    assert (buf[0] == 3).all() and (buf[2] == 3).all() and (lse[0] == 4).all() and (lse[2] == 4).all()
+    ctx.sync()
+    pg.k.copy_(kk)
+    O2, L2 = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu([300, 20]))
+    assert torch.isfinite(O2.float()).all()
+
+
+def test_widest_windows_and_rows_in_front_of_the_cache(ctx):   # noqa: F811
+    for W, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (3, 2 ** 31 - 1)):
+        _case(ctx, [5, 300], [40, 200], 4, 2, 64, 16, F16, W, sinks)
+        _case(ctx, [5, 300], [4, 3], 4, 2, 64, 16, F16, W, sinks, max_rows=4, split_p=True)
+
+
+def test_many_sequences(ctx):   # noqa: F811
+    """Hundreds of sequences, empty ones among them, with rows enough for the row kernel."""
+    lens = [(13 * i) % 90 + 40 for i in range(700)]
+    news = [(0, 7, 33)[i % 3] if i % 5 else 1 for i in range(700)]
+    _case(ctx, lens, news, 4, 1, 64, 16, F16)
+    _case(ctx, lens, news, 6, 2, 64, 16, BF16, W=20, sinks=3, max_rows=33, pad=4)
+
+
+@pytest.mark.parametrize("D,H_kv", [(128, 8), (64, 16)])
+def test_pages_beyond_32_bits(ctx, D, H_kv):   # noqa: F811
+    """Pages more than 2^31 elements (and 2^32 bytes) into the cache: append, one token, rows, and a value that is not
+    finite among them."""
+    P, n_pages = 64, 2 ** 31 // (H_kv * 64 * D) + 40
+    k, v = (torch.empty((n_pages, H_kv, P, D), dtype=F16, device="cuda") for _ in range(2))
+    n, m, H_q = 700, 200, 2 * H_kv
+    table = (n_pages - 1 - torch.arange(11, device="cuda")).to(i32)[None].contiguous()
+    x = _rand(5, n, H_q + 2 * H_kv, D, dtype=F16)
+    c = binding.PagedCache(k, v)
+    ln = torch.tensor([n], dtype=i32, device="cuda")
+    q = ctx.paged_append(c, table, ln, x[:, H_q:H_q + H_kv], x[:, H_q + H_kv:], Q=x[:, :H_q], cu_rows=_cu([n]), norm=True)
+    assert torch.equal(v[table[0, 3].long(), :, 5], x[3 * P + 5, H_q + H_kv:])
+    small = slice(n_pages - 11, n_pages)
+    tab = table - (n_pages - 11)
+    want = ref.attend(k[small], v[small], tab, [n], [m], q[n - m:])
+    O, L = ctx.paged_attend(c, table, ln, q[n - m:], cu_rows=_cu([m]))
+    ref.check_attend(O, L, want, F16, ref.P_ONCE[F16])
+    O, L = ctx.paged_attend(c, table, ln, q[-1:])
+    ref.check_attend(O, L, [t[-1:] for t in want], F16, ref.P_SPLIT[F16])
+    v[table[0, (n - 50) // P].long(), :, (n - 50) % P] = math.nan
+    O, L = ctx.paged_attend(c, table, ln, q[n - m:], cu_rows=_cu([m]))
+    ref.check_attend(O[:m - 50], L[:m - 50], [t[:m - 50] for t in want], F16, ref.P_ONCE[F16])
+    assert torch.isnan(O[m - 50:]).all()
+    ctx.sync()
