@@ -219,6 +219,9 @@ struct RowTile {
     int len;        // its cached tokens, as given
 };
 
+// Tiles of tt rows that n rows take.
+__device__ __forceinline__ uint32_t tiles_of(int n, int tt) { return (static_cast<uint32_t>(max(0, n)) + tt - 1u) / static_cast<uint32_t>(tt); }
+
 // The sequence and rows of CTA tile `idx` (tiles of tt rows, the sequences' tiles end to end). One warp; PER sequences a
 // lane at a time. (Row counts that make no sense, from a cu_rows that does not ascend, give some tile or none: the
 // caller checks every index that follows from it.)
@@ -234,7 +237,7 @@ __device__ __forceinline__ RowTile find_tile_by(const PagedAttn& P, int idx, int
         for (int i = 0; i < PER; ++i) len[i] = PER == 1 && bl + i < P.B ? P.kv_len[bl + i] : 0;   // many: loaded once found
         int64_t sum = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += (max(0, cu[i + 1] - cu[i]) + (int64_t)tt - 1) / tt;
+        for (int i = 0; i < PER; ++i) sum += tiles_of(cu[i + 1] - cu[i], tt);
         int64_t inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -250,7 +253,7 @@ __device__ __forceinline__ RowTile find_tile_by(const PagedAttn& P, int idx, int
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int n = max(0, cu[i + 1] - cu[i]);
-                    const int64_t nt = (n + (int64_t)tt - 1) / tt;
+                    const int64_t nt = tiles_of(n, tt);
                     if (t.b < 0 && at < nt) t = RowTile{bl + i, static_cast<int>(at * tt), n, cu[i], PER == 1 ? len[i] : P.kv_len[bl + i]};
                     at -= nt;
                 }
@@ -273,7 +276,7 @@ __device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt
 // Whether the sequences' tiles are more than the grid was made for: some sequence has more rows than max_rows.
 __device__ __forceinline__ bool too_many_rows(const PagedAttn& P, int tt, int lane) {
     int64_t total = 0;
-    for (int b = lane; b < P.B; b += 32) total += (max(0, P.cu_rows[b + 1] - P.cu_rows[b]) + (int64_t)tt - 1) / tt;
+    for (int b = lane; b < P.B; b += 32) total += tiles_of(P.cu_rows[b + 1] - P.cu_rows[b], tt);
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     return total > P.row_tiles;
@@ -289,13 +292,12 @@ __device__ __forceinline__ Keys keys_of(int p0, int p1, int window, int sinks, i
     Keys k;
     k.se = 0;
     k.ws = 0;
-    const int end = (p1 + box) / box * box;      // p1 + 1 rounded up; 0 for p1 < 0
+    const int end = (p1 + box) & -box;           // p1 + 1 rounded up (box is a power of two)
     if (window > 0) {
         const int first = max(0, p0 - window + 1);
-        k.ws = first / box * box;
+        k.ws = first & -box;
         const int s = min(sinks, p1 + 1);
-        k.se = min((s + box - 1) / box * box, k.ws);
-        if (k.se < 0) k.se = 0;
+        k.se = max(0, min((s + box - 1) & -box, k.ws));
     }
     k.total = p1 < 0 ? 0 : k.se + end - k.ws;
     return k;
@@ -450,12 +452,10 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     const int sub = blockIdx.x % per_tile;
     const int g = sub % P.H_kv, split = sub / P.H_kv;
 
-    if (tid == 0) {
+    if (warp == RW_LOAD_WARP && lane == 0) {
         for (int i = 0; i < N_BAR; ++i) mbar_init(bar + 8 * i, (8 * i >= B_P && 8 * i < B_O) ? 4 : (8 * i >= B_X && 8 * i < B_S) ? 2 : 1);
         fence_mbar_init();
         s_spoilt->any = s_spoilt->n = 0;
-    }
-    if (warp == RW_LOAD_WARP && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_q) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_v) : "memory");
@@ -471,6 +471,13 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
     if (warp == RW_LOAD_WARP) {
         const RowTile t = find_tile(P, tile_idx, tt, lane);
         if (lane == 0) *s_tile = t;
+        // Q at once: rows token * G + head; rows behind the sequence's hold others' or nothing
+        if (t.b >= 0 && lane < (min(t.n - t.tok0, tt) > tpt ? 2 : 1)) {
+            mbar_arrive_expect_tx(bar + B_Q + 8 * lane, C::CH * G * tpt * 128);
+            for (int c = 0; c < C::CH; ++c)
+                tma5(s_base + lane * C::TILE + c * C::CHUNK, &P.tm_q, 0, 0, t.row0 + t.tok0 + lane * tpt, c, g, bar + B_Q + 8 * lane);
+        }
+        __syncwarp();
         if (blockIdx.x == 0 && too_many_rows(P, tt, lane) && lane == 0) set_err(P.err, ERR_KV_LEN);
     }
     fence_before();
@@ -493,8 +500,9 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
         const int box = P.box;
         const Keys K = keys_of(p0, p1, P.window, P.sinks, box);
         const int nblk_all = (K.total + RW_BLOCK - 1) / RW_BLOCK;
-        const int j0 = static_cast<int>((int64_t)nblk_all * split / P.n_split);
-        const int j1 = static_cast<int>((int64_t)nblk_all * (split + 1) / P.n_split);
+        // (at most 2^23 blocks and 152 splits: within 32 bits)
+        const int j0 = P.n_split == 1 ? 0 : static_cast<int>(static_cast<uint32_t>(nblk_all) * split / static_cast<uint32_t>(P.n_split));
+        const int j1 = P.n_split == 1 ? nblk_all : static_cast<int>(static_cast<uint32_t>(nblk_all) * (split + 1) / static_cast<uint32_t>(P.n_split));
         const int nb = j1 - j0;
         auto keys_in = [&](int j) { return min(RW_BLOCK, K.total - (j0 + j) * RW_BLOCK); };   // of block j of this CTA
         bool failed = false;
@@ -504,11 +512,6 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
             if (warp == RW_LOAD_WARP) {
                 // ------------------------------------------------------------ loads
                 if (nb > 0) {
-                    if (lane < ntile) {   // Q rows token * G + head; rows behind the sequence's hold others' or nothing
-                        mbar_arrive_expect_tx(bar + B_Q + 8 * lane, C::CH * G * tpt * 128);
-                        for (int c = 0; c < C::CH; ++c)
-                            tma5(s_base + lane * C::TILE + c * C::CHUNK, &P.tm_q, 0, 0, rt.row0 + rt.tok0 + lane * tpt, c, g, bar + B_Q + 8 * lane);
-                    }
                     const int bpb = RW_BLOCK / box;     // boxes of a whole block
                     int pg = 0, tok = 0;
                     auto locate = [&](int j) {          // lane i: page and token of box i of block j
@@ -539,12 +542,14 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                         if (jv + 1 < nb) locate(jv + 1);
                     }
                     if (jv < nb && lane == 0) set_err(P.err, ERR_ROWS_LOAD);
-                    // the copies in flight land before the CTA can end, whatever the other warps do
+                    // the copies in flight land before the CTA can end, whatever the other warps do (Q's below)
                     for (int j = max(0, jk - C::NK); j < jk; ++j)
                         if (!__all_sync(0xffffffffu, wait_bar(bar + B_KF + 8 * (j % C::NK), (j / C::NK) & 1))) break;
                     for (int j = max(0, jv - C::NV); j < jv; ++j)
                         if (!__all_sync(0xffffffffu, wait_bar(bar + B_VF + 8 * (j % C::NV), (j / C::NV) & 1))) break;
                 }
+                for (int t = 0; t < ntile; ++t)
+                    if (!__all_sync(0xffffffffu, wait_bar(bar + B_Q + 8 * t, 0))) break;
             } else if (warp == RW_MMA_WARP) {
                 // ------------------------------------------------------------ MMAs
                 // broadcasts, so that the compiler sees them as uniform
@@ -826,6 +831,8 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     set_err(P.err, ERR_ROWS_SOFTMAX);
                 }
                 fence_after();
+                // without keys nothing else has waited for Q, over which the result is staged
+                if (nb == 0 && !__all_sync(0xffffffffu, wait_bar(bar + B_Q + 8 * t, 0))) failed = true;
                 // the record of spoilt keys is complete
                 asm volatile("barrier.cta.sync %0, 192;" ::"r"(1 + t) : "memory");
                 if (!failed) {
@@ -838,6 +845,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                     uint8_t* stage = smem + t * C::TILE + (warp & 3) * 32 * (D * 2);
                     if (nb > 0 && s_spoilt->any)
                         add_spoilt<T, D>(P, s_spoilt, b, g, trow * P.q_row + (int64_t)hq * P.q_head, p, K, m, o_tm);
+                    const bool nothing = __any_sync(0xffffffffu, l == 0.f);
 #pragma unroll 2
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                             ld32(o_tm + c, o);
                             wait_ld();
                         }
-                        if (l == 0.f) {     // nothing seen (and O unwritten where the CTA has no keys)
+                        if (nothing && l == 0.f) {     // nothing seen (and O unwritten where the CTA has no keys)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = 0.f;
                         }
