@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -64,14 +65,9 @@ class PagedBatchT(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("max_rows", ctypes.c_int)]
 
 
-class RotaryT(ctypes.Structure):
-    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int), ("R", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p)]
-
-
-class RowsT(ctypes.Structure):
-    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("H", ctypes.c_int)] + [
-        (n, ctypes.c_int64) for n in ("in_row", "in_head", "out_row", "out_head")] + [("weight", ctypes.c_void_p)]
+# pck_rows and pck_rotary as they lie in memory
+_ROWS = struct.Struct("QQi4xqqqqQ")
+_ROTARY = struct.Struct("Qiii4xQ")
 
 
 _lib = None
@@ -263,18 +259,6 @@ def _on(device, **tensors):
             raise ValueError(f"{name}: must be on the CUDA device {device}, not {t.device}")
 
 
-def _rows(t, out, weight):
-    """pck_rows of t [T, H, D] (None: no rows of this kind)."""
-    if t is None:
-        return None
-    i = t.stride()
-    w = None if weight is None else weight.data_ptr()
-    if out is None:
-        return RowsT(t.data_ptr(), None, t.shape[1], i[0], i[1], 0, 0, w)
-    o = out.stride()
-    return RowsT(t.data_ptr(), out.data_ptr(), t.shape[1], i[0], i[1], o[0], o[1], w)
-
-
 # The checks of a call's usual arguments, in one pass without names: what fails here goes through the named
 # checks, which say what is wrong.
 def _rows_fit(t, dtype, shape, device):
@@ -303,13 +287,6 @@ except AttributeError:
         return torch.cuda.current_stream(index).cuda_stream
 
 
-def _rotary(cos_sin, interleaved, positions):
-    if cos_sin is None:
-        return None
-    return RotaryT(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
-                   None if positions is None else positions.data_ptr())
-
-
 def _check_rope(cos_sin, positions, T):
     if cos_sin is None:
         if positions is not None:
@@ -321,9 +298,6 @@ def _check_rope(cos_sin, positions, T):
     if positions is not None:
         _need(positions, "positions", torch.int32, (T,))
 
-
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
 
 
 class PagedCache:
@@ -362,6 +336,10 @@ class Context:
             raise PckError(rc, "pck_create failed")
         self.h = h
         self.device = torch.device("cuda", device)
+        # room for three pck_rows and a pck_rotary, filled in place by each call (the library has read them when the call
+        # returns, and one context is called by one thread at a time)
+        self._args = (ctypes.c_int64 * 28)()
+        self._args_at = ctypes.addressof(self._args)
 
     def close(self):
         if getattr(self, "h", None):
@@ -583,6 +561,23 @@ class Context:
         t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
+    def _put_rows(self, i, t, out, weight):
+        """pck_rows i of the arguments, from t [T, H, D]; its address (None: no rows of this kind)."""
+        if t is None:
+            return None
+        s = t.stride()
+        o = (0, 0) if out is None else out.stride()
+        _ROWS.pack_into(self._args, 64 * i, t.data_ptr(), 0 if out is None else out.data_ptr(), t.shape[1], s[0], s[1], o[0], o[1],
+                        0 if weight is None else weight.data_ptr())
+        return self._args_at + 64 * i
+
+    def _put_rotary(self, cos_sin, interleaved, positions):
+        if cos_sin is None:
+            return None
+        n, R = cos_sin.shape
+        _ROTARY.pack_into(self._args, 192, cos_sin.data_ptr(), n, R, bool(interleaved), 0 if positions is None else positions.data_ptr())
+        return self._args_at + 192
+
     def _batch(self, cache, table, kv_len, cu_rows, T, max_rows):
         dev = self.device
         B, W = kv_len.shape[0] if kv_len.dim() == 1 else -1, table.shape[-1] if table.dim() == 2 else -1
@@ -642,8 +637,8 @@ class Context:
             Q_out = self._empty(stream, Q.shape, dt)
         if K is not None and K_out is None:
             K_out = self._empty(stream, K.shape, dt)
-        self._launch(self.lib.pck_qk_norm_rope, stream, _ROWS_DT[dt], T, D, _ref(_rows(Q, Q_out, q_weight)),
-                     _ref(_rows(K, K_out, k_weight)), norm, eps, _ref(_rotary(cos_sin, interleaved, positions)))
+        self._launch(self.lib.pck_qk_norm_rope, stream, _ROWS_DT[dt], T, D, self._put_rows(0, Q, Q_out, q_weight),
+                     self._put_rows(1, K, K_out, k_weight), norm, eps, self._put_rotary(cos_sin, interleaved, positions))
         return Q_out, K_out
 
     def _rope_fits(self, cos_sin, positions, T, need_positions):
@@ -689,9 +684,9 @@ class Context:
             _on(dev, K=K, V=V, Q=Q, Q_out=Q_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, positions=positions)
         if Q is not None and Q_out is None:
             Q_out = self._empty(stream, Q.shape, dt)
-        self._launch(self.lib.pck_paged_append, stream, cache.ref, _ref(batch), _ROWS_DT[dt],
-                     _ref(_rows(Q, Q_out, q_weight)), _ref(_rows(K, None, k_weight)), _ref(_rows(V, None, None)),
-                     norm, eps, _ref(_rotary(cos_sin, interleaved, positions)))
+        self._launch(self.lib.pck_paged_append, stream, cache.ref, ctypes.byref(batch), _ROWS_DT[dt],
+                     self._put_rows(0, Q, Q_out, q_weight), self._put_rows(1, K, None, k_weight), self._put_rows(2, V, None, None),
+                     norm, eps, self._put_rotary(cos_sin, interleaved, positions))
         return Q_out
 
     def paged_attend(self, cache, table, kv_len, Q, cu_rows=None, max_rows=None, window=0, sinks=0, prior=None, O=None,

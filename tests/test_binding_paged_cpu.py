@@ -113,3 +113,29 @@ def test_attend():
     _raises(lambda: f(prior=(Q.float(), lse[:2])), "prior LSE: shape")
     _raises(lambda: f(n=n[:2], tab=tab[:2]), "cu_rows is needed")
     _raises(lambda: f(), "must be on the CUDA device")
+
+
+def test_packed_arguments_match_the_header(tmp_path):
+    """The formats in which the binding writes pck_rows and pck_rotary, and its structures, against the C compiler's."""
+    import ctypes
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "pck.h"\nint main(void) {\n'
+                   + "".join(f'printf("%zu ", offsetof({t}, {f}));\n' for t, fs in (
+                       ("pck_rows", "in out H in_row in_head out_row out_head weight"),
+                       ("pck_rotary", "cos_sin n_pos R interleaved positions"),
+                       ("pck_paged_cache", "K V dtype H_kv D page_size n_pages k_page k_head k_token v_page v_head v_token"),
+                       ("pck_paged_batch", "B T cu_rows kv_len table max_pages max_rows")) for f in fs.split())
+                   + 'printf("%zu %zu %zu %zu", sizeof(pck_rows), sizeof(pck_rotary), sizeof(pck_paged_cache), sizeof(pck_paged_batch));\nreturn 0;\n}\n')
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()]
+    rows, rot = [0, 8, 16, 24, 32, 40, 48, 56], [0, 8, 12, 16, 24]
+    structs = [getattr(t, n).offset for t in (binding.PagedCacheT, binding.PagedBatchT) for n, *_ in t._fields_]
+    assert got == rows + rot + structs + [binding._ROWS.size, binding._ROTARY.size, ctypes.sizeof(binding.PagedCacheT), ctypes.sizeof(binding.PagedBatchT)]
+    assert binding._ROWS.unpack(binding._ROWS.pack(*range(1, 9))) == tuple(range(1, 9))
+    at = binding._ROWS.pack(1, 2, 3, 4, 5, 6, 7, 8)
+    assert [int.from_bytes(at[o:o + (4 if o == 16 else 8)], "little") for o in rows] == list(range(1, 9))
+    at = binding._ROTARY.pack(1, 2, 3, 4, 5)
+    assert [int.from_bytes(at[o:o + (4 if o in (8, 12, 16) else 8)], "little") for o in rot] == list(range(1, 6))
