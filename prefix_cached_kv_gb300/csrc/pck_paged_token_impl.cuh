@@ -28,6 +28,8 @@
 //    per range, at most two per range, and a second, programmatically launched kernel joins them.
 //  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA whose warps take its
 //    units in turn and join through shared memory: one launch.
+// Measured: one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 87 us, 6.2 TB/s; 16 caches of 30-65k tokens
+// (2 kv heads of 256) 229 us, 6.6 TB/s; 64 ragged sequences (8 kv heads of 64) 84 us, 5.4 TB/s.
 #pragma once
 
 #include "pck_paged.cuh"
@@ -35,14 +37,20 @@
 namespace pck {
 namespace {
 
-constexpr int TK_DIRECT_UNITS = 32;    // 512 tokens
-constexpr int TK_FEW_ITEMS = 2;        // items per SM up to which a range is a CTA's
+// Units of an item up to which it gets a CTA (1024 tokens): one sequence of 300 tokens 7.1 us against 11.2 cut into
+// ranges, of 1000 tokens 10.8 against 11.4, of 2000 tokens 15.4 against 10.5 (8 kv heads of 128).
+constexpr int TK_DIRECT_UNITS = 64;
+// Items per SM up to which a range is a CTA's: one cache of 131k tokens 87 us against 96 with a range per warp, 32
+// windows of 2048 tokens (1.7 items per SM) 47 against 53; 64 ragged sequences (3.4) 101 against 85.
+constexpr int TK_FEW_ITEMS = 2;
 // How a call is cut.
 enum { TK_ITEM, TK_CTA, TK_WARP };     // an item per CTA; ranges per CTA; ranges per warp
-// Units per range at least (two per warp, or what a warp's start is worth).
-__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_CTA ? 16 : 8; }
+// Units per range at least (one per warp, or what a warp's start is worth): 2000 tokens 10.2 us, with twice as many
+// 10.5, with four times 11.9.
+__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_CTA ? 8 : 4; }
 // What an item costs beside its units (its q, its end), in units: ranges are cut by units + this per item, so that a
-// range of many short items does not take long after the others.
+// range of many short items does not take long after the others (64 ragged sequences, ranges per CTA: 132 us with 0, 122
+// with 8, 101 with 24; ranges per warp: 122 with 4, 101 with 8, 85 with 16, 87 with 32).
 __host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_CTA ? 24 : 16; }
 constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
 

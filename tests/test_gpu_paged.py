@@ -229,7 +229,7 @@ def test_token_nan_in_a_visible_key_shows(ctx):
 
 def test_token_split_widths_agree(ctx):
     """A wide table (ranges over all SMs, joined) and a narrow one (a CTA per item) hold the same bound."""
-    for width in (32, 33, 4000):
+    for width in (32, 64, 65, 4000):
         _attend_case(ctx, [500, 0, 1, 512, 77], 8, 2, 128, 16, F16, width=width, prior=True)
 
 
@@ -300,7 +300,7 @@ def test_refusals(ctx):
         ctx.h, ctypes.byref(c.c), ctypes.byref(batch), 4, Q.data_ptr(), 256, 64, 0, 0, Op, Lp, O.data_ptr(), None, ws, n, None)
     assert call(None, 0) == binding.OK                                            # 7 pages: a CTA per item, no workspace
     assert call(None, 0, Op=O.data_ptr()) == binding.EINVAL                       # a prior without its LSE
-    batch.max_pages = 40                                                          # (not launched: refused first)
+    batch.max_pages = 100                                                         # (not launched: refused first)
     assert call(None, 0) == binding.EINVAL and call(vp(O.data_ptr()), 64) == binding.EINVAL
     n = ctypes.c_size_t()
     assert lib.pck_paged_workspace(ctx.h, ctypes.byref(c.c), ctypes.byref(batch), 4, 0, 0, ctypes.byref(n)) == binding.OK and n.value > 64
