@@ -19,14 +19,23 @@ size_t paged_token_plan(PagedAttn& p, int D, int sms) {
     p.heads_per_group = (p.G + p.n_groups - 1) / p.n_groups;
     p.cols = p.heads_per_group * rows;
     int64_t bound = ((int64_t)p.max_pages * p.page + PG_SUB - 1) / PG_SUB;   // units of one item
+    int64_t direct = TK_DIRECT_UNITS;
     if (p.window > 0) {
-        const int64_t w = ((int64_t)p.window + rows + PG_SUB - 1) / PG_SUB + 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;
-        if (w < bound) bound = w;
+        const int64_t edges = 1 + ((int64_t)p.sinks + PG_SUB - 1) / PG_SUB;    // units beside the window's own
+        const int64_t w = ((int64_t)p.window + rows + PG_SUB - 1) / PG_SUB + edges;
+        if (w < bound) {
+            bound = w;
+            direct += 1 + (edges < 8 ? edges : 8);      // (a window of 1024 tokens has as many units in the middle)
+        }
     }
     const int64_t items = (int64_t)p.B * p.H_kv * p.n_groups;
-    p.mode = bound <= TK_DIRECT_UNITS ? TK_ITEM : items <= (int64_t)TK_FEW_ITEMS * sms ? TK_CTA : TK_WARP;
-    p.n_ctas = p.mode == TK_ITEM ? static_cast<int>(items) : sms;
-    const size_t ranges = p.mode == TK_ITEM ? 0 : (size_t)p.n_ctas * (p.mode == TK_CTA ? 1 : D <= 128 ? TCfg<128>::NW : TCfg<256>::NW);
+    const bool spread = items > sms;                    // more than one item per SM
+    p.mode = items > (int64_t)TK_FEW_ITEMS * sms ? TK_WARP
+             : bound <= direct                   ? (spread ? TK_ITEM_HALF : TK_ITEM)
+                                                 : (spread ? TK_CTA_HALF : TK_CTA);
+    p.n_ctas = is_split(p.mode) ? sms * per_sm(p.mode) : static_cast<int>(items);
+    const int nw = D <= 128 ? TCfg<128>::NW : TCfg<256>::NW;
+    const size_t ranges = is_split(p.mode) ? (size_t)p.n_ctas * (p.mode == TK_WARP ? nw : 1) : 0;
     return ranges * (2 * slot_floats(D, p.cols) * sizeof(float) + sizeof(JoinDesc));
 }
 

@@ -11,11 +11,11 @@
 //    leaves its page). The units of all items (sequence, kv head, group of q heads) laid end to end
 //    are cut into equal ranges from the lengths on the device (one block scan per CTA), so a ragged
 //    batch, one long sequence and many short ones all load every SM evenly, and a captured graph
-//    follows the lengths it finds. Few items (at most TK_FEW_ITEMS per SM): a range per CTA, whose warps
-//    take every NW-th unit and join through shared memory; neighbouring warps then read neighbouring
-//    tiles, and an item has few pieces. Many: a range per warp, because a change of item (its q, its end)
-//    then stalls one of the SM's eight streams and not all of them.
-//  * One CTA per SM; each warp streams its units through a ring of its own (two TMA tile loads a unit,
+//    follows the lengths it finds. A range is a CTA's, whose warps take every NW-th unit and join through
+//    shared memory: neighbouring warps then read neighbouring tiles, and an item has few pieces. With more
+//    items than SMs the CTAs have half the warps, two to an SM, so that a change of item (its q, its end) stalls
+//    half of the SM's streams; with many more a range is a warp's, and it stalls one of them.
+//  * One or two CTAs per SM; each warp streams its units through a ring of its own (two TMA tile loads a unit,
 //    128-byte swizzle, evict-first: read once). Lane i of a warp resolves the i-th of its next 32 units
 //    (sequence, tile, page number) at once, so page-table latency is paid once in 32 units and off the
 //    critical path; rings run on across items.
@@ -26,10 +26,12 @@
 //    hidden behind the loads.
 //  * An item that lies within one range is finished there; one that crosses ranges leaves a partial [m, l, O]
 //    per range, at most two per range, and a second, programmatically launched kernel joins them.
-//  * When no sequence can have more than TK_DIRECT_UNITS units, each item gets a CTA whose warps take its
-//    units in turn and join through shared memory: one launch.
+//  * When no sequence can have more than TK_DIRECT_UNITS units and the items are not many, each item gets a CTA
+//    whose warps take its units in turn and join through shared memory: one launch. With more items than SMs
+//    these CTAs too have half the warps (24 sequences of 100 tokens, 8 kv heads: 6.9 us against 11.0; 64 of 500
+//    tokens 27.9 against 36.3).
 // Measured: one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 87 us, 6.2 TB/s; 16 caches of 30-65k tokens
-// (2 kv heads of 256) 229 us, 6.6 TB/s; 64 ragged sequences (8 kv heads of 64) 84 us, 5.4 TB/s.
+// (2 kv heads of 256) 230 us, 6.5 TB/s; 64 ragged sequences (8 kv heads of 64) 83 us, 5.5 TB/s.
 #pragma once
 
 #include "pck_paged.cuh"
@@ -37,26 +39,31 @@
 namespace pck {
 namespace {
 
-// Units of an item up to which it gets a CTA (1024 tokens): one sequence of 300 tokens 7.1 us against 11.2 cut into
-// ranges, of 1000 tokens 10.8 against 11.4, of 2000 tokens 15.4 against 10.5 (8 kv heads of 128).
+// Units of an item up to which it gets a CTA (1024 tokens): one sequence of 300 tokens 7.1 us against 10.0 cut into
+// ranges, of 1000 tokens 10.8 against 10.4, of 2000 tokens 15.3 against 10.2 (8 kv heads of 128). Items of equal length
+// gain up to 4000 tokens (24 x 2000: 35.6 against 41.2), but ragged ones lose twice that (24 x 1-2000: 26.1 against 17.2).
 constexpr int TK_DIRECT_UNITS = 64;
-// Items per SM up to which a range is a CTA's: one cache of 131k tokens 87 us against 96 with a range per warp, 32
-// windows of 2048 tokens (1.7 items per SM) 47 against 53; 64 ragged sequences (3.4) 101 against 85.
-constexpr int TK_FEW_ITEMS = 2;
-// How a call is cut.
-enum { TK_ITEM, TK_CTA, TK_WARP };     // an item per CTA; ranges per CTA; ranges per warp
+// Items per SM above which a range is a warp's. 64 ragged sequences (3.4 per SM) 83 us with a range per half CTA, 86 with
+// one per warp, 101 with one per whole CTA; 200 x 1-1000 tokens (10.5) 45 against 43, 600 x 100 (32) 85 against 58. Items
+// that could have a CTA each: 100 x 500 tokens (5.3) 41 us with one, 52 with a range per warp; 200 x 1-1000 47 against 43.
+constexpr int TK_FEW_ITEMS = 6;
+// How a call is cut: an item per CTA, per CTA of half the warps; a range per CTA, per CTA of half the warps, per warp.
+// At one item per SM or less, CTAs are whole: one cache of 131k tokens 87 us (halves 89), 16 caches of 30-65k 230 (234).
+enum { TK_ITEM, TK_ITEM_HALF, TK_CTA, TK_CTA_HALF, TK_WARP };
+__host__ __device__ constexpr bool is_split(int mode) { return mode >= TK_CTA; }
+__host__ __device__ constexpr int per_sm(int mode) { return mode == TK_ITEM_HALF || mode == TK_CTA_HALF ? 2 : 1; }   // CTAs
 // Units per range at least (one per warp, or what a warp's start is worth): 2000 tokens 10.2 us, with twice as many
 // 10.5, with four times 11.9.
-__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_CTA ? 8 : 4; }
+__host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_WARP ? 4 : 8; }
 // What an item costs beside its units (its q, its end), in units: ranges are cut by units + this per item, so that a
 // range of many short items does not take long after the others (64 ragged sequences, ranges per CTA: 132 us with 0, 122
 // with 8, 101 with 24; ranges per warp: 122 with 4, 101 with 8, 85 with 16, 87 with 32).
-__host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_CTA ? 24 : 16; }
+__host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_WARP ? 16 : 24; }
 constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
 
-template <int D>
+template <int D, int PER_SM = 1>
 struct TCfg {
-    static constexpr int NW = D <= 128 ? 8 : 4;                   // warps per CTA
+    static constexpr int NW = (D <= 128 ? 8 : 4) / PER_SM;        // warps per CTA
     static constexpr int UNIT = PG_SUB * D * 2;                   // bytes of a K (or V) unit
     static constexpr int STAGE = 2 * UNIT;
     static constexpr int ST = D <= 64 ? 6 : D == 192 ? 4 : 3;     // stages of a warp's ring
@@ -233,8 +240,8 @@ struct JoinDesc {
 
 // ROWS: a sequence may have several rows (cu_rows); else it has one.
 template <typename T, int D, int NB, int MODE, bool ROWS>
-__global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const __grid_constant__ PagedAttn P) {
-    using C = TCfg<D>;
+__global__ void __launch_bounds__(TCfg<D, per_sm(MODE)>::NW * 32, per_sm(MODE)) paged_token_kernel(const __grid_constant__ PagedAttn P) {
+    using C = TCfg<D, per_sm(MODE)>;
     constexpr int NW = C::NW, ST = C::ST, KS = D / 16, NT = NW * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(TCfg<D>::NW * 32, 1) paged_token_kernel(const 
     const int Hg = P.H_kv * P.n_groups;
     const int B = P.B;
     const int heads = P.heads_per_group, cols = P.cols;
-    constexpr bool SPLIT = MODE != TK_ITEM, BY_WARP = MODE == TK_WARP;
+    constexpr bool SPLIT = is_split(MODE), BY_WARP = MODE == TK_WARP;
     constexpr int TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
     const int worker = BY_WARP ? warp * gridDim.x + blockIdx.x : blockIdx.x;    // few workers spread over the SMs
     int workers = BY_WARP ? gridDim.x * NW : gridDim.x;
@@ -791,7 +798,8 @@ __global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_cons
 
 template <typename T, int D, int NB, int MODE, bool ROWS>
 cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
-    using C = TCfg<D>;
+    using C = TCfg<D, per_sm(MODE)>;
+    constexpr bool SPLIT = is_split(MODE);
     static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
     const cudaError_t e0 = allow_smem<paged_token_kernel<T, D, NB, MODE, ROWS>>(C::SMEM_BASE + 4 * (TK_MAX_B + 1), p.device);
     if (e0 != cudaSuccess) return e0;
@@ -801,12 +809,12 @@ cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_ctas);
     cfg.blockDim = dim3(C::NW * 32);
-    cfg.dynamicSmemBytes = C::SMEM_BASE + 4 * ((MODE != TK_ITEM ? p.B : 1) + 1);
+    cfg.dynamicSmemBytes = C::SMEM_BASE + 4 * ((SPLIT ? p.B : 1) + 1);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token_kernel<T, D, NB, MODE, ROWS>, p);
-    if (e != cudaSuccess || MODE == TK_ITEM) return e;
+    if (e != cudaSuccess || !SPLIT) return e;
     cfg.gridDim = dim3(p.n_ctas, p.cols, MODE == TK_WARP ? C::NW : 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
@@ -816,7 +824,9 @@ cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
 template <typename T, int D, int NB, bool ROWS>
 cudaError_t launch_m(PagedAttn& p, cudaStream_t st) {
     return p.mode == TK_WARP  ? launch_t<T, D, NB, TK_WARP, ROWS>(p, st)
+           : p.mode == TK_CTA_HALF ? launch_t<T, D, NB, TK_CTA_HALF, ROWS>(p, st)
            : p.mode == TK_CTA ? launch_t<T, D, NB, TK_CTA, ROWS>(p, st)
+           : p.mode == TK_ITEM_HALF ? launch_t<T, D, NB, TK_ITEM_HALF, ROWS>(p, st)
                               : launch_t<T, D, NB, TK_ITEM, ROWS>(p, st);
 }
 template <typename T, int D, int NB>

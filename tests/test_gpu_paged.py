@@ -182,6 +182,30 @@ def test_token_many_items(ctx, dtype, H_q, H_kv, D):
     _attend_case(ctx, lens, H_q, H_kv, D, 32, dtype, W=300, sinks=5, prior=True, nhd=True, seed=4, width=600)
 
 
+@pytest.mark.parametrize("B", [1, 19, 20, 40, 77, 160, 310, 700])
+@pytest.mark.parametrize("H_q,H_kv,D", [(8, 8, 128), (12, 3, 64), (32, 2, 128), (16, 4, 256)])
+def test_token_short_caches(ctx, B, H_q, H_kv, D):
+    """An item per CTA, per CTA of half the warps, and ranges per warp once the items are many."""
+    lens = [(61 * i * i + 7 * B) % 300 for i in range(B)]
+    _attend_case(ctx, lens, H_q, H_kv, D, 16, F16 if B % 2 else BF16, prior=B % 3 == 0)
+    _attend_case(ctx, lens, H_q, H_kv, D, 32, BF16, W=50, sinks=3, seed=3)
+
+
+@pytest.mark.parametrize("B,H_q,H_kv,D", [(19, 8, 8, 128), (20, 32, 8, 128), (77, 12, 3, 64), (40, 16, 4, 192), (70, 24, 8, 256), (912, 1, 1, 64), (913, 1, 1, 64)])
+def test_token_ranges_of_ragged_caches(ctx, B, H_q, H_kv, D):
+    """One item per SM and just above, up to six: ranges per CTA and per CTA of half the warps, then per warp."""
+    lens = [(61 * i * i + 7 * B) % (1700 if i % 5 == 0 else 90) for i in range(B)]
+    _attend_case(ctx, lens, H_q, H_kv, D, 16, BF16 if B % 2 else F16, prior=B % 4 == 0, width=2000)
+    _attend_case(ctx, lens, H_q, H_kv, D, 16, BF16, W=1100, sinks=20, width=2000, seed=2)
+
+
+@pytest.mark.parametrize("W,sinks", [(1023, 0), (1024, 0), (1024, 17), (1025, 0), (1100, 300)])
+def test_token_windows_of_a_cta(ctx, W, sinks):
+    lens = [0, 1, 15, 16, 17, 1000, 1023, 1024, 1025, 1040, 1337, 2000, 4999]
+    _attend_case(ctx, lens, 8, 2, 128, 16, BF16, W=W, sinks=sinks)
+    _attend_case(ctx, lens * 10, 8, 2, 64, 16, F16, W=W, sinks=sinks, seed=2)
+
+
 def test_token_hidden_keys_hold_anything(ctx):
     """Behind the window, in front of the last token and in unneeded pages: NaN, infinities, the lowest value, and table
     entries that are no pages."""
