@@ -199,6 +199,16 @@ def test_token_ranges_of_ragged_caches(ctx, B, H_q, H_kv, D):
     _attend_case(ctx, lens, H_q, H_kv, D, 16, BF16, W=1100, sinks=20, width=2000, seed=2)
 
 
+@pytest.mark.parametrize("B,n", [(14, 1100), (16, 1500), (20, 1200), (38, 1100), (39, 1100), (64, 1050)])
+@pytest.mark.parametrize("spread", [0, 0.2])
+def test_token_caches_of_one_length(ctx, B, n, spread):
+    """Items that stay whole because they have nearly one length, and those that just do not."""
+    lens = [n - int(spread * n * ((7 * i) % 10) / 10) for i in range(B)]
+    _attend_case(ctx, lens, 16, 8, 64, 16, BF16, prior=B % 2 == 0)
+    if not spread:
+        _attend_case(ctx, [3000 - 100 * (i % 2) for i in range(B)], 8, 8, 64, 32, F16, W=n, sinks=5, seed=2)
+
+
 @pytest.mark.parametrize("W,sinks", [(1023, 0), (1024, 0), (1024, 17), (1025, 0), (1100, 300)])
 def test_token_windows_of_a_cta(ctx, W, sinks):
     lens = [0, 1, 15, 16, 17, 1000, 1023, 1024, 1025, 1040, 1337, 2000, 4999]
