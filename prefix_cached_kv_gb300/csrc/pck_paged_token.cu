@@ -34,8 +34,7 @@ size_t paged_token_plan(PagedAttn& p, int D, int sms) {
              : bound <= direct                   ? (spread ? TK_ITEM_HALF : TK_ITEM)
                                                  : (spread ? TK_CTA_HALF : TK_CTA);
     p.n_ctas = is_split(p.mode) ? sms * per_sm(p.mode) : static_cast<int>(items);
-    const int nw = D <= 128 ? TCfg<128>::NW : TCfg<256>::NW;
-    const size_t ranges = is_split(p.mode) ? (size_t)p.n_ctas * (p.mode == TK_WARP ? nw : 1) : 0;
+    const size_t ranges = is_split(p.mode) ? (size_t)p.n_ctas * (p.mode == TK_WARP ? warps_sm(D, TK_WARP) : 1) : 0;
     return ranges * (2 * slot_floats(D, p.cols) * sizeof(float) + sizeof(JoinDesc));
 }
 

@@ -54,6 +54,12 @@ constexpr int TK_FEW_ITEMS = 6;
 enum { TK_ITEM, TK_ITEM_HALF, TK_CTA, TK_CTA_HALF, TK_WARP };
 __host__ __device__ constexpr bool is_split(int mode) { return mode >= TK_CTA; }
 __host__ __device__ constexpr int per_sm(int mode) { return mode == TK_ITEM_HALF || mode == TK_CTA_HALF ? 2 : 1; }   // CTAs
+// Warps per SM. At D = 64 a unit is 4 KB and its warp's chain of MMAs bounds it: where an item or a range is short, 16
+// warps with 3 stages each beat 8 with 6 (600 x 1-1000 tokens 58 us against 78, 64 of them 16 against 20, one sequence of
+// 1000 tokens 8.6 against 9.9), but a CTA's long ranges then have more to join (64 ragged sequences 91 against 83).
+__host__ __device__ constexpr int warps_sm(int D, int mode) {
+    return D > 128 ? 4 : D == 64 && mode != TK_CTA && mode != TK_CTA_HALF ? 16 : 8;
+}
 // Units per range at least (one per warp, or what a warp's start is worth): 2000 tokens 10.2 us, with twice as many
 // 10.5, with four times 11.9.
 __host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_WARP ? 4 : 8; }
@@ -63,12 +69,12 @@ __host__ __device__ constexpr int tk_min_units(int mode) { return mode == TK_WAR
 __host__ __device__ constexpr int tk_item_units(int mode) { return mode == TK_WARP ? 16 : 24; }
 constexpr int TK_MAX_B = PCK_PAGED_MAX_BATCH;
 
-template <int D, int PER_SM = 1>
+template <int D, int MODE>
 struct TCfg {
-    static constexpr int NW = (D <= 128 ? 8 : 4) / PER_SM;        // warps per CTA
+    static constexpr int NW = warps_sm(D, MODE) / per_sm(MODE);   // warps per CTA
     static constexpr int UNIT = PG_SUB * D * 2;                   // bytes of a K (or V) unit
     static constexpr int STAGE = 2 * UNIT;
-    static constexpr int ST = D <= 64 ? 6 : D == 192 ? 4 : 3;     // stages of a warp's ring
+    static constexpr int ST = D <= 64 ? 48 / warps_sm(D, MODE) : D == 192 ? 4 : 3;      // stages of a warp's ring
     static constexpr int RING = NW * ST * STAGE;
     static constexpr int JROW = D / 2 + 4;                        // floats of a join row (half of D, padded)
     static constexpr int JOIN = NW * 8 * JROW * 4;
@@ -242,8 +248,8 @@ struct JoinDesc {
 
 // ROWS: a sequence may have several rows (cu_rows); else it has one.
 template <typename T, int D, int NB, int MODE, bool ROWS>
-__global__ void __launch_bounds__(TCfg<D, per_sm(MODE)>::NW * 32, per_sm(MODE)) paged_token_kernel(const __grid_constant__ PagedAttn P) {
-    using C = TCfg<D, per_sm(MODE)>;
+__global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_token_kernel(const __grid_constant__ PagedAttn P) {
+    using C = TCfg<D, MODE>;
     constexpr int NW = C::NW, ST = C::ST, KS = D / 16, NT = NW * 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -823,7 +829,7 @@ __global__ void __launch_bounds__(256) paged_token_join_kernel(const __grid_cons
 
 template <typename T, int D, int NB, int MODE, bool ROWS>
 cudaError_t launch_t(PagedAttn& p, cudaStream_t st) {
-    using C = TCfg<D, per_sm(MODE)>;
+    using C = TCfg<D, MODE>;
     constexpr bool SPLIT = is_split(MODE);
     static_assert(C::SMEM_BASE + 4 * (TK_MAX_B + 1) <= 232448, "one CTA's shared memory");
     const cudaError_t e0 = allow_smem<paged_token_kernel<T, D, NB, MODE, ROWS>>(C::SMEM_BASE + 4 * (TK_MAX_B + 1), p.device);
