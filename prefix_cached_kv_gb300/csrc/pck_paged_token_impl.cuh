@@ -21,11 +21,11 @@
 //    128-byte swizzle, evict-first: read once). Lane i of a warp resolves the i-th of its next 32 units
 //    (sequence, tile, page number) at once, so page-table latency is paid once in 32 units and off the
 //    critical path; rings run on across items.
-//  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads, or rows x q heads, as columns; the running
-//    maximum moves only when a score passes it by 8 (log2), so every p <= 2^8; p goes into
-//    O^T += V^T p^T as a 16-bit hi + lo pair (two MMAs into one accumulator), which keeps ~22 bits
-//    (16 for bf16) of p: the result's own rounding is then the only visible one, and these MMAs are
-//    hidden behind the loads.
+//  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads, or rows x q heads, as columns. m stands TOP
+//    (log2) below the running maximum and moves only when a score passes m by CAP, so every p <= 2^CAP; p goes into
+//    O^T += V^T p^T as a 16-bit hi + lo pair (two MMAs into one accumulator), which keeps 22 bits of p (fp16, of a p
+//    above 2^-15 of the largest one; below that it is held to 2^-37 of the largest) or 16 (bf16, of any p): the
+//    result's own rounding is then the only visible one, and these MMAs are hidden behind the loads.
 //  * An item that lies within one range is finished there; one that crosses ranges leaves a partial [m, l, O]
 //    per range, at most two per range, and a second, programmatically launched kernel joins them.
 //  * When no sequence can have more than TK_DIRECT_UNITS units and the items are not many, each item gets a CTA
@@ -88,6 +88,12 @@ struct TCfg {
 
 template <typename T> struct Elem;
 template <> struct Elem<__half> {
+    // fp16 has no step below 2^-24, so p = 2^-20 would have five bits and 2^-26 none, however many keys have it: the
+    // maximum stands at 2^12 when it moves and may rise to 2^15.9 (65,504 is the largest value). A weight is then
+    // within 2^-37 of the largest one. At 2^0, 40,000 equal keys behind one 24 to 26 (log2) above them moved O by 3e-4 of
+    // the largest |v|. Costs nothing: one cache of 131k tokens 87.8 us as with 2^0, the ragged batch 83.5 against 83.0
+    // (2^7 83.6, 2^14 84.0).
+    static constexpr float TOP = 12.f, CAP = 15.9f;
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         mma16816(c, a, b0, b1);
     }
@@ -103,6 +109,7 @@ template <> struct Elem<__half> {
     }
 };
 template <> struct Elem<__nv_bfloat16> {
+    static constexpr float TOP = 0.f, CAP = 8.f;      // p keeps its bits at any size
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_to
                         if (key > p || (P.window > 0 && key <= p - P.window && key >= P.sinks)) v = -INFINITY;
                     }
                     s4[nb][i] = v;
-                    up |= !(v <= m[nb][i & 1] + 8.f);   // (a NaN too)
+                    up |= !(v <= m[nb][i & 1] + Elem<T>::CAP);   // (a NaN too)
                 }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_to
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        mx = fmaxf(mx, m[nb][i]);
+                        mx = fmaxf(mx - Elem<T>::TOP, m[nb][i]);
                         const float al = m[nb][i] > -INFINITY ? ex2_approx(m[nb][i] - mx) : 0.f;
                         m[nb][i] = mx;
                         l[nb][i] *= al;
