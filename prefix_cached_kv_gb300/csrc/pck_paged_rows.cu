@@ -16,8 +16,8 @@
 //    K-major B operand of S = Q K^T as it lies; V, stored token by token, is the MN-major B operand of
 //    O += P V, so nothing is transposed.
 //  * One warp issues tcgen05.mma: S0(j+1) right behind O0 += P0(j) V(j), then the same for tile 1.
-//  * Warps 0-3 and 4-7 are the tiles' softmax, a thread per row. p = 2^(s - m) at the running maximum, which
-//    is checked by the weights' sum and moved only when that passes 2^15: no pass over the scores looks for
+//  * Warps 0-3 and 4-7 are the tiles' softmax, a thread per row. p = 2^(s - m), m a little below the running maximum;
+//    it is checked by the weights' sum and moved only when that passes its CAP: no pass over the scores looks for
 //    a maximum, and O is rarely rescaled. p is rounded once to the cache's type for the second MMA (a
 //    rounding like that of the 16-bit output); its fp32 sum takes the unrounded p.
 //  * Keys: with a window, the sinks' boxes and then the window's are laid end to end, so no block is spent
@@ -186,6 +186,18 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 
 template <typename T> struct IsBf16 { static constexpr bool value = false; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
+
+// Where the maximum stands when it moves (log2), and the sum of a block's weights up to which it stays. fp16 has no step
+// below 2^-24: with the maximum at 2^0 a weight under 2^-25 of it vanished, however many keys had one (131,070 keys 25
+// (log2) below one: O off by 3.9e-3 of the largest |v|, as much as it is). At 2^6 a weight is within 2^-31 of the largest
+// one, and a block of weights of 1 still sums to 2^13. 4096 ragged prompt rows behind a window of 1024: 163.7 us at 2^0,
+// 163.8 at 2^6, 167.6 at 2^7 (rows whose first block is mostly hidden pass the sum again); 8k prompts as before.
+template <typename T> struct Weights {
+    static constexpr float TOP = 6.f, CAP = 61440.f;      // (a weight is at most the sum, and fp16 ends at 65,504)
+};
+template <> struct Weights<__nv_bfloat16> {
+    static constexpr float TOP = 0.f, CAP = 32768.f;
+};
 template <typename T> __device__ __forceinline__ uint32_t pack16(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack16<__half>(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
 template <> __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float a, float b) {
@@ -753,7 +765,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                         f2_unpack(acc[1], b0, b1);
                         bs = (a0 + a1) + (b0 + b1);
                     };
-                    // The maximum moves only when it has to: a sum up to 2^15 bounds every p by 2^15, which fp16 and
+                    // The maximum moves only when it has to: a sum up to CAP bounds every p by it, which fp16 and
                     // bf16 hold as exactly as smaller ones. Otherwise (and where a row has no maximum yet) the block's
                     // maximum is found, O and l are rescaled, and the weights taken again.
                     bool again = true;
@@ -762,7 +774,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                             if (full) weights(std::false_type());
                             else weights(std::true_type());
                         }
-                        again = __any_sync(0xffffffffu, row_ok && (!(bs <= 32768.f) || m == -INFINITY));
+                        again = __any_sync(0xffffffffu, row_ok && (!(bs <= Weights<T>::CAP) || m == -INFINITY));
                     }
                     if (again) {
                         float bm = -INFINITY;
@@ -783,7 +795,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                                 bm = fmaxf(bm, fmaxf(b0, b1));
                             }
                         }
-                        const float mn = fmaxf(m, bm * sc);
+                        const float mn = fmaxf(m, bm * sc - Weights<T>::TOP);
                         const float al = mn > m ? ex2_approx(m - mn) : 1.0f;     // 0 from m = -inf
                         if (j > 0) {   // O is quiet once P V of the previous block is done
                             if (!__all_sync(0xffffffffu, !failed && wait_bar(bar + B_O + 8 * t, (j - 1) & 1))) failed = true;

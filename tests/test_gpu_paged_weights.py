@@ -53,3 +53,11 @@ def test_token_weights_behind_a_dominant_key(ctx, dtype, n, rows, B, H_kv, G, D,
     # two additions to a lane's sum for each
     tiles = min(n // 16 + 1, 64 + 2 * B * H_kv * (n // 16) // (152 * (8 if D <= 128 else 4)))
     _check(ctx, n, rows, B, H_kv, G, D, dtype, ref.P_SPLIT[dtype], at, 2 * tiles)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n,rows,B,H_kv,G,D", [(131070, 20, 1, 2, 4, 128), (131070, 40, 1, 1, 4, 64),     # keys split
+                                               (131070, 300, 1, 64, 1, 64), (100000, 300, 2, 20, 2, 128)])   # whole
+@pytest.mark.parametrize("at", [0, 777])
+def test_rows_weights_behind_a_dominant_key(ctx, dtype, n, rows, B, H_kv, G, D, at):   # noqa: F811
+    _check(ctx, n, rows, B, H_kv, G, D, dtype, ref.P_ONCE[dtype], at, n // 128 + 1)     # one addition a block of 128 keys
