@@ -295,8 +295,8 @@ int pck_noalloc_status(void *stream, int *code);
  * captured graphs, may overlap when their own buffers do not; on the host, one context is still
  * called by one thread at a time. A value on the device that is out of range (a page number
  * outside [0, n_pages), a rotary position outside the table, a length beyond the table's width, more
- * rows than max_rows) is never followed: the call's results are then invalid and pck_sync reports PCK_ECUDA with code
- * 8, 9 or 10. The current device is left as it was. */
+ * rows than max_rows, cu_rows that descends or points outside [0, T]) is never followed: the call's results are then
+ * invalid and pck_sync reports PCK_ECUDA with code 8, 9 or 10. The current device is left as it was. */
 
 /* A cache: K and V hold [n_pages, H_kv, page_size, D] in any order of the first three dimensions
  * (strides in elements, D innermost and contiguous), fp16 or bf16. Both must be 16-byte aligned,
@@ -311,7 +311,7 @@ typedef struct pck_paged_cache {
 } pck_paged_cache;
 
 /* The sequences of a call. Sequence b's rows are cu_rows[b] .. cu_rows[b+1]-1 of T (cu_rows
- * ascending from 0; rows behind the last sequence's are neither read nor written); they are the
+ * ascending; rows in front of the first sequence's or behind the last's are neither read nor written); they are the
  * last ones of its kv_len[b] cached tokens: row i of its n rows stands at cache position
  * kv_len[b] - n + i, and token p of the cache lies in page table[b][p / page_size], slot
  * p % page_size. Table entries that no visible token needs are not read. cu_rows NULL: one row per
@@ -398,7 +398,7 @@ int pck_info(pck_ctx *ctx, pck_info_t *out);
  * of an M=1 query with |q| * log2(e) / sqrt(D) >= 65504 (or not finite): the M=1 kernels
  * carry q * log2(e) / sqrt(D) as an fp16 hi + lo pair, so |q| < 65504 * sqrt(D) / log2(e)
  * (e.g. 363,000 at D = 64) is the valid range; 8 a page number, 9 a rotary position, 10 a cache
- * length or row count out of range (the paged-tail calls); 11 a page tile of a one-row paged attention; 12 loads, 13
+ * length, row count or cu_rows out of range (the paged-tail calls); 11 a page tile of a one-row paged attention; 12 loads, 13
  * MMAs, 14 softmax, 15 final O of a ragged paged attention. The error word and the selector's counters
  * are then reset, so the context stays usable. */
 int pck_sync(pck_ctx *ctx, void *stream);

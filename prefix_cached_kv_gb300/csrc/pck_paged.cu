@@ -110,12 +110,20 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
         int b = t, n_b_left = 1;
         if (P.cu_rows) {
             int cnt = 0;   // sequences whose rows start at or before t
-            for (int i = lane; i <= P.B; i += L) cnt += P.cu_rows[i] <= t;
+            bool bad = false;
+            for (int i = lane; i <= P.B; i += L) {
+                const int r0 = P.cu_rows[i];
+                cnt += r0 <= t;
+                if (blockIdx.x == 0 && i < P.B) bad |= !rows_sound(r0, P.cu_rows[i + 1], P.T);
+            }
+            if (bad) set_err(P.err, ERR_KV_LEN);
 #pragma unroll
             for (int o = L / 2; o; o >>= 1) cnt += __shfl_xor_sync(mask, cnt, o, L);
             b = cnt - 1;
-            if (b < 0 || b >= P.B) return;         // padding behind the last sequence
-            n_b_left = P.cu_rows[b + 1] - t;
+            if (b < 0 || b >= P.B) return;         // a row of no sequence
+            const int r1 = P.cu_rows[b + 1];
+            if (P.cu_rows[b] > t || r1 <= t) return;   // (nor here: cu_rows does not ascend)
+            n_b_left = r1 - t;
         }
         const int64_t p = (int64_t)P.kv_len[b] - n_b_left;
         if (p < 0) return;                          // no such token: a padded sequence

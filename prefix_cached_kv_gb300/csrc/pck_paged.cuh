@@ -20,7 +20,7 @@ namespace pck {
 // Device error codes of these operators (pck_sync reports them).
 constexpr int ERR_PAGE_ID = 8;       // a page number of the table outside [0, n_pages)
 constexpr int ERR_ROPE_POS = 9;      // a position outside the rotary table
-constexpr int ERR_KV_LEN = 10;         // a cache length beyond the table, or more rows than max_rows
+constexpr int ERR_KV_LEN = 10;       // a cache length beyond the table, more rows than max_rows, or cu_rows that makes no sense
 constexpr int ERR_PAGED_TOKEN = 11;  // one-token attention: a page tile never landed
 constexpr int ERR_ROWS_LOAD = 12;    // row attention: producer, MMA warp, softmax, final O
 constexpr int ERR_ROWS_MMA = 13;
@@ -125,6 +125,9 @@ inline cudaError_t allow_smem(int bytes, int device) {
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
+
+// Whether [r0, r1) can be a sequence's rows among T.
+__device__ __forceinline__ bool rows_sound(int r0, int r1, int T) { return r0 >= 0 && r1 >= r0 && r1 <= T; }
 
 // Orders this thread's earlier view of memory (ordinary loads and stores) before its later TMA accesses.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }

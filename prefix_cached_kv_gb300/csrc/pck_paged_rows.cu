@@ -288,13 +288,15 @@ __device__ __forceinline__ RowTile find_tile(const PagedAttn& P, int idx, int tt
     return P.B <= 32 ? find_tile_by<1>(P, idx, tt, lane) : find_tile_by<8>(P, idx, tt, lane);
 }
 
-// Whether the sequences' tiles are more than the grid was made for: some sequence has more rows than max_rows.
-__device__ __forceinline__ bool too_many_rows(const PagedAttn& P, int tt, int lane) {
-    int64_t total = 0;
-    for (int b = lane; b < P.B; b += 32) total += tiles_of(P.cu_rows[b + 1] - P.cu_rows[b], tt);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    return total > P.row_tiles;
+// Whether a sequence has more rows than max_rows (their tiles may be more than the grid was made for), or cu_rows makes
+// no sense.
+__device__ __forceinline__ bool bad_rows(const PagedAttn& P, int lane) {
+    bool bad = false;
+    for (int b = lane; b < P.B; b += 32) {
+        const int r0 = P.cu_rows[b], r1 = P.cu_rows[b + 1];
+        bad |= !rows_sound(r0, r1, P.T) || r1 - r0 > P.max_rows;
+    }
+    return __any_sync(0xffffffffu, bad);
 }
 
 // The keys of a CTA: boxes of the sinks, [0, se), then [ws, end), laid end to end: total keys, a multiple
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 tma5(s_base + lane * C::TILE + c * C::CHUNK, &P.tm_q, 0, 0, t.row0 + t.tok0 + lane * tpt, c, g, bar + B_Q + 8 * lane);
         }
         __syncwarp();
-        if (blockIdx.x == 0 && too_many_rows(P, tt, lane) && lane == 0) set_err(P.err, ERR_KV_LEN);
+        if (blockIdx.x == 0 && bad_rows(P, lane) && lane == 0) set_err(P.err, ERR_KV_LEN);
     }
     fence_before();
     __syncthreads();

@@ -171,22 +171,17 @@ __device__ __forceinline__ Span span_of(int len, int rows, int window, int sinks
     return s;
 }
 
-// Sequence b's rows: the first one's index and their number (at most max_rows).
+// Sequence b's rows: the first one's index and their number (at most max_rows; none where cu_rows makes no sense).
 struct RowSpan {
     int r0, n;
 };
 template <bool ROWS>
 __device__ __forceinline__ RowSpan rows_of(const PagedAttn& P, int b, bool report) {
     if (!ROWS) return RowSpan{b, 1};
-    RowSpan r;
-    r.r0 = P.cu_rows[b];
-    r.n = P.cu_rows[b + 1] - r.r0;
-    if (r.n > P.max_rows) {
-        if (report) set_err(P.err, ERR_KV_LEN);
-        r.n = P.max_rows;
-    }
-    if (r.n < 0 || r.r0 < 0 || r.r0 > P.T - r.n) r.n = 0;
-    return r;
+    const int r0 = P.cu_rows[b], r1 = P.cu_rows[b + 1];
+    const bool ok = rows_sound(r0, r1, P.T);
+    if (report && !(ok && r1 - r0 <= P.max_rows)) set_err(P.err, ERR_KV_LEN);
+    return RowSpan{r0, ok ? min(r1 - r0, P.max_rows) : 0};
 }
 
 __device__ __forceinline__ int clamp_len(const PagedAttn& P, int b, bool report) {

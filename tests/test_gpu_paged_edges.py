@@ -1,0 +1,69 @@
+"""Calls of the paged tail at the edges of what its interface allows, on the GPU."""
+import math
+
+import pytest
+import torch
+
+from prefix_cached_kv_gb300 import binding
+from tests import paged_ref as ref
+from tests.test_gpu_paged import BF16, F16, F32, _close, _rand, ctx, i32   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _cu(*at):
+    return torch.tensor(at, dtype=i32, device="cuda")
+
+
+def _reports(ctx, fn):
+    """Whether the call sets the device error of a length or row count out of range (and no other)."""
+    ctx.sync()
+    fn()
+    try:
+        ctx.sync()
+    except binding.PckError as e:
+        assert e.code == binding.ECUDA and "code 10" in str(e), str(e)
+        return True
+    return False
+
+
+@pytest.mark.parametrize("max_rows", [2, 3, 4, 300])
+@pytest.mark.parametrize("cu,sound", [((0, 2, 4), True), ((0, 0, 4), True), ((0, 3, 4), True), ((0, 1, 2), True), ((1, 2, 3), True),
+                                      ((0, 3, 5), False), ((0, 4, 2), False), ((2, 0, 4), False), ((-1, 2, 4), False), ((0, 0, -3), False),
+                                      ((0, 2 ** 31 - 1, 4), False), ((-2 ** 31, 2 ** 31 - 1, 4), False), ((5, 5, 6), False)])
+def test_row_counts_that_make_no_sense_are_reported(ctx, cu, sound, max_rows):   # noqa: F811
+    """cu_rows that descends or points outside the call's rows is reported by the append and by either attention, and so
+    are more rows than max_rows; sound ones are not."""
+    pg = ref.Pages(4, [400, 400], 1, 64, 16, F16)
+    c = binding.PagedCache(pg.k, pg.v)
+    T = 4 if max_rows < 300 else 400
+    if T == 400 and not sound and max(cu) <= 6:
+        cu = tuple(x if x in (0, -1) else x * 100 for x in cu)
+    Q = _rand(5, T, 4, 64, dtype=F16)
+    t = _cu(*cu)
+    few = sound and all(b - a <= max_rows for a, b in zip(cu, cu[1:]))
+    assert _reports(ctx, lambda: ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=t, max_rows=max_rows)) is not few
+    k0, v0 = pg.k.clone(), pg.v.clone()
+    assert _reports(ctx, lambda: ctx.paged_append(c, pg.table, pg.lens - 50, Q[:, :1], Q[:, 1:2], cu_rows=t)) is not sound
+    if not sound:      # no token behind the sequences' own was written
+        for b in range(2):
+            for p in range(350, 400):
+                at = (pg.table[b, p // 16].long(), slice(None), p % 16)
+                assert torch.equal(k0[at], pg.k[at]) and torch.equal(v0[at], pg.v[at])
+
+
+def test_rows_in_front_of_and_behind_the_sequences(ctx):   # noqa: F811
+    """Rows that belong to no sequence, before the first or behind the last, are left as they were."""
+    pg = ref.Pages(4, [400, 90], 2, 64, 16, F16)
+    c = binding.PagedCache(pg.k, pg.v)
+    for news, mr in (([3, 2], 3), ([300, 20], None)):
+        T = 2 + sum(news) + 3
+        Q = _rand(5, T, 4, 64, dtype=F16)
+        cu = _cu(2, 2 + news[0], 2 + sum(news))
+        O, L = torch.full((T, 4, 64), 5.0, dtype=F16, device="cuda"), torch.full((T, 4), 6.0, device="cuda")
+        ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=cu, max_rows=mr, O=O, LSE=L)
+        want = ref.attend(pg.k, pg.v, pg.table, [400, 90], news, Q[2:-3])
+        ref.check_attend(O[2:-3], L[2:-3], want, F16, ref.P_ONCE[F16])
+        for x, y in ((O[:2], L[:2]), (O[-3:], L[-3:])):
+            assert (x == 5).all() and (y == 6).all()
+    ctx.sync()
