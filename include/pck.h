@@ -315,8 +315,9 @@ typedef struct pck_paged_cache {
  * last ones of its kv_len[b] cached tokens: row i of its n rows stands at cache position
  * kv_len[b] - n + i, and token p of the cache lies in page table[b][p / page_size], slot
  * p % page_size. Table entries that no visible token needs are not read. cu_rows NULL: one row per
- * sequence (T == B). max_pages * page_size is at most 2^30. Rows with a negative cache position (a padded sequence of length 0) see and
- * store nothing. */
+ * sequence (T == B). max_pages * page_size is at most 2^30. Rows with a negative
+ * cache position (a padded sequence of length 0) see and store nothing: attention gives O = 0 and LSE = -inf (or the
+ * prior's), an append Q = 0. */
 typedef struct pck_paged_batch {
     int B, T;
     const int32_t *cu_rows;   /* device [B + 1], or NULL */

@@ -651,7 +651,8 @@ class Context:
                      q_weight=None, k_weight=None, eps=1e-6, interleaved=False, Q_out=None, stream=None):
         """Store K (normed and rotated as by qk_norm_rope) and V rows [T, H_kv, D] into the cache slots of the last
         rows of each sequence (see pck_paged_batch; kv_len counts them), and norm and rotate Q [T, H_q, D] in the
-        same pass. positions: None takes the cache positions. Returns Q_out (None without Q)."""
+        same pass (0 for a padded sequence's). positions: None takes the cache positions. Returns Q_out (None
+        without Q)."""
         if K.dim() != 3 or K.shape[1:] != (cache.H_kv, cache.D):
             raise ValueError(f"K must be [T, {cache.H_kv}, {cache.D}]")
         T, D, dt, dev = K.shape[0], cache.D, K.dtype, self.device

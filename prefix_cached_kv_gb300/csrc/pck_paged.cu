@@ -126,7 +126,16 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
             n_b_left = r1 - t;
         }
         const int64_t p = (int64_t)P.kv_len[b] - n_b_left;
-        if (p < 0) return;                          // no such token: a padded sequence
+        if (p < 0) {                                // no such token: a padded sequence stores nothing, and its q is 0
+            const float zero[8] = {};
+            if (lane < P.D / 16)
+                for (int h = h0; h < P.q.H; h += P.spt) {
+                    TI* dst = static_cast<TI*>(P.q.out) + (int64_t)t * P.q.out_row + (int64_t)h * P.q.out_head + 16 * lane;
+                    Vec8<TI>::store(dst, zero);
+                    Vec8<TI>::store(dst + 8, zero);
+                }
+            return;
+        }
         if (p >= (int64_t)P.max_pages * P.page) {
             if (lane == 0) set_err(P.err, ERR_KV_LEN);
             return;

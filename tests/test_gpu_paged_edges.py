@@ -67,3 +67,31 @@ def test_rows_in_front_of_and_behind_the_sequences(ctx):   # noqa: F811
         for x, y in ((O[:2], L[:2]), (O[-3:], L[-3:])):
             assert (x == 5).all() and (y == 6).all()
     ctx.sync()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rope", [False, True])
+def test_append_of_padded_sequences_gives_q_zero(ctx, dtype, rope):   # noqa: F811
+    """Rows at a negative cache position store nothing; their Q comes out as zeros, not as it lay in memory."""
+    cache = F16 if dtype == F32 else dtype
+    H_q, H_kv, D = 5, 2, 64
+    for lens, news in (([9, 0, 17, 0], [1, 1, 1, 1]), ([40, 2, 0], [3, 6, 4])):
+        pg = ref.Pages(2, lens, H_kv, D, 16, cache)
+        T = sum(news)
+        x = _rand(3, T + 2, H_q + 2 * H_kv, D, dtype=dtype)
+        one = all(m == 1 for m in news)
+        cu = None if one else _cu(0, *torch.tensor(news).cumsum(0).tolist())
+        n = T if one else T + 2
+        cs = ref.angles(50, 32, "cuda") if rope else None
+        p = torch.tensor([q for _, q in ref.rows_of(lens, news)], device="cuda")
+        for positions in (None, torch.cat((p, p.new_full((2,), 9))).to(i32)[:n] if rope else None):
+            Qo = torch.full((n, H_q, D), math.nan, dtype=dtype, device="cuda")
+            Q = x[:n, :H_q].clone()
+            for out in (Qo, Q):     # of its own, and in place
+                ctx.paged_append(binding.PagedCache(pg.k, pg.v), pg.table, pg.lens, x[:n, H_q:H_q + H_kv], x[:n, H_q + H_kv:], Q=Q,
+                                 cu_rows=cu, cos_sin=cs, positions=positions, norm=True, Q_out=out)
+                assert (out[:T][p < 0] == 0).all()
+                good = p >= 0
+                _close(out[:T][good], ref.norm_rope(x[:T, :H_q][good], None, 1e-6, cs, p[good]), dtype, "q")
+            assert torch.isnan(Qo[T:]).all() and torch.equal(Q[T:], x[T:n, :H_q])    # of no sequence: left as they were
+    ctx.sync()
