@@ -373,7 +373,7 @@ int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
  * O_prior (device fp32 [T, H_q, D]) and LSE_prior ([T, H_q]): attention of the same rows over other
  * keys, e.g. what pck_query_batch gave for a resident prefix: O and LSE are then those over both
  * (both NULL otherwise).
- * One row per sequence (cu_rows NULL), or a few (max_rows * H_q / H_kv at most 16, 8 at D > 128): split
+ * One row per sequence (cu_rows NULL), or a few (min(max_rows, T) * H_q / H_kv at most 16, 8 at D > 128): split
  * over the cache's length and joined; D in {64, 128, 192, 256}. More rows: tiles of 256 rows (tokens x
  * heads of a kv head) on the tensor cores, D in {64, 128}, H_q / H_kv at most 128. B <=
  * PCK_PAGED_MAX_BATCH.

@@ -161,9 +161,10 @@ int attend_shape(pck_ctx* c, const pck_paged_cache* k, const pck_paged_batch* b,
     if (rc != PCK_OK) return rc;
     if (H_q < 1 || H_q > 1024 || H_q % k->H_kv) return ctx_fail(c, PCK_EINVAL, "H_q=%d is not a multiple of H_kv=%d (at most 1024)", H_q, k->H_kv);
     if (window < 0 || sinks < 0) return ctx_fail(c, PCK_EINVAL, "window=%d sinks=%d", window, sinks);
+    p.max_rows = b->max_rows < b->T ? b->max_rows : b->T;     // no sequence has more rows than there are
     if (b->cu_rows) {
-        if (!paged_token_rows_ok(H_q / k->H_kv, b->max_rows, k->D)) {
-            if (!paged_rows_dim_ok(k->D)) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d with %d rows of a sequence: 64 or 128", k->D, b->max_rows);
+        if (!paged_token_rows_ok(H_q / k->H_kv, p.max_rows, k->D)) {
+            if (!paged_rows_dim_ok(k->D)) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d with %d rows of a sequence: 64 or 128", k->D, p.max_rows);
             if (H_q / k->H_kv > 128) return ctx_fail(c, PCK_EUNSUPPORTED, "%d q heads per kv head: at most 128 with cu_rows", H_q / k->H_kv);
         }
     } else if (!paged_token_dim_ok(k->D)) {
@@ -180,7 +181,6 @@ int attend_shape(pck_ctx* c, const pck_paged_cache* k, const pck_paged_batch* b,
     p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
     p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
     p.cu_rows = b->cu_rows;
-    p.max_rows = b->max_rows < b->T ? b->max_rows : b->T;
     p.dtype = k->dtype;
     if ((int64_t)b->B * (((int64_t)b->max_pages * k->page_size + PG_SUB - 1) / PG_SUB + 64) >= (int64_t(1) << 31))
         return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld tokens", b->B, (long long)b->max_pages * k->page_size);

@@ -95,3 +95,16 @@ def test_append_of_padded_sequences_gives_q_zero(ctx, dtype, rope):   # noqa: F8
                 _close(out[:T][good], ref.norm_rope(x[:T, :H_q][good], None, 1e-6, cs, p[good]), dtype, "q")
             assert torch.isnan(Qo[T:]).all() and torch.equal(Q[T:], x[T:n, :H_q])    # of no sequence: left as they were
     ctx.sync()
+
+
+def test_max_rows_beyond_the_rows(ctx):   # noqa: F811
+    """max_rows is a bound: one far above the rows that there are decides nothing that the rows themselves do not."""
+    for D, G, T in ((192, 4, 2), (256, 2, 4), (256, 8, 1), (128, 4, 4), (64, 3, 5)):
+        pg = ref.Pages(6, [300], 2, D, 16, F16)
+        Q = _rand(7, T, 2 * G, D, dtype=F16)
+        c = binding.PagedCache(pg.k, pg.v)
+        want = ref.attend(pg.k, pg.v, pg.table, [300], [T], Q)
+        for mr in (T, 100, 2 ** 31 - 1):
+            O, L = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu(0, T), max_rows=mr)
+            ref.check_attend(O, L, want, F16, ref.P_SPLIT[F16])
+    ctx.sync()
