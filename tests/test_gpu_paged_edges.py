@@ -108,3 +108,20 @@ def test_max_rows_beyond_the_rows(ctx):   # noqa: F811
             O, L = ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu(0, T), max_rows=mr)
             ref.check_attend(O, L, want, F16, ref.P_SPLIT[F16])
     ctx.sync()
+
+
+def test_bounds_wider_than_32_bits(ctx):   # noqa: F811
+    """Windows, sinks and row bounds beyond int32 are as good as the widest, and never wrap to a narrow one."""
+    pg = ref.Pages(6, [300], 2, 64, 16, F16)
+    Q = _rand(7, 3, 4, 64, dtype=F16)
+    c = binding.PagedCache(pg.k, pg.v)
+    at = lambda **kw: ctx.paged_attend(c, pg.table, pg.lens, Q, cu_rows=_cu(0, 3), **kw)   # noqa: E731
+    want = at()
+    for kw in (dict(window=2 ** 32 + 20), dict(window=2 ** 31 + 5), dict(window=20, sinks=2 ** 32 + 1), dict(max_rows=2 ** 32 + 1), dict(window=2 ** 63 - 1)):
+        for a, b in zip(at(**kw), want):
+            assert torch.equal(a, b), kw
+    for kw in (dict(window=-2 ** 32), dict(sinks=-2 ** 32 - 1), dict(max_rows=-2 ** 32 + 1), dict(max_rows=2 ** 32 * -1)):
+        with pytest.raises(binding.PckError) as e:
+            at(**kw)
+        assert e.value.code == binding.EINVAL
+    ctx.sync()
