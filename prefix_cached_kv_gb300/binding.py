@@ -588,9 +588,9 @@ class Context:
 
     def _batch(self, cache, table, kv_len, cu_rows, T, max_rows):
         dev = self.device
-        if T > _INT_MAX or table.shape[-1:] > (_INT_MAX,):
-            raise ValueError("more rows, or a wider table, than 2^31 - 1")
         B, W = kv_len.shape[0] if kv_len.dim() == 1 else -1, table.shape[-1] if table.dim() == 2 else -1
+        if T > _INT_MAX or W > _INT_MAX:
+            raise ValueError("more rows, or a wider table, than 2^31 - 1")
         if not (cache.device == dev and _dense_fit(kv_len, torch.int32, (B,), dev) and _dense_fit(table, torch.int32, (B, W), dev)
                 and (T == B if cu_rows is None else _dense_fit(cu_rows, torch.int32, (B + 1,), dev))):
             if table.dim() != 2 or B < 0:
@@ -607,7 +607,8 @@ class Context:
             _on(dev, kv_len=kv_len, table=table, cu_rows=cu_rows)
         if cu_rows is None:
             return PagedBatchT(B, T, None, kv_len.data_ptr(), table.data_ptr(), W, 1)
-        return PagedBatchT(B, T, cu_rows.data_ptr(), kv_len.data_ptr(), table.data_ptr(), W, T if max_rows is None else _bound(max_rows))
+        max_rows = T if max_rows is None else max_rows if 0 < max_rows <= _INT_MAX else _bound(max_rows)
+        return PagedBatchT(B, T, cu_rows.data_ptr(), kv_len.data_ptr(), table.data_ptr(), W, max_rows)
 
     def qk_norm_rope(self, Q, K, positions=None, cos_sin=None, norm=None, q_weight=None, k_weight=None, eps=1e-6,
                      interleaved=False, Q_out=None, K_out=None, stream=None):
@@ -710,7 +711,8 @@ class Context:
         if Q.dim() != 3 or Q.shape[2] != cache.D:
             raise ValueError(f"Q must be [T, H_q, {cache.D}]")
         T, H_q, _ = shape = Q.shape
-        window, sinks = _bound(window), _bound(sinks)
+        if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
+            window, sinks = _bound(window), _bound(sinks)
         dt, dev = cache.dtype, self.device
         Op, Lp = (None, None) if prior is None else prior
         fits = (_rows_fit(Q, dt, shape, dev) and (O is None or _dense_fit(O, dt, shape, dev))
