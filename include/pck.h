@@ -372,11 +372,17 @@ int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
  * and LSE = -inf. Cached tokens that no row of the call sees are not used, whatever they hold.
  * O_prior (device fp32 [T, H_q, D]) and LSE_prior ([T, H_q]): attention of the same rows over other
  * keys, e.g. what pck_query_batch gave for a resident prefix: O and LSE are then those over both
- * (both NULL otherwise).
+ * (both NULL otherwise). pck_query at M > 1 gives [H_q, M, D] and [H_q, M]: the caller transposes these. `window`
+ * and `sinks` count the tokens of this cache alone and a prior is taken whole, so a layer whose window, or whose first
+ * tokens, lie in a resident prefix is not window + prior.
+ * Scores, maxima, sums and O are held in fp32. The weights 2^(s - m) that multiply V are rounded: in the one-token
+ * kernel to a pair of 16-bit values (22 bits in fp16, 16 in bf16; the output's own rounding is coarser), in the
+ * row kernel once to the cache's type (11 bits, 8 in bf16; prompts of the kind measured then differ from 64 bits by
+ * 1.3 times the output's own rounding). fp16 weights below 2^-37 (rows: 2^-31) of the largest one are lost.
  * One row per sequence (cu_rows NULL), or a few (min(max_rows, T) * H_q / H_kv at most 16, 8 at D > 128): split
  * over the cache's length and joined; D in {64, 128, 192, 256}. More rows: tiles of 256 rows (tokens x
- * heads of a kv head) on the tensor cores, D in {64, 128}, H_q / H_kv at most 128. B <=
- * PCK_PAGED_MAX_BATCH.
+ * heads of a kv head) on the tensor cores, D in {64, 128}, H_q / H_kv at most 128. Other head dimensions, which an
+ * append fills a cache with, return PCK_EUNSUPPORTED. B <= PCK_PAGED_MAX_BATCH.
  * workspace: device, 16-byte aligned, pck_paged_workspace bytes (which may be 0), read and written
  * by this call only while it runs: calls that may overlap need one each. */
 int pck_paged_attend(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int H_q,

@@ -13,18 +13,18 @@
 // pairs when they are adjacent), so a rotation needs no exchange between lanes; the norm's sum takes
 // log2 L shuffles. `spt` subwarps share a token and step over its heads, so the token's table row
 // is read into registers once for H / spt heads: few subwarps per token while there are tokens
-// enough to fill the SMs, many when there are few. 16,384 tokens of 64 + 8 heads of 128: 107 us, 5.7 TB/s read and
-// written (0.84 of a copy); an append of 8 ragged prompts, 32 + 8 + 8 heads: 59 us, 5.5 TB/s.
+// enough to fill the SMs, many when there are few. 16,384 tokens of 64 + 8 heads of 128: 105-107 us, 5.8 TB/s read and
+// written (0.85 of a copy); an append of 8 ragged prompts, 32 + 8 + 8 heads: 59 us, 5.5 TB/s.
 #include "pck_paged.cuh"
 
 namespace pck {
 namespace {
 
 constexpr int NR_THREADS = 256;
-// Heads whose loads a lane has in flight, and blocks per SM (64 registers): 16,384 tokens of 72 heads in 106.7 us; one
-// head 111, four heads 115 (3 blocks); five blocks spill (138).
+// Heads whose loads a lane has in flight, and blocks per SM (64 registers, 16 bytes a thread spilt): 16,384 tokens of 72
+// heads in 106.7 us; one head 111, four heads 115 (3 blocks); five blocks spill many more (138).
 constexpr int NR_HEADS = 2;
-template <typename TI> __host__ __device__ constexpr int nr_blocks() { return sizeof(TI) == 4 ? 3 : 4; }   // fp32 rows take 80 registers
+template <typename TI> __host__ __device__ constexpr int nr_blocks() { return sizeof(TI) == 4 ? 3 : 4; }   // fp32 rows take 80 registers, 16 bytes spilt
 
 template <typename T>
 struct Vec8;   // 8 elements: as they lie in memory (Raw), and as fp32

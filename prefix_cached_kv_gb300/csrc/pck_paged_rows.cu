@@ -27,9 +27,10 @@
 //    shared memory, since 0 * NaN would keep what they hold. V rows of partly hidden blocks that are not
 //    finite are cleared too, and added at the end by the rows that see them.
 //  * Few rows over a long cache: the keys are split over n_split CTAs and a second kernel joins them.
-// Measured: a prompt of 8192 rows, 32 / 8 heads of 128, 355-360 us, 1,530-1,550 TFLOP/s (0.79 of cuBLAS bf16); heads of 64
-// 260-267 us; 4096 rows on 16k tokens 645-690 us; ragged prompts with a window of 1024, 24 / 8 heads, 164 us. A block of
-// both tiles takes ~3,000 cycles where its MMAs take 2,048: the chain softmax - hand-off - P V - S bounds it.
+// Measured: a prompt of 8192 rows, 32 / 8 heads of 128, bf16 355-369 us (1,490-1,550 TFLOP/s, 0.77-0.80 of cuBLAS bf16),
+// fp16 360-379 us; heads of 64 260-267 us; 4096 rows on 16k tokens 640-675 us (3.4 waves of nearly equal CTAs: 0.87 of
+// what an even load would take); ragged prompts with a window of 1024, 24 / 8 heads, 164 us. A block of both tiles takes
+// ~3,000 cycles where its MMAs take 2,048: the chain softmax - hand-off - P V - S bounds it.
 #include <algorithm>
 #include <type_traits>
 
@@ -42,7 +43,8 @@ constexpr int RW_M = 128;              // rows of a tile
 constexpr int RW_BLOCK = 128;          // keys of a block
 constexpr int RW_THREADS = 384;        // two softmax warpgroups; MMA warp, load warp, two warps that look V over
 constexpr int RW_MMA_WARP = 8, RW_LOAD_WARP = 9, RW_EDGE_WARP = 10;
-// registers a thread: 168 at launch (384 x 168 <= 65,536); 216 x 256 + 72 x 128 = 384 x 168 after the split
+// registers a thread: 168 at launch (384 x 168 <= 65,536); 216 x 256 + 72 x 128 = 384 x 168 after the split. (The compiler
+// keeps to 168 for all and spills 80 bytes a thread at D = 128, 68 at 64.)
 constexpr int RW_REGS_SOFTMAX = 216, RW_REGS_OTHER = 72;
 
 template <int D>
@@ -190,7 +192,7 @@ template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; }
 // Where the maximum stands when it moves (log2), and the sum of a block's weights up to which it stays. fp16 has no step
 // below 2^-24: with the maximum at 2^0 a weight under 2^-25 of it vanished, however many keys had one (131,070 keys 25
 // (log2) below one: O off by 3.9e-3 of the largest |v|, as much as it is). At 2^6 a weight is within 2^-31 of the largest
-// one, and a block of weights of 1 still sums to 2^13. 4096 ragged prompt rows behind a window of 1024: 163.7 us at 2^0,
+// one, and a block of weights of 1 still sums to 2^13. Ragged prompts with a window of 1024: 163.7 us at 2^0,
 // 163.8 at 2^6, 167.6 at 2^7 (rows whose first block is mostly hidden pass the sum again); 8k prompts as before.
 template <typename T> struct Weights {
     static constexpr float TOP = 6.f, CAP = 61440.f;      // (a weight is at most the sum, and fp16 ends at 65,504)

@@ -5,8 +5,9 @@
 //   s_j = tau q_h . k_j,  O = sum_j 2^(s_j' - m) v_j / l,  LSE = (m + log2 l) ln 2   (s' = s log2 e)
 // over the visible keys: all n, or with a window W the last W and the first `sinks`.
 //
-// Every K and V byte is read once and used for G = H_q / H_kv heads: 4 G flop per 4 bytes, so HBM
-// bounds it and the kernel's business is to keep loads in flight on every SM whatever the lengths:
+// Every K and V byte is read once and used for G = H_q / H_kv heads (above 16 of them, 8 at D > 128, once for each 16
+// or 8: they are items of their own): 4 G flop per 4 bytes, so HBM bounds it and the kernel's business is to keep loads
+// in flight on every SM whatever the lengths:
 //  * A unit is a cache tile of 16 tokens of one kv head (a page is a multiple of 16, so a unit never
 //    leaves its page). The units of all items (sequence, kv head, group of q heads) laid end to end
 //    are cut into equal ranges from the lengths on the device (one block scan per CTA), so a ragged
@@ -18,7 +19,7 @@
 //    one length (a batch behind one window, say) stay whole where they fill the CTAs: 32 windows of 2048 tokens
 //    46.3 us against 49.2, 24 x 4000 tokens 65 against 72, 16 x 32,000 314 against 319 (8 kv heads of 128).
 //  * One or two CTAs per SM; each warp streams its units through a ring of its own (two TMA tile loads a unit,
-//    128-byte swizzle, evict-first: read once). Lane i of a warp resolves the i-th of its next 32 units
+//    128-byte swizzle, evict-first). Lane i of a warp resolves the i-th of its next 32 units
 //    (sequence, tile, page number) at once, so page-table latency is paid once in 32 units and off the
 //    critical path; rings run on across items.
 //  * S^T = K q^T with the 16 tokens as MMA rows and up to 8 (16) q heads, or rows x q heads, as columns. m stands TOP
@@ -32,8 +33,9 @@
 //    whose warps take its units in turn and join through shared memory: one launch. With more items than SMs
 //    these CTAs too have half the warps (24 sequences of 100 tokens, 8 kv heads: 6.9 us against 11.0; 64 of 500
 //    tokens 27.9 against 36.3).
-// Measured: one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 87 us, 6.2 TB/s; 16 caches of 30-65k tokens
-// (2 kv heads of 256) 230 us, 6.5 TB/s; 64 ragged sequences (8 kv heads of 64) 83 us, 5.5 TB/s.
+// Measured: one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 88 us, 6.1 TB/s; 16 caches of 30-65k tokens
+// (2 kv heads of 256) 232 us, 6.5 TB/s; 64 ragged sequences (8 kv heads of 64) 83.5 us, 5.5 TB/s; 32 windows of 2048
+// tokens (8 kv heads of 128, 8 q heads each) 46 us, 5.0 TB/s.
 #pragma once
 
 #include "pck_paged.cuh"
