@@ -394,6 +394,49 @@ int pck_paged_attend(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
 int pck_paged_workspace(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged_batch *batch, int H_q,
                         int window, int sinks, size_t *bytes);
 
+/* ---- The same tail held in 8 bits.
+ *
+ * A quantised cache: codes K and V [n_pages, H_kv, page_size, D] in FP8 e4m3 (1-4-3 bits, largest value 448, NaN 0x7f,
+ * no infinities) in any order of the first three dimensions (strides in elements, D contiguous; 16-byte aligned, strides of
+ * dimensions larger than 1 positive multiples of 16), and one scale per token and kv head, K_scale and V_scale
+ * [n_pages, H_kv, page_size], contiguous, 16-byte aligned: a power of two 2^(byte - 127) (E8M0; 255 is NaN). A value is
+ * code * 2^(byte - 127). D + 1 bytes a head row where 16-bit pages have 2 D.
+ * page_size, D, the batch, the rotary table, streams, workspaces and errors are as above. */
+typedef struct pck_paged_cache_e4m3 {
+    void *K, *V;                       /* device */
+    uint8_t *K_scale, *V_scale;        /* device */
+    int H_kv, D, page_size;
+    int64_t n_pages;
+    int64_t k_page, k_head, k_token;   /* strides of K */
+    int64_t v_page, v_head, v_token;   /* strides of V */
+} pck_paged_cache_e4m3;
+
+/* pck_paged_append into a quantised cache. dtype: of Q, K and V, F32, F16 or BF16. A head row y (K normed and rotated in fp32, V as
+ * it is) whose largest finite magnitude is a gets the least e with a 2^-e <= 448, held to -126 .. 120 (a row of zeros: -126), and
+ * the codes y 2^-e rounded to nearest even: one rounding, of half a step 2^-4 of the value, or 2^-10 * 2^e where that is
+ * more. Infinities and NaN become NaN. */
+int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int dtype,
+                          const pck_rows *Q, const pck_rows *K, const pck_rows *V, int norm, float eps,
+                          const pck_rotary *rope, void *stream);
+
+/* pck_paged_attend over the values of a quantised cache. q_dtype: of Q and O, F16 or BF16. The workspace holds what the
+ * rows see as 16-bit values of q_dtype (bf16 holds them exactly; fp16 those within its range, beyond which they are 65,504). */
+int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,
+                          const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
+                          const float *O_prior, const float *LSE_prior, void *O, float *LSE,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of that call into *bytes. */
+int pck_paged_workspace_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype,
+                             int H_q, int window, int sinks, size_t *bytes);
+
+/* Rows of a quantised cache read back: each sequence's last cached tokens (its rows, as in pck_paged_batch; cu_rows from
+ * kv_len takes whole caches), K->out and V->out [T, H_kv, D] of dtype F32, F16 or BF16 with the strides given (in and weight are
+ * not used): [H_kv, N, D], as pck_store takes it, is a row stride of D. Values are rounded once (fp32 and bf16
+ * hold them exactly; in fp16 what is beyond 65,504 is 65,504). Rows at a negative cache position are 0. */
+int pck_paged_read_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int dtype,
+                        const pck_rows *K, const pck_rows *V, void *stream);
+
 /* Counters of ctx. */
 int pck_info(pck_ctx *ctx, pck_info_t *out);
 

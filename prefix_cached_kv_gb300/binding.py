@@ -28,7 +28,8 @@ EXPORTS = (
     "pck_query_sparse_auto_fused", "pck_query_batch", "pck_query_sparse_batch", "pck_quantize_mlx4g32", "pck_info", "pck_sync",
     "pck_attend_records_noalloc", "pck_noalloc_status", "pck_query_sparse", "pck_get_block_means",
     "pck_dequantize_mlx4g32", "pck_query_batch_host", "pck_qk_norm_rope", "pck_paged_append", "pck_paged_attend",
-    "pck_paged_workspace",
+    "pck_paged_workspace", "pck_paged_append_e4m3", "pck_paged_attend_e4m3", "pck_paged_workspace_e4m3",
+    "pck_paged_read_e4m3",
 )
 
 
@@ -58,6 +59,12 @@ class PagedCacheT(ctypes.Structure):
     _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("dtype", ctypes.c_int), ("H_kv", ctypes.c_int),
                 ("D", ctypes.c_int), ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int64)] + [
                     (n, ctypes.c_int64) for n in ("k_page", "k_head", "k_token", "v_page", "v_head", "v_token")]
+
+
+class PagedCacheE4m3T(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("K", "V", "K_scale", "V_scale")] + [
+        (n, ctypes.c_int) for n in ("H_kv", "D", "page_size")] + [
+            (n, ctypes.c_int64) for n in ("n_pages", "k_page", "k_head", "k_token", "v_page", "v_head", "v_token")]
 
 
 class PagedBatchT(ctypes.Structure):
@@ -110,6 +117,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "pck_paged_append": (i, [vp, vp, vp, i, vp, vp, vp, i, ctypes.c_float, vp, vp]),
         "pck_paged_attend": (i, [vp, vp, vp, i, vp, i64, i64, i, i, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
         "pck_paged_workspace": (i, [vp, vp, vp, i, i, i, ctypes.POINTER(ctypes.c_size_t)]),
+        "pck_paged_append_e4m3": (i, [vp, vp, vp, i, vp, vp, vp, i, ctypes.c_float, vp, vp]),
+        "pck_paged_attend_e4m3": (i, [vp, vp, vp, i, i, vp, i64, i64, i, i, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "pck_paged_workspace_e4m3": (i, [vp, vp, vp, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]),
+        "pck_paged_read_e4m3": (i, [vp, vp, vp, i, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -313,6 +324,8 @@ class PagedCache:
     strides with D contiguous do: for pages stored [n_pages, page_size, H_kv, D] pass their
     transpose(1, 2). Holds the tensors and the descriptor that the calls take; checked once, here."""
 
+    quantized = False
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v must be [n_pages, H_kv, page_size, D] tensors of one shape and dtype")
@@ -328,6 +341,35 @@ class PagedCache:
         self.n_pages, self.H_kv, self.page_size, self.D = k.shape
         self.c = PagedCacheT(k.data_ptr(), v.data_ptr(), _PAGED_DT[k.dtype], self.H_kv, self.D, self.page_size,
                              self.n_pages, *k.stride()[:3], *v.stride()[:3])
+        self.ref = ctypes.byref(self.c)
+        self._ws = {}   # workspace bytes by the sizes of a call
+
+
+class QuantizedPagedCache:
+    """A paged KV cache in 8 bits, of the caller's: codes k and v [n_pages, H_kv, page_size, D], float8_e4m3fn, with any
+    strides that keep D contiguous, and one scale per token and kv head, k_scale and v_scale [n_pages, H_kv, page_size],
+    contiguous, float8_e8m0fnu (or uint8, the exponent bytes). The calls of the paged tail take it in a PagedCache's place:
+    rows come in any of their types, and attention's Q and O are fp16 or bf16."""
+
+    quantized = True
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [n_pages, H_kv, page_size, D] tensors of one shape")
+        for t, name in ((k, "k"), (v, "v")):
+            _need(t, name, torch.float8_e4m3fn, k.shape, strided=True)
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype not in (torch.float8_e8m0fnu, torch.uint8):
+                raise ValueError(f"{name}: dtype {t.dtype}, expected float8_e8m0fnu or uint8")
+            _need(t, name, t.dtype, k.shape[:3])
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not t.is_cuda:
+                raise ValueError(f"{name}: must be on the CUDA device")
+        _on(k.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.k, self.v, self.k_scale, self.v_scale, self.device, self.dtype = k, v, k_scale, v_scale, k.device, k.dtype
+        self.n_pages, self.H_kv, self.page_size, self.D = k.shape
+        self.c = PagedCacheE4m3T(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.H_kv, self.D,
+                                 self.page_size, self.n_pages, *k.stride()[:3], *v.stride()[:3])
         self.ref = ctypes.byref(self.c)
         self._ws = {}   # workspace bytes by the sizes of a call
 
@@ -664,13 +706,13 @@ class Context:
                      q_weight=None, k_weight=None, eps=1e-6, interleaved=False, Q_out=None, stream=None):
         """Store K (normed and rotated as by qk_norm_rope) and V rows [T, H_kv, D] into the cache slots of the last
         rows of each sequence (see pck_paged_batch; kv_len counts them), and norm and rotate Q [T, H_q, D] in the
-        same pass (0 for a padded sequence's). positions: None takes the cache positions. Returns Q_out (None
-        without Q)."""
+        same pass (0 for a padded sequence's). positions: None takes the cache positions. A QuantizedPagedCache gets the
+        rows as codes and scales (see pck_paged_append_e4m3). Returns Q_out (None without Q)."""
         if K.dim() != 3 or K.shape[1:] != (cache.H_kv, cache.D):
             raise ValueError(f"K must be [T, {cache.H_kv}, {cache.D}]")
         T, D, dt, dev = K.shape[0], cache.D, K.dtype, self.device
-        if dt != cache.dtype and dt != torch.float32:
-            raise ValueError(f"K: dtype {dt}, expected {cache.dtype} or float32")
+        if dt not in _ROWS_DT if cache.quantized else dt != cache.dtype and dt != torch.float32:
+            raise ValueError(f"K: dtype {dt}, expected {'float16, bfloat16' if cache.quantized else cache.dtype} or float32")
         norm = (q_weight is not None or k_weight is not None) if norm is None else bool(norm)
         fits = (_rows_fit(K, dt, K.shape, dev) and _rows_fit(V, dt, K.shape, dev)
                 and _side_fits(Q, Q_out, q_weight, dt, T, D, dev, norm)
@@ -698,7 +740,7 @@ class Context:
             _on(dev, K=K, V=V, Q=Q, Q_out=Q_out, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, positions=positions)
         if Q is not None and Q_out is None:
             Q_out = self._empty(stream, Q.shape, dt)
-        self._launch(self.lib.pck_paged_append, stream, cache.ref, ctypes.byref(batch), _ROWS_DT[dt],
+        self._launch(self.lib.pck_paged_append_e4m3 if cache.quantized else self.lib.pck_paged_append, stream, cache.ref, ctypes.byref(batch), _ROWS_DT[dt],
                      self._put_rows(0, Q, Q_out, q_weight), self._put_rows(1, K, None, k_weight), self._put_rows(2, V, None, None),
                      norm, eps, self._put_rotary(cos_sin, interleaved, positions))
         return Q_out
@@ -707,13 +749,17 @@ class Context:
                      LSE=None, want_lse=True, workspace=None, stream=None):
         """Attention of Q [T, H_q, D] over the cached tokens of its sequences (see pck_paged_attend); prior: (O, LSE)
         of the same rows over other keys, fp32, merged in. max_rows bounds the rows of a sequence (default: T with
-        cu_rows, else 1). Outputs and the workspace are allocated when not given. Returns (O, LSE)."""
+        cu_rows, else 1). Outputs and the workspace are allocated when not given; over a QuantizedPagedCache O is of
+        Q's type, fp16 or bf16. Returns (O, LSE)."""
         if Q.dim() != 3 or Q.shape[2] != cache.D:
             raise ValueError(f"Q must be [T, H_q, {cache.D}]")
         T, H_q, _ = shape = Q.shape
         if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
             window, sinks = _bound(window), _bound(sinks)
-        dt, dev = cache.dtype, self.device
+        quantized, dev = cache.quantized, self.device
+        dt = Q.dtype if quantized else cache.dtype
+        if quantized and dt not in _PAGED_DT:
+            raise ValueError(f"Q: dtype {dt}, expected float16 or bfloat16")
         Op, Lp = (None, None) if prior is None else prior
         fits = (_rows_fit(Q, dt, shape, dev) and (O is None or _dense_fit(O, dt, shape, dev))
                 and (LSE is None or _dense_fit(LSE, torch.float32, (T, H_q), dev))
@@ -732,10 +778,15 @@ class Context:
             _on(dev, Q=Q, O=O, LSE=LSE, prior_O=Op, prior_LSE=Lp, workspace=workspace)
         bref = ctypes.byref(batch)
         key = (batch.B, T, batch.max_pages, batch.max_rows, cu_rows is None, H_q, window, sinks, self.h.value)
+        if quantized:
+            key += (dt,)
         need = cache._ws.get(key)
         if need is None:
             n = ctypes.c_size_t()
-            self._rc(self.lib.pck_paged_workspace(self.h, cache.ref, bref, H_q, window, sinks, ctypes.byref(n)))
+            if quantized:
+                self._rc(self.lib.pck_paged_workspace_e4m3(self.h, cache.ref, bref, _PAGED_DT[dt], H_q, window, sinks, ctypes.byref(n)))
+            else:
+                self._rc(self.lib.pck_paged_workspace(self.h, cache.ref, bref, H_q, window, sinks, ctypes.byref(n)))
             if len(cache._ws) >= 256:
                 cache._ws.clear()
             need = cache._ws[key] = n.value
@@ -748,11 +799,47 @@ class Context:
         if LSE is None and want_lse:
             LSE = self._empty(stream, (T, H_q), torch.float32)
         st = Q.stride()
-        self._launch(self.lib.pck_paged_attend, stream, cache.ref, bref, H_q, Q.data_ptr(), st[0], st[1], window, sinks,
-                     None if Op is None else Op.data_ptr(), None if Lp is None else Lp.data_ptr(), O.data_ptr(),
-                     None if LSE is None else LSE.data_ptr(), None if workspace is None else workspace.data_ptr(),
-                     0 if workspace is None else workspace.numel() * workspace.element_size())
+        rest = (H_q, Q.data_ptr(), st[0], st[1], window, sinks, None if Op is None else Op.data_ptr(),
+                None if Lp is None else Lp.data_ptr(), O.data_ptr(), None if LSE is None else LSE.data_ptr(),
+                None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel() * workspace.element_size())
+        if quantized:
+            self._launch(self.lib.pck_paged_attend_e4m3, stream, cache.ref, bref, _PAGED_DT[dt], *rest)
+        else:
+            self._launch(self.lib.pck_paged_attend, stream, cache.ref, bref, *rest)
         return O, LSE
+
+    def paged_read(self, cache, table, kv_len, T=None, cu_rows=None, dtype=torch.float16, K_out=None, V_out=None, stream=None):
+        """Rows of a QuantizedPagedCache as values: the last ones of each sequence (see pck_paged_read_e4m3), T in all
+        (default: one of each; needed with cu_rows unless K_out and V_out are given). K_out and V_out [T, H_kv, D], float32,
+        float16 or bfloat16, any strides with D contiguous, are allocated of `dtype` when not given. Returns (K_out, V_out)."""
+        if not cache.quantized:
+            raise ValueError("cache: a QuantizedPagedCache is needed")
+        if (K_out is None) != (V_out is None):
+            raise ValueError("K_out and V_out go together")
+        if K_out is not None and K_out.dim() != 3:
+            raise ValueError(f"K_out must be [T, {cache.H_kv}, {cache.D}]")
+        if T is None:
+            if K_out is None and cu_rows is not None:
+                raise ValueError("T is needed with cu_rows")
+            T = kv_len.numel() if K_out is None else K_out.shape[0]
+        if T < 0:
+            raise ValueError(f"T={T}")
+        dev, shape = self.device, (T, cache.H_kv, cache.D)
+        dt = dtype if K_out is None else K_out.dtype
+        if dt not in _ROWS_DT:
+            raise ValueError(f"dtype {dt}, expected float32, float16 or bfloat16")
+        fits = K_out is None or _rows_fit(K_out, dt, shape, dev) and _rows_fit(V_out, dt, shape, dev)
+        if not fits:
+            _need(K_out, "K_out", dt, shape, strided=True)
+            _need(V_out, "V_out", dt, shape, strided=True)
+        batch = self._batch(cache, table, kv_len, cu_rows, T, None)
+        if not fits:
+            _on(dev, K_out=K_out, V_out=V_out)
+        if K_out is None:
+            K_out, V_out = self._empty(stream, shape, dt), self._empty(stream, shape, dt)
+        self._launch(self.lib.pck_paged_read_e4m3, stream, cache.ref, ctypes.byref(batch), _ROWS_DT[dt],
+                     self._put_rows(0, K_out, K_out, None), self._put_rows(1, V_out, V_out, None))
+        return K_out, V_out
 
     def info(self) -> dict:
         out = InfoT()

@@ -50,6 +50,7 @@ struct RopeParams {
     const int32_t* positions;        // [T] or nullptr (append: the row's cache position)
     // append: destination pages of k and v (out strides: page, head, token)
     int append;
+    uint8_t *k_scale, *v_scale;      // a quantised cache's scales [n_pages, H_kv, page]
     int B, page, max_pages;
     int64_t n_pages, k_page, v_page;
     const int32_t* cu_rows;

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "pck_paged.cuh"
+#include "pck_paged_e4m3.cuh"
 
 using namespace pck;
 
@@ -27,6 +28,7 @@ struct DeviceScope {
     }
 };
 
+constexpr int DT_E4M3 = -1;             // run_rope: the append to a quantised cache
 constexpr int MAX_TOKENS = 1 << 30;     // of one sequence, by the table's width; windows and sinks are cut to it
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -67,19 +69,31 @@ bool encode_pages(CUtensorMap* tm, int dtype, void* base, int page_size, int D, 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int check_cache(pck_ctx* c, const pck_paged_cache* k) {
-    if (!k || !k->K || !k->V) return ctx_fail(c, PCK_EINVAL, "NULL cache");
-    if (k->dtype != PCK_DT_F16 && k->dtype != PCK_DT_BF16) return ctx_fail(c, PCK_EINVAL, "cache dtype %d is not fp16 or bf16", k->dtype);
+// What both kinds of cache have in common; strides in multiples of `elems` elements (16 bytes).
+template <typename Cache>
+int check_pages(pck_ctx* c, const Cache* k, int elems) {
     if (k->H_kv < 1 || k->H_kv > PCK_MAX_HEADS) return ctx_fail(c, PCK_EINVAL, "H_kv=%d out of range [1, %d]", k->H_kv, PCK_MAX_HEADS);
     if (k->D < 16 || k->D > 512 || k->D % 16) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d is not a multiple of 16 up to 512", k->D);
     if (k->page_size < 16 || k->page_size % 16 || k->page_size > (1 << 20))
         return ctx_fail(c, PCK_EUNSUPPORTED, "page_size=%d is not a multiple of 16 (at most 2^20)", k->page_size);
     if (k->n_pages < 1 || k->n_pages >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EINVAL, "n_pages=%lld out of range", (long long)k->n_pages);
     if (!aligned16(k->K) || !aligned16(k->V)) return ctx_fail(c, PCK_EINVAL, "K and V must be 16-byte aligned");
-    if (!stride_ok(k->k_page, k->n_pages, 8) || !stride_ok(k->k_head, k->H_kv, 8) || !stride_ok(k->k_token, k->page_size, 8) ||
-        !stride_ok(k->v_page, k->n_pages, 8) || !stride_ok(k->v_head, k->H_kv, 8) || !stride_ok(k->v_token, k->page_size, 8))
-        return ctx_fail(c, PCK_EINVAL, "cache strides must be positive multiples of 8 elements");
+    if (!stride_ok(k->k_page, k->n_pages, elems) || !stride_ok(k->k_head, k->H_kv, elems) || !stride_ok(k->k_token, k->page_size, elems) ||
+        !stride_ok(k->v_page, k->n_pages, elems) || !stride_ok(k->v_head, k->H_kv, elems) || !stride_ok(k->v_token, k->page_size, elems))
+        return ctx_fail(c, PCK_EINVAL, "cache strides must be positive multiples of %d elements", elems);
     return PCK_OK;
+}
+
+int check_cache(pck_ctx* c, const pck_paged_cache* k) {
+    if (!k || !k->K || !k->V) return ctx_fail(c, PCK_EINVAL, "NULL cache");
+    if (k->dtype != PCK_DT_F16 && k->dtype != PCK_DT_BF16) return ctx_fail(c, PCK_EINVAL, "cache dtype %d is not fp16 or bf16", k->dtype);
+    return check_pages(c, k, 8);
+}
+
+int check_cache(pck_ctx* c, const pck_paged_cache_e4m3* k) {
+    if (!k || !k->K || !k->V || !k->K_scale || !k->V_scale) return ctx_fail(c, PCK_EINVAL, "NULL cache or scales");
+    if (!aligned16(k->K_scale) || !aligned16(k->V_scale)) return ctx_fail(c, PCK_EINVAL, "K_scale and V_scale must be 16-byte aligned");
+    return check_pages(c, k, 16);
 }
 
 int check_batch(pck_ctx* c, const pck_paged_batch* b, int page_size) {
@@ -147,7 +161,8 @@ int run_rope(pck_ctx* c, const RopeParams& p, int in_dtype, int cache_dtype, voi
     const CtxView v = ctx_view(c);
     DeviceScope dev(v.device);
     if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
-    const cudaError_t e = launch_norm_rope(p, in_dtype, cache_dtype, v.sms, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cache_dtype == DT_E4M3 ? launch_append_e4m3(p, in_dtype, v.sms, st) : launch_norm_rope(p, in_dtype, cache_dtype, v.sms, st);
     return e == cudaSuccess ? PCK_OK : ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
 }
 
@@ -209,42 +224,14 @@ bool encode_q(CUtensorMap* tm, const PagedAttn& p, int D, int tokens) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-extern "C" {
-
-int pck_qk_norm_rope(pck_ctx* c, int dtype, int T, int D, const pck_rows* Q, const pck_rows* K, int norm, float eps,
-                     const pck_rotary* rope, void* stream) {
-    if (!c) return PCK_EINVAL;
-    if (!dtype_any(dtype)) return ctx_fail(c, PCK_EINVAL, "dtype=%d", dtype);
-    if (T < 0) return ctx_fail(c, PCK_EINVAL, "T=%d", T);
-    if (D < 16 || D > 512 || D % 16) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d is not a multiple of 16 up to 512", D);
-    if (!norm && !rope) return ctx_fail(c, PCK_EINVAL, "neither a norm nor a rotation");
-    if (T == 0) return PCK_OK;
-    if ((!Q || !Q->in) && (!K || !K->in)) return ctx_fail(c, PCK_EINVAL, "neither Q nor K");
-    if (norm && !(eps >= 0.f)) return ctx_fail(c, PCK_EINVAL, "eps=%g", eps);
-    int rc = PCK_OK;
-    if (Q && Q->in && (rc = check_rows(c, Q, "Q", T, D, dtype, true)) != PCK_OK) return rc;
-    if (K && K->in && (rc = check_rows(c, K, "K", T, D, dtype, true)) != PCK_OK) return rc;
-    if ((rc = check_rope(c, rope, D, true)) != PCK_OK) return rc;
-    RopeParams p = {};
-    p.q = rows_arg(Q, norm != 0);
-    p.k = rows_arg(K, norm != 0);
-    p.T = T;
-    p.D = D;
-    p.eps = eps;
-    set_rope(p, rope);
-    p.err = ctx_view(c).dev_err;
-    return run_rope(c, p, dtype, PCK_DT_F16, stream);
-}
-
-int pck_paged_append(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int dtype, const pck_rows* Q,
-                     const pck_rows* K, const pck_rows* V, int norm, float eps, const pck_rotary* rope, void* stream) {
-    if (!c) return PCK_EINVAL;
+// The append to either kind of cache; dtype_ok: whether the rows' type suits it.
+template <typename Cache>
+int append_rows(pck_ctx* c, const Cache* cache, const pck_paged_batch* batch, int dtype, bool dtype_ok, const pck_rows* Q,
+                const pck_rows* K, const pck_rows* V, int norm, float eps, const pck_rotary* rope, RopeParams& p) {
     int rc = check_cache(c, cache);
     if (rc != PCK_OK) return rc;
     if ((rc = check_batch(c, batch, cache->page_size)) != PCK_OK) return rc;
-    if (dtype != cache->dtype && dtype != PCK_DT_F32) return ctx_fail(c, PCK_EINVAL, "dtype=%d is neither the cache's nor fp32", dtype);
+    if (!dtype_ok) return ctx_fail(c, PCK_EINVAL, "dtype=%d does not suit the cache (its own type or fp32)", dtype);
     if (batch->T == 0 || batch->B == 0) return PCK_OK;
     if (!K || !K->in || !V || !V->in) return ctx_fail(c, PCK_EINVAL, "NULL K or V");
     if (K->H != cache->H_kv || V->H != cache->H_kv) return ctx_fail(c, PCK_EINVAL, "K and V have %d and %d heads, the cache %d", K->H, V->H, cache->H_kv);
@@ -254,7 +241,6 @@ int pck_paged_append(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     if ((rc = check_rows(c, K, "K", T, D, dtype, false)) != PCK_OK) return rc;
     if ((rc = check_rows(c, V, "V", T, D, dtype, false)) != PCK_OK) return rc;
     if ((rc = check_rope(c, rope, D, false)) != PCK_OK) return rc;
-    RopeParams p = {};
     p.q = rows_arg(Q, norm != 0);
     p.k = rows_arg(K, norm != 0);
     p.v = rows_arg(V, false);
@@ -279,33 +265,28 @@ int pck_paged_append(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     p.kv_len = batch->kv_len;
     p.table = batch->table;
     p.err = ctx_view(c).dev_err;
-    return run_rope(c, p, dtype, cache->dtype, stream);
-}
-
-int pck_paged_workspace(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, int window, int sinks,
-                        size_t* bytes) {
-    if (!c) return PCK_EINVAL;
-    if (!bytes) return ctx_fail(c, PCK_EINVAL, "NULL bytes");
-    PagedAttn p = {};
-    const int rc = attend_shape(c, cache, batch, H_q, window, sinks, p);
-    if (rc != PCK_OK) return rc;
-    *bytes = p.B == 0 || p.T == 0 ? 0 : attend_plan(p, cache->D, ctx_view(c).sms);
     return PCK_OK;
 }
 
-int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, const void* Q, int64_t q_row,
-                     int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O, float* LSE,
-                     void* workspace, size_t workspace_bytes, void* stream) {
-    if (!c) return PCK_EINVAL;
+int check_attend_rows(pck_ctx* c, int T, int H_q, const void* Q, int64_t q_row, int64_t q_head, const float* O_prior,
+                      const float* LSE_prior, const void* O, const void* workspace) {
+    if (!Q || !O) return ctx_fail(c, PCK_EINVAL, "NULL Q or O");
+    if (!aligned16(Q) || !aligned16(O) || !aligned16(O_prior) || !aligned16(workspace))
+        return ctx_fail(c, PCK_EINVAL, "Q, O, O_prior and the workspace must be 16-byte aligned");
+    if (!stride_ok(q_row, T, 8) || !stride_ok(q_head, H_q, 8)) return ctx_fail(c, PCK_EINVAL, "Q strides must be positive multiples of 8");
+    if ((O_prior != nullptr) != (LSE_prior != nullptr)) return ctx_fail(c, PCK_EINVAL, "O_prior and LSE_prior go together");
+    return PCK_OK;
+}
+
+int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, const void* Q, int64_t q_row,
+               int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O, float* LSE,
+               void* workspace, size_t workspace_bytes, void* stream) {
     PagedAttn p = {};
     const int rc = attend_shape(c, cache, batch, H_q, window, sinks, p);
     if (rc != PCK_OK) return rc;
     if (p.B == 0 || p.T == 0) return PCK_OK;
-    if (!Q || !O) return ctx_fail(c, PCK_EINVAL, "NULL Q or O");
-    if (!aligned16(Q) || !aligned16(O) || !aligned16(O_prior) || !aligned16(workspace))
-        return ctx_fail(c, PCK_EINVAL, "Q, O, O_prior and the workspace must be 16-byte aligned");
-    if (!stride_ok(q_row, p.T, 8) || !stride_ok(q_head, H_q, 8)) return ctx_fail(c, PCK_EINVAL, "Q strides must be positive multiples of 8");
-    if ((O_prior != nullptr) != (LSE_prior != nullptr)) return ctx_fail(c, PCK_EINVAL, "O_prior and LSE_prior go together");
+    const int rc2 = check_attend_rows(c, p.T, H_q, Q, q_row, q_head, O_prior, LSE_prior, O, workspace);
+    if (rc2 != PCK_OK) return rc2;
     const CtxView v = ctx_view(c);
     const int D = cache->D;
     const size_t need = attend_plan(p, D, v.sms);
@@ -341,6 +322,214 @@ int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
     if (e != cudaSuccess) return ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
     ctx_count_query(c);
     return PCK_OK;
+}
+
+// Attention over a quantised cache through 16-bit pages: what the rows see is read back into pages of the workspace (of Q's
+// type, in the order of the sequences), and those are attended to.
+struct Expanded {
+    pck_paged_cache cache;           // of the workspace; K and V are set by the call
+    pck_paged_batch batch;           // its table is the workspace's page map
+    int slots;                       // pages of a sequence
+    size_t off_v, off_map, off_inner, total;    // workspace: K, V, page map, the attention's own
+};
+
+int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batch* b, int q_dtype, int H_q, int window, int sinks, Expanded& x) {
+    x = Expanded{};
+    int rc = check_cache(c, k);
+    if (rc != PCK_OK) return rc;
+    if ((rc = check_batch(c, b, k->page_size)) != PCK_OK) return rc;
+    if (q_dtype != PCK_DT_F16 && q_dtype != PCK_DT_BF16) return ctx_fail(c, PCK_EINVAL, "q_dtype=%d is not fp16 or bf16", q_dtype);
+    if (window < 0 || sinks < 0) return ctx_fail(c, PCK_EINVAL, "window=%d sinks=%d", window, sinks);
+    const int64_t page = k->page_size;
+    int64_t slots = b->max_pages;
+    if (window > 0) {
+        const int64_t rows = b->cu_rows ? (b->max_rows < b->T ? b->max_rows : b->T) : 1;
+        const int64_t some = (sinks + page - 1) / page + (window + rows) / page + 2;
+        if (some < slots) slots = some;
+    }
+    const int64_t pages = b->B * slots;
+    if (pages >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld pages", b->B, (long long)slots);
+    x.slots = static_cast<int>(slots);
+    void* const some = reinterpret_cast<void*>(256);                     // stands for the workspace in the checks
+    x.cache = pck_paged_cache{some, some, q_dtype, k->H_kv, k->D, k->page_size, pages > 0 ? pages : 1,
+                              k->H_kv * page * k->D, page * k->D, k->D, k->H_kv * page * k->D, page * k->D, k->D};
+    x.batch = *b;
+    PagedAttn p = {};
+    if ((rc = attend_shape(c, &x.cache, b, H_q, window, sinks, p)) != PCK_OK) return rc;
+    if (p.B == 0 || p.T == 0) return PCK_OK;
+    const size_t side = (size_t)pages * k->H_kv * page * k->D * 2;       // a multiple of 512 bytes
+    x.off_v = side;
+    x.off_map = 2 * side;
+    x.off_inner = x.off_map + (((size_t)b->B * b->max_pages * 4 + 255) & ~size_t(255));
+    x.total = x.off_inner + attend_plan(p, k->D, ctx_view(c).sms);
+    return PCK_OK;
+}
+
+void read_params(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batch* b, ReadParams& p) {
+    p.K = static_cast<const uint8_t*>(k->K);
+    p.V = static_cast<const uint8_t*>(k->V);
+    p.k_scale = k->K_scale;
+    p.v_scale = k->V_scale;
+    p.k_page = k->k_page;
+    p.k_head = k->k_head;
+    p.k_token = k->k_token;
+    p.v_page = k->v_page;
+    p.v_head = k->v_head;
+    p.v_token = k->v_token;
+    p.H = k->H_kv;
+    p.D = k->D;
+    p.page = k->page_size;
+    p.n_pages = k->n_pages;
+    p.B = b->B;
+    p.T = b->T;
+    p.max_pages = b->max_pages;
+    p.cu_rows = b->cu_rows;
+    p.kv_len = b->kv_len;
+    p.table = b->table;
+    p.err = ctx_view(c).dev_err;
+}
+
+int run_read(pck_ctx* c, const ReadParams& p, int out_dtype, void* stream) {
+    const CtxView v = ctx_view(c);
+    DeviceScope dev(v.device);
+    if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
+    const cudaError_t e = launch_paged_read(p, out_dtype, v.sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PCK_OK : ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" {
+
+int pck_qk_norm_rope(pck_ctx* c, int dtype, int T, int D, const pck_rows* Q, const pck_rows* K, int norm, float eps,
+                     const pck_rotary* rope, void* stream) {
+    if (!c) return PCK_EINVAL;
+    if (!dtype_any(dtype)) return ctx_fail(c, PCK_EINVAL, "dtype=%d", dtype);
+    if (T < 0) return ctx_fail(c, PCK_EINVAL, "T=%d", T);
+    if (D < 16 || D > 512 || D % 16) return ctx_fail(c, PCK_EUNSUPPORTED, "D=%d is not a multiple of 16 up to 512", D);
+    if (!norm && !rope) return ctx_fail(c, PCK_EINVAL, "neither a norm nor a rotation");
+    if (T == 0) return PCK_OK;
+    if ((!Q || !Q->in) && (!K || !K->in)) return ctx_fail(c, PCK_EINVAL, "neither Q nor K");
+    if (norm && !(eps >= 0.f)) return ctx_fail(c, PCK_EINVAL, "eps=%g", eps);
+    int rc = PCK_OK;
+    if (Q && Q->in && (rc = check_rows(c, Q, "Q", T, D, dtype, true)) != PCK_OK) return rc;
+    if (K && K->in && (rc = check_rows(c, K, "K", T, D, dtype, true)) != PCK_OK) return rc;
+    if ((rc = check_rope(c, rope, D, true)) != PCK_OK) return rc;
+    RopeParams p = {};
+    p.q = rows_arg(Q, norm != 0);
+    p.k = rows_arg(K, norm != 0);
+    p.T = T;
+    p.D = D;
+    p.eps = eps;
+    set_rope(p, rope);
+    p.err = ctx_view(c).dev_err;
+    return run_rope(c, p, dtype, PCK_DT_F16, stream);
+}
+
+int pck_paged_append(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int dtype, const pck_rows* Q,
+                     const pck_rows* K, const pck_rows* V, int norm, float eps, const pck_rotary* rope, void* stream) {
+    if (!c) return PCK_EINVAL;
+    RopeParams p = {};
+    const int rc = append_rows(c, cache, batch, dtype, cache && (dtype == cache->dtype || dtype == PCK_DT_F32), Q, K, V, norm, eps, rope, p);
+    if (rc != PCK_OK || p.T == 0) return rc;
+    return run_rope(c, p, dtype, cache->dtype, stream);
+}
+
+int pck_paged_append_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int dtype, const pck_rows* Q,
+                          const pck_rows* K, const pck_rows* V, int norm, float eps, const pck_rotary* rope, void* stream) {
+    if (!c) return PCK_EINVAL;
+    RopeParams p = {};
+    const int rc = append_rows(c, cache, batch, dtype, dtype_any(dtype), Q, K, V, norm, eps, rope, p);
+    if (rc != PCK_OK || p.T == 0) return rc;
+    p.k_scale = cache->K_scale;
+    p.v_scale = cache->V_scale;
+    return run_rope(c, p, dtype, DT_E4M3, stream);
+}
+
+int pck_paged_workspace(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, int window, int sinks,
+                        size_t* bytes) {
+    if (!c) return PCK_EINVAL;
+    if (!bytes) return ctx_fail(c, PCK_EINVAL, "NULL bytes");
+    PagedAttn p = {};
+    const int rc = attend_shape(c, cache, batch, H_q, window, sinks, p);
+    if (rc != PCK_OK) return rc;
+    *bytes = p.B == 0 || p.T == 0 ? 0 : attend_plan(p, cache->D, ctx_view(c).sms);
+    return PCK_OK;
+}
+
+int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, const void* Q, int64_t q_row,
+                     int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O, float* LSE,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    if (!c) return PCK_EINVAL;
+    return attend_run(c, cache, batch, H_q, Q, q_row, q_head, window, sinks, O_prior, LSE_prior, O, LSE, workspace, workspace_bytes, stream);
+}
+
+int pck_paged_workspace_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int q_dtype, int H_q, int window,
+                             int sinks, size_t* bytes) {
+    if (!c) return PCK_EINVAL;
+    if (!bytes) return ctx_fail(c, PCK_EINVAL, "NULL bytes");
+    Expanded x;
+    const int rc = expand_shape(c, cache, batch, q_dtype, H_q, window, sinks, x);
+    if (rc != PCK_OK) return rc;
+    *bytes = x.total;
+    return PCK_OK;
+}
+
+int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int q_dtype, int H_q, const void* Q,
+                          int64_t q_row, int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O,
+                          float* LSE, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!c) return PCK_EINVAL;
+    Expanded x;
+    int rc = expand_shape(c, cache, batch, q_dtype, H_q, window, sinks, x);
+    if (rc != PCK_OK || x.total == 0) return rc;
+    if ((rc = check_attend_rows(c, batch->T, H_q, Q, q_row, q_head, O_prior, LSE_prior, O, workspace)) != PCK_OK) return rc;
+    if (workspace_bytes < x.total || !workspace)
+        return ctx_fail(c, PCK_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, x.total);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    x.cache.K = ws;
+    x.cache.V = ws + x.off_v;
+    x.batch.table = reinterpret_cast<int32_t*>(ws + x.off_map);
+    ReadParams p = {};
+    read_params(c, cache, batch, p);
+    p.max_rows = batch->cu_rows ? (batch->max_rows < batch->T ? batch->max_rows : batch->T) : 1;
+    p.Ko = x.cache.K;
+    p.Vo = x.cache.V;
+    p.pages = 1;
+    p.slots = x.slots;
+    p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
+    p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
+    p.page_map = reinterpret_cast<int32_t*>(ws + x.off_map);
+    if ((rc = run_read(c, p, q_dtype, stream)) != PCK_OK) return rc;
+    return attend_run(c, &x.cache, &x.batch, H_q, Q, q_row, q_head, window, sinks, O_prior, LSE_prior, O, LSE, ws + x.off_inner,
+                      workspace_bytes - x.off_inner, stream);
+}
+
+int pck_paged_read_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int dtype, const pck_rows* K,
+                        const pck_rows* V, void* stream) {
+    if (!c) return PCK_EINVAL;
+    int rc = check_cache(c, cache);
+    if (rc != PCK_OK) return rc;
+    if ((rc = check_batch(c, batch, cache->page_size)) != PCK_OK) return rc;
+    if (!dtype_any(dtype)) return ctx_fail(c, PCK_EINVAL, "dtype=%d", dtype);
+    if (batch->T == 0 || batch->B == 0) return PCK_OK;
+    if (!K || !V) return ctx_fail(c, PCK_EINVAL, "NULL K or V");
+    const int e = elems16(dtype);
+    for (const pck_rows* r : {K, V}) {
+        if (!r->out || !aligned16(r->out)) return ctx_fail(c, PCK_EINVAL, "K and V: outputs must be set and 16-byte aligned");
+        if (r->H != cache->H_kv) return ctx_fail(c, PCK_EINVAL, "%d heads, the cache has %d", r->H, cache->H_kv);
+        if (!stride_ok(r->out_row, batch->T, e) || !stride_ok(r->out_head, r->H, e))
+            return ctx_fail(c, PCK_EINVAL, "K and V: strides must be positive multiples of %d elements", e);
+    }
+    ReadParams p = {};
+    read_params(c, cache, batch, p);
+    p.max_rows = batch->T;
+    p.Ko = K->out;
+    p.Vo = V->out;
+    p.ko_row = K->out_row;
+    p.ko_head = K->out_head;
+    p.vo_row = V->out_row;
+    p.vo_head = V->out_head;
+    return run_read(c, p, dtype, stream);
 }
 
 }  // extern "C"
