@@ -88,6 +88,8 @@ struct PagedAttn {
     int cols;                        // columns of a work item: rows x heads
     int mode;                        // how the call is cut
     int n_ctas;
+    const uint8_t *k_scale, *v_scale;   // a quantised cache's scales [n_pages, H_kv, page]
+    int halves;                      // its pages are no multiples of a unit: loaded in halves of 16 tokens
     // row kernel
     int n_split, row_tiles, box;     // key splits, row tiles of the grid, tokens of a TMA box
     const void *k_base, *v_base;
@@ -95,6 +97,7 @@ struct PagedAttn {
 };
 
 bool paged_token_dim_ok(int D);
+int paged_token_cols(int D);                              // columns (rows x q heads of a kv head) that a work item can have
 bool paged_token_rows_ok(int G, int max_rows, int D);     // ragged rows few enough for the one-token kernel
 constexpr int paged_token_box_rows() { return PG_SUB; }   // tokens of a TMA tile load
 size_t paged_token_plan(PagedAttn& p, int D, int sms);    // how the call is cut; its workspace in bytes

@@ -268,6 +268,41 @@ int append_rows(pck_ctx* c, const Cache* cache, const pck_paged_batch* batch, in
     return PCK_OK;
 }
 
+// Pages of codes as {CHB codes, token, D / CHB, head, page} with a box of `rows` tokens and all of a row's D / CHB runs, swizzled
+// by their width: runs of 128 codes where D has them, of 64 otherwise.
+bool encode_codes(CUtensorMap* tm, void* base, int page_size, int D, int H, int64_t n_pages, int64_t s_tok, int64_t s_head,
+                  int64_t s_page, int rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const int run = D % 128 == 0 ? 128 : 64;
+    const int64_t st = page_size > 1 ? s_tok : D, sh = H > 1 ? s_head : D, sp = n_pages > 1 ? s_page : D;
+    const cuuint64_t dims[5] = {(cuuint64_t)run, (cuuint64_t)page_size, (cuuint64_t)(D / run), (cuuint64_t)H, (cuuint64_t)n_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)st, (cuuint64_t)run, (cuuint64_t)sh, (cuuint64_t)sp};
+    const cuuint32_t box[5] = {(cuuint32_t)run, (cuuint32_t)rows, (cuuint32_t)(D / run), 1, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              run == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The parts of an attention call that its kernels read beside its shape.
+void attend_args(PagedAttn& p, const CtxView& v, const pck_paged_batch* batch, int D, const void* Q, int64_t q_row, int64_t q_head,
+                 const float* O_prior, const float* LSE_prior, void* O, float* LSE, void* workspace) {
+    p.Q = Q;
+    p.O = O;
+    p.LSE = LSE;
+    p.O_prior = O_prior;
+    p.LSE_prior = LSE_prior;
+    p.q_row = q_row;
+    p.q_head = q_head;
+    p.kv_len = batch->kv_len;
+    p.table = batch->table;
+    p.scale_log2 = PG_LOG2E / sqrtf(static_cast<float>(D));
+    p.ws = static_cast<float*>(workspace);
+    p.err = v.dev_err;
+    p.device = v.device;
+}
+
 int check_attend_rows(pck_ctx* c, int T, int H_q, const void* Q, int64_t q_row, int64_t q_head, const float* O_prior,
                       const float* LSE_prior, const void* O, const void* workspace) {
     if (!Q || !O) return ctx_fail(c, PCK_EINVAL, "NULL Q or O");
@@ -292,19 +327,7 @@ int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* 
     const size_t need = attend_plan(p, D, v.sms);
     if (workspace_bytes < need || (need && !workspace))
         return ctx_fail(c, PCK_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    p.Q = Q;
-    p.O = O;
-    p.LSE = LSE;
-    p.O_prior = O_prior;
-    p.LSE_prior = LSE_prior;
-    p.q_row = q_row;
-    p.q_head = q_head;
-    p.kv_len = batch->kv_len;
-    p.table = batch->table;
-    p.scale_log2 = PG_LOG2E / sqrtf(static_cast<float>(D));
-    p.ws = static_cast<float*>(workspace);
-    p.err = v.dev_err;
-    p.device = v.device;
+    attend_args(p, v, batch, D, Q, q_row, q_head, O_prior, LSE_prior, O, LSE, workspace);
     p.k_base = cache->K;
     p.v_base = cache->V;
     const int64_t strides[6] = {cache->k_page, cache->k_head, cache->k_token, cache->v_page, cache->v_head, cache->v_token};
@@ -324,9 +347,11 @@ int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* 
     return PCK_OK;
 }
 
-// Attention over a quantised cache through 16-bit pages: what the rows see is read back into pages of the workspace (of Q's
+// Attention over a quantised cache. One row of a sequence, or a few: over the codes. More: through 16-bit pages: what the rows see is read back into pages of the workspace (of Q's
 // type, in the order of the sequences), and those are attended to.
 struct Expanded {
+    PagedAttn p;                     // over the codes: its shape
+    bool direct;
     pck_paged_cache cache;           // of the workspace; K and V are set by the call
     pck_paged_batch batch;           // its table is the workspace's page map
     int slots;                       // pages of a sequence
@@ -340,7 +365,19 @@ int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batc
     if ((rc = check_batch(c, b, k->page_size)) != PCK_OK) return rc;
     if (q_dtype != PCK_DT_F16 && q_dtype != PCK_DT_BF16) return ctx_fail(c, PCK_EINVAL, "q_dtype=%d is not fp16 or bf16", q_dtype);
     if (window < 0 || sinks < 0) return ctx_fail(c, PCK_EINVAL, "window=%d sinks=%d", window, sinks);
+    // the shape's checks are those of a 16-bit cache of this geometry (contiguous: its strides are not looked at)
     const int64_t page = k->page_size;
+    void* const some = reinterpret_cast<void*>(256);                     // stands for the workspace
+    x.cache = pck_paged_cache{some, some, q_dtype, k->H_kv, k->D, k->page_size, k->n_pages,
+                              k->H_kv * page * k->D, page * k->D, k->D, k->H_kv * page * k->D, page * k->D, k->D};
+    x.batch = *b;
+    if ((rc = attend_shape(c, &x.cache, b, H_q, window, sinks, x.p)) != PCK_OK) return rc;
+    if (x.p.B == 0 || x.p.T == 0) return PCK_OK;
+    x.direct = !tiled_rows(x.p, k->D);
+    if (x.direct) {
+        x.total = paged_token_e4m3_plan(x.p, k->D, ctx_view(c).sms);
+        return PCK_OK;
+    }
     int64_t slots = b->max_pages;
     if (window > 0) {
         const int64_t rows = b->cu_rows ? (b->max_rows < b->T ? b->max_rows : b->T) : 1;
@@ -350,18 +387,12 @@ int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batc
     const int64_t pages = b->B * slots;
     if (pages >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld pages", b->B, (long long)slots);
     x.slots = static_cast<int>(slots);
-    void* const some = reinterpret_cast<void*>(256);                     // stands for the workspace in the checks
-    x.cache = pck_paged_cache{some, some, q_dtype, k->H_kv, k->D, k->page_size, pages > 0 ? pages : 1,
-                              k->H_kv * page * k->D, page * k->D, k->D, k->H_kv * page * k->D, page * k->D, k->D};
-    x.batch = *b;
-    PagedAttn p = {};
-    if ((rc = attend_shape(c, &x.cache, b, H_q, window, sinks, p)) != PCK_OK) return rc;
-    if (p.B == 0 || p.T == 0) return PCK_OK;
+    x.cache.n_pages = pages;
     const size_t side = (size_t)pages * k->H_kv * page * k->D * 2;       // a multiple of 512 bytes
     x.off_v = side;
     x.off_map = 2 * side;
     x.off_inner = x.off_map + (((size_t)b->B * b->max_pages * 4 + 255) & ~size_t(255));
-    x.total = x.off_inner + attend_plan(p, k->D, ctx_view(c).sms);
+    x.total = x.off_inner + paged_rows_plan(x.p, k->D, ctx_view(c).sms);
     return PCK_OK;
 }
 
@@ -481,10 +512,27 @@ int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const p
     if (!c) return PCK_EINVAL;
     Expanded x;
     int rc = expand_shape(c, cache, batch, q_dtype, H_q, window, sinks, x);
-    if (rc != PCK_OK || x.total == 0) return rc;
+    if (rc != PCK_OK || x.p.B == 0 || x.p.T == 0) return rc;
     if ((rc = check_attend_rows(c, batch->T, H_q, Q, q_row, q_head, O_prior, LSE_prior, O, workspace)) != PCK_OK) return rc;
-    if (workspace_bytes < x.total || !workspace)
+    if (workspace_bytes < x.total || (x.total && !workspace))
         return ctx_fail(c, PCK_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, x.total);
+    if (x.direct) {
+        const CtxView v = ctx_view(c);
+        PagedAttn& p = x.p;
+        attend_args(p, v, batch, cache->D, Q, q_row, q_head, O_prior, LSE_prior, O, LSE, workspace);
+        p.k_scale = cache->K_scale;
+        p.v_scale = cache->V_scale;
+        DeviceScope dev(v.device);
+        if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
+        const int rows = paged_token_e4m3_box(cache->D, p.page);
+        if (!encode_codes(&p.tm_k, cache->K, p.page, cache->D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows) ||
+            !encode_codes(&p.tm_v, cache->V, p.page, cache->D, p.H_kv, cache->n_pages, cache->v_token, cache->v_head, cache->v_page, rows))
+            return ctx_fail(c, PCK_ECUDA, "the driver refused the cache's tensor map");
+        const cudaError_t e = launch_paged_token_e4m3(p, cache->D, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
+        ctx_count_query(c);
+        return PCK_OK;
+    }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     x.cache.K = ws;
     x.cache.V = ws + x.off_v;

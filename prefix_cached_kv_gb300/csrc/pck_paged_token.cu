@@ -5,15 +5,14 @@ namespace pck {
 
 bool paged_token_dim_ok(int D) { return D == 64 || D == 128 || D == 192 || D == 256; }
 
-// Columns (rows x q heads of a kv head) that a work item can have.
-static int token_cols(int D) { return D <= 128 ? 16 : 8; }
-bool paged_token_rows_ok(int G, int max_rows, int D) { return paged_token_dim_ok(D) && (int64_t)G * max_rows <= token_cols(D); }
+int paged_token_cols(int D) { return D <= 128 ? 16 : 8; }
+bool paged_token_rows_ok(int G, int max_rows, int D) { return paged_token_dim_ok(D) && (int64_t)G * max_rows <= paged_token_cols(D); }
 
 // How a call is cut; fills heads_per_group, n_groups, cols, mode and n_ctas, and returns the workspace
 // bytes. Up to 8 q heads (16 at D <= 128) share a work item and one read of the kv head; more are
 // split evenly into several items. A few rows of a sequence share it as well.
 size_t paged_token_plan(PagedAttn& p, int D, int sms) {
-    const int most = token_cols(D);
+    const int most = paged_token_cols(D);
     const int rows = p.cu_rows ? p.max_rows : 1;
     p.n_groups = (p.G * rows + most - 1) / most;       // 1 with more than one row
     p.heads_per_group = (p.G + p.n_groups - 1) / p.n_groups;

@@ -154,20 +154,21 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* tm, int 
         ::"r"(dst), "l"(tm), "r"(0), "r"(tok), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(pol) : "memory");
 }
 
-// The units (cache tiles of 16 tokens) that one sequence's rows read: tiles [0, ns) hold the sinks, then come tiles
+// The units (cache tiles of SUB tokens) that one sequence's rows read: tiles [0, ns) hold the sinks, then come tiles
 // [w0, w0 + n - ns). `rows` of len tokens: the first row sees len - rows + 1 keys. A sequence without keys (or rows)
 // has one unit with nothing visible.
 struct Span {
     int n, ns, w0;
 };
+template <int SUB = PG_SUB>
 __device__ __forceinline__ Span span_of(int len, int rows, int window, int sinks) {
     Span s;
-    const int end = rows > 0 ? (len + PG_SUB - 1) / PG_SUB : 0, first = len - rows + 1;
+    const int end = rows > 0 ? (len + SUB - 1) / SUB : 0, first = len - rows + 1;
     s.ns = 0;
     s.w0 = 0;
     if (window > 0 && rows > 0 && first > window) {
-        s.w0 = (first - window) / PG_SUB;
-        s.ns = min((min(sinks, len) + PG_SUB - 1) / PG_SUB, s.w0);
+        s.w0 = (first - window) / SUB;
+        s.ns = min((min(sinks, len) + SUB - 1) / SUB, s.w0);
     }
     s.n = max(1, s.ns + end - s.w0);
     return s;
@@ -250,6 +251,111 @@ struct JoinDesc {
     int r0, x, pieces, rows;
 };
 
+// The range of a worker (a warp of a TK_WARP call, else the CTA) among the units of all items laid end to end: [u0, u1). pre
+// gets the units before each sequence (of the CTA's one sequence when nothing is split). idle: more workers than ranges.
+struct Cut {
+    int64_t u0, u1, U;       // U: the items' whole weight
+    int workers, b_first;
+    bool idle;
+};
+template <int NW, int MODE, bool ROWS, int SUB>
+__device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int workers, int* s_scan, int* pre) {
+    constexpr int NT = NW * 32, TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
+    constexpr bool SPLIT = is_split(MODE), BY_WARP = MODE == TK_WARP;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hg = P.H_kv * P.n_groups, B = P.B;
+    Cut c;
+    c.U = 0;
+    c.b_first = 0;
+    c.workers = workers;
+    c.idle = false;
+    if (SPLIT) {
+        // units before each sequence (per kv head and group): a scan over the lengths
+        const int per = (B + NT - 1) / NT;
+        int sum = 0, top = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < B) {
+                const int n = span_of<SUB>(clamp_len(P, b, blockIdx.x == 0), rows_of<ROWS>(P, b, blockIdx.x == 0).n, P.window, P.sinks).n;
+                sum += n;
+                top = max(top, n);
+            }
+        }
+        if (!BY_WARP) top = __reduce_max_sync(0xffffffffu, top);
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) {
+            s_scan[warp] = inc;
+            s_scan[32 + warp] = top;
+        }
+        __syncthreads();
+        int base = 0;
+        for (int w = 0; w < warp; ++w) base += s_scan[w];
+        int run = base + inc - sum;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < B) {
+                pre[b] = run;
+                run += span_of<SUB>(clamp_len(P, b, false), rows_of<ROWS>(P, b, false).n, P.window, P.sinks).n;
+            }
+        }
+        if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
+        __syncthreads();
+        c.U = ((int64_t)pre[B] + (int64_t)TK_ITEM_UNITS * B) * Hg;      // the items' whole weight
+        const int64_t most = (c.U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
+        if (most < workers) workers = static_cast<int>(most);
+        c.workers = workers;
+        c.idle = worker >= workers;
+        if (c.idle) return c;
+        // the unit at which weight w falls; weights behind an item's units fall on its end
+        auto unit_at = [&](int64_t w) -> int64_t {
+            const int v = static_cast<int>(w / Hg);
+            int lo = 0, hi = B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] + TK_ITEM_UNITS * mid <= v) lo = mid;
+                else hi = mid - 1;
+            }
+            const int n = pre[lo + 1] - pre[lo], nw = n + TK_ITEM_UNITS;
+            const int64_t rem = w - ((int64_t)pre[lo] + (int64_t)TK_ITEM_UNITS * lo) * Hg;
+            const int64_t x = rem / nw;
+            return (int64_t)pre[lo] * Hg + x * n + min((int64_t)n, rem - x * nw);
+        };
+        // Items of nearly one length (the longest at most 6/5 of the mean) that fill the ranges, or the last round of
+        // them, to a half (three quarters where an SM has one) stay whole: nothing is left to join.
+        bool even = false;
+        const int64_t items = (int64_t)B * Hg;
+        if (!BY_WARP) {
+            for (int w = 0; w < NW; ++w) top = max(top, s_scan[32 + w]);
+            const int64_t left = items % workers;
+            even = (int64_t)5 * top * B <= (int64_t)6 * pre[B]
+                   && (items < workers ? items * 4 >= workers * (MODE == TK_CTA ? 3 : 2) : left == 0 || left * 2 >= workers);
+        }
+        auto unit_of = [&](int64_t item) -> int64_t {
+            const int b = static_cast<int>(item / Hg);
+            return b < B ? (int64_t)pre[b] * Hg + (item - (int64_t)b * Hg) * (pre[b + 1] - pre[b]) : (int64_t)pre[B] * Hg;
+        };
+        c.u0 = even ? unit_of(items * worker / workers) : unit_at(c.U * worker / workers);
+        c.u1 = even ? unit_of(items * (worker + 1) / workers)
+               : worker + 1 < workers ? unit_at(c.U * (worker + 1) / workers) : (int64_t)pre[B] * Hg;
+    } else {
+        c.b_first = blockIdx.x / Hg;
+        const int n = span_of<SUB>(clamp_len(P, c.b_first, true), rows_of<ROWS>(P, c.b_first, true).n, P.window, P.sinks).n;
+        if (tid == 0) {
+            pre[0] = 0;
+            pre[1] = n;
+        }
+        __syncthreads();
+        c.u0 = (int64_t)(blockIdx.x - c.b_first * Hg) * n;
+        c.u1 = c.u0 + n;
+    }
+    return c;
+}
+
 // ROWS: a sequence may have several rows (cu_rows); else it has one.
 template <typename T, int D, int NB, int MODE, bool ROWS>
 __global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_token_kernel(const __grid_constant__ PagedAttn P) {
@@ -281,98 +387,18 @@ __global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_to
     const int B = P.B;
     const int heads = P.heads_per_group, cols = P.cols;
     constexpr bool SPLIT = is_split(MODE), BY_WARP = MODE == TK_WARP;
-    constexpr int TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
+    constexpr int TK_ITEM_UNITS = tk_item_units(MODE);
     const int worker = BY_WARP ? warp * gridDim.x + blockIdx.x : blockIdx.x;    // few workers spread over the SMs
     int workers = BY_WARP ? gridDim.x * NW : gridDim.x;
     JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * workers * slot_floats(D, cols));
-    int64_t u0, u1;            // units of all items end to end
-    int64_t U = 0;
-    int b_first = 0;
-    if (SPLIT) {
-        // units before each sequence (per kv head and group): a scan over the lengths
-        const int per = (B + NT - 1) / NT;
-        int sum = 0, top = 0;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < B) {
-                const int n = span_of(clamp_len(P, b, blockIdx.x == 0), rows_of<ROWS>(P, b, blockIdx.x == 0).n, P.window, P.sinks).n;
-                sum += n;
-                top = max(top, n);
-            }
-        }
-        if (!BY_WARP) top = __reduce_max_sync(0xffffffffu, top);
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) {
-            s_scan[warp] = inc;
-            s_scan[32 + warp] = top;
-        }
-        __syncthreads();
-        int base = 0;
-        for (int w = 0; w < warp; ++w) base += s_scan[w];
-        int run = base + inc - sum;
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            if (b < B) {
-                pre[b] = run;
-                run += span_of(clamp_len(P, b, false), rows_of<ROWS>(P, b, false).n, P.window, P.sinks).n;
-            }
-        }
-        if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
-        __syncthreads();
-        U = ((int64_t)pre[B] + (int64_t)TK_ITEM_UNITS * B) * Hg;      // the items' whole weight
-        const int64_t most = (U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
-        if (most < workers) workers = static_cast<int>(most);
-        if (worker >= workers) {
-            if (BY_WARP ? lane == 0 : tid == 0) jd[worker].pieces = 0;
-            return;
-        }
-        // the unit at which weight w falls; weights behind an item's units fall on its end
-        auto unit_at = [&](int64_t w) -> int64_t {
-            const int v = static_cast<int>(w / Hg);
-            int lo = 0, hi = B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] + TK_ITEM_UNITS * mid <= v) lo = mid;
-                else hi = mid - 1;
-            }
-            const int n = pre[lo + 1] - pre[lo], nw = n + TK_ITEM_UNITS;
-            const int64_t rem = w - ((int64_t)pre[lo] + (int64_t)TK_ITEM_UNITS * lo) * Hg;
-            const int64_t x = rem / nw;
-            return (int64_t)pre[lo] * Hg + x * n + min((int64_t)n, rem - x * nw);
-        };
-        // Items of nearly one length (the longest at most 6/5 of the mean) that fill the ranges, or the last round of
-        // them, to a half (three quarters where an SM has one) stay whole: nothing is left to join.
-        bool even = false;
-        const int64_t items = (int64_t)B * Hg;
-        if (!BY_WARP) {
-            for (int w = 0; w < NW; ++w) top = max(top, s_scan[32 + w]);
-            const int64_t left = items % workers;
-            even = (int64_t)5 * top * B <= (int64_t)6 * pre[B]
-                   && (items < workers ? items * 4 >= workers * (MODE == TK_CTA ? 3 : 2) : left == 0 || left * 2 >= workers);
-        }
-        auto unit_of = [&](int64_t item) -> int64_t {
-            const int b = static_cast<int>(item / Hg);
-            return b < B ? (int64_t)pre[b] * Hg + (item - (int64_t)b * Hg) * (pre[b + 1] - pre[b]) : (int64_t)pre[B] * Hg;
-        };
-        u0 = even ? unit_of(items * worker / workers) : unit_at(U * worker / workers);
-        u1 = even ? unit_of(items * (worker + 1) / workers)
-             : worker + 1 < workers ? unit_at(U * (worker + 1) / workers) : (int64_t)pre[B] * Hg;
-    } else {
-        b_first = blockIdx.x / Hg;
-        const int n = span_of(clamp_len(P, b_first, true), rows_of<ROWS>(P, b_first, true).n, P.window, P.sinks).n;
-        if (tid == 0) {
-            pre[0] = 0;
-            pre[1] = n;
-        }
-        __syncthreads();
-        u0 = (int64_t)(blockIdx.x - b_first * Hg) * n;
-        u1 = u0 + n;
+    const Cut cut = cut_units<NW, MODE, ROWS, PG_SUB>(P, worker, workers, s_scan, pre);
+    if (SPLIT && cut.idle) {
+        if (BY_WARP ? lane == 0 : tid == 0) jd[worker].pieces = 0;
+        return;
     }
+    const int64_t u0 = cut.u0, u1 = cut.u1, U = cut.U;
+    workers = cut.workers;
+    const int b_first = cut.b_first;
     const int nseq = SPLIT ? B : 1;     // sequences in pre[]
 
     // ---- a warp's units: u0 + k of its own range, u0 + warp + k NW of its CTA's. Lane i resolves unit k0 + i: coordinates of its
