@@ -522,11 +522,15 @@ int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const p
         attend_args(p, v, batch, cache->D, Q, q_row, q_head, O_prior, LSE_prior, O, LSE, workspace);
         p.k_scale = cache->K_scale;
         p.v_scale = cache->V_scale;
+        p.k_base = cache->K;
+        p.v_base = cache->V;
+        const int64_t strides[6] = {cache->k_page, cache->k_head, cache->k_token, cache->v_page, cache->v_head, cache->v_token};
+        for (int i = 0; i < 6; ++i) p.kv_stride[i] = strides[i];
         DeviceScope dev(v.device);
         if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
-        const int rows = paged_token_e4m3_box(cache->D, p.page);
-        if (!encode_codes(&p.tm_k, cache->K, p.page, cache->D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows) ||
-            !encode_codes(&p.tm_v, cache->V, p.page, cache->D, p.H_kv, cache->n_pages, cache->v_token, cache->v_head, cache->v_page, rows))
+        const int rows = paged_token_e4m3_box(p, cache->D);     // (pages in pieces are not loaded by tiles)
+        if (!p.halves && (!encode_codes(&p.tm_k, cache->K, p.page, cache->D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows) ||
+            !encode_codes(&p.tm_v, cache->V, p.page, cache->D, p.H_kv, cache->n_pages, cache->v_token, cache->v_head, cache->v_page, rows)))
             return ctx_fail(c, PCK_ECUDA, "the driver refused the cache's tensor map");
         const cudaError_t e = launch_paged_token_e4m3(p, cache->D, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));

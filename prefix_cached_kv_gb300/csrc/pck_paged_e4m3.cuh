@@ -58,10 +58,11 @@ struct ReadParams {
 cudaError_t launch_paged_read(const ReadParams& p, int out_dtype, int sms, cudaStream_t st);
 
 // One-token attention over codes.
-bool paged_token_e4m3_halves(int D, int page);
-int paged_token_e4m3_box(int D, int page);                   // tokens of a TMA tile load
+int paged_token_e4m3_box(const PagedAttn& p, int D);         // tokens of a TMA tile load, of a planned call
 size_t paged_token_e4m3_plan(PagedAttn& p, int D, int sms);  // how the call is cut; its workspace in bytes
 cudaError_t launch_paged_token_e4m3(PagedAttn& p, int D, cudaStream_t st);
+cudaError_t launch_paged_token_e4m3_128(PagedAttn& p, cudaStream_t st);
+cudaError_t launch_paged_token_e4m3_wide(PagedAttn& p, int D, cudaStream_t st);
 
 cudaError_t launch_append_e4m3(const RopeParams& p, int in_dtype, int sms, cudaStream_t st);
 

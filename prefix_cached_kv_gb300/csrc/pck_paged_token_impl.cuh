@@ -251,6 +251,11 @@ struct JoinDesc {
     int r0, x, pieces, rows;
 };
 
+// a / b for a >= 0, b > 0: most quotients here need no 64-bit division, which takes some 100 instructions one after another.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int b) {
+    return (a >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // The range of a worker (a warp of a TK_WARP call, else the CTA) among the units of all items laid end to end: [u0, u1). pre
 // gets the units before each sequence (of the CTA's one sequence when nothing is split). idle: more workers than ranges.
 struct Cut {
@@ -258,9 +263,9 @@ struct Cut {
     int workers, b_first;
     bool idle;
 };
-template <int NW, int MODE, bool ROWS, int SUB>
+template <int NW, int MODE, bool ROWS, int SUB, int TK_ITEM_UNITS>
 __device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int workers, int* s_scan, int* pre) {
-    constexpr int NT = NW * 32, TK_ITEM_UNITS = tk_item_units(MODE), TK_MIN_UNITS = tk_min_units(MODE);
+    constexpr int NT = NW * 32, TK_MIN_UNITS = tk_min_units(MODE);
     constexpr bool SPLIT = is_split(MODE), BY_WARP = MODE == TK_WARP;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hg = P.H_kv * P.n_groups, B = P.B;
@@ -272,11 +277,11 @@ __device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int wor
     if (SPLIT) {
         // units before each sequence (per kv head and group): a scan over the lengths
         const int per = (B + NT - 1) / NT;
-        int sum = 0, top = 0;
+        int sum = 0, top = 0, n = 0;          // (one sequence a thread, most often: its n is not looked up again)
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
             if (b < B) {
-                const int n = span_of<SUB>(clamp_len(P, b, blockIdx.x == 0), rows_of<ROWS>(P, b, blockIdx.x == 0).n, P.window, P.sinks).n;
+                n = span_of<SUB>(clamp_len(P, b, blockIdx.x == 0), rows_of<ROWS>(P, b, blockIdx.x == 0).n, P.window, P.sinks).n;
                 sum += n;
                 top = max(top, n);
             }
@@ -300,20 +305,20 @@ __device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int wor
             const int b = tid * per + i;
             if (b < B) {
                 pre[b] = run;
-                run += span_of<SUB>(clamp_len(P, b, false), rows_of<ROWS>(P, b, false).n, P.window, P.sinks).n;
+                run += per == 1 ? n : span_of<SUB>(clamp_len(P, b, false), rows_of<ROWS>(P, b, false).n, P.window, P.sinks).n;
             }
         }
         if (tid == NT - 1) pre[B] = run;      // the last thread's sum is the total (later b's are empty)
         __syncthreads();
         c.U = ((int64_t)pre[B] + (int64_t)TK_ITEM_UNITS * B) * Hg;      // the items' whole weight
-        const int64_t most = (c.U + TK_MIN_UNITS - 1) / TK_MIN_UNITS;
+        const int64_t most = div_pos(c.U + TK_MIN_UNITS - 1, TK_MIN_UNITS);
         if (most < workers) workers = static_cast<int>(most);
         c.workers = workers;
         c.idle = worker >= workers;
         if (c.idle) return c;
         // the unit at which weight w falls; weights behind an item's units fall on its end
         auto unit_at = [&](int64_t w) -> int64_t {
-            const int v = static_cast<int>(w / Hg);
+            const int v = static_cast<int>(div_pos(w, Hg));
             int lo = 0, hi = B - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -322,7 +327,7 @@ __device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int wor
             }
             const int n = pre[lo + 1] - pre[lo], nw = n + TK_ITEM_UNITS;
             const int64_t rem = w - ((int64_t)pre[lo] + (int64_t)TK_ITEM_UNITS * lo) * Hg;
-            const int64_t x = rem / nw;
+            const int64_t x = div_pos(rem, nw);
             return (int64_t)pre[lo] * Hg + x * n + min((int64_t)n, rem - x * nw);
         };
         // Items of nearly one length (the longest at most 6/5 of the mean) that fill the ranges, or the last round of
@@ -331,17 +336,20 @@ __device__ __forceinline__ Cut cut_units(const PagedAttn& P, int worker, int wor
         const int64_t items = (int64_t)B * Hg;
         if (!BY_WARP) {
             for (int w = 0; w < NW; ++w) top = max(top, s_scan[32 + w]);
-            const int64_t left = items % workers;
+            const int64_t left = items - div_pos(items, workers) * workers;
             even = (int64_t)5 * top * B <= (int64_t)6 * pre[B]
                    && (items < workers ? items * 4 >= workers * (MODE == TK_CTA ? 3 : 2) : left == 0 || left * 2 >= workers);
         }
         auto unit_of = [&](int64_t item) -> int64_t {
-            const int b = static_cast<int>(item / Hg);
+            const int b = static_cast<int>(div_pos(item, Hg));
             return b < B ? (int64_t)pre[b] * Hg + (item - (int64_t)b * Hg) * (pre[b + 1] - pre[b]) : (int64_t)pre[B] * Hg;
         };
-        c.u0 = even ? unit_of(items * worker / workers) : unit_at(c.U * worker / workers);
-        c.u1 = even ? unit_of(items * (worker + 1) / workers)
-               : worker + 1 < workers ? unit_at(c.U * (worker + 1) / workers) : (int64_t)pre[B] * Hg;
+        // both ends at once: even lanes the first, odd lanes the last
+        const int at = worker + (lane & 1);
+        const int64_t end = even ? unit_of(div_pos(items * at, workers))
+                            : at < workers ? unit_at(div_pos(c.U * at, workers)) : (int64_t)pre[B] * Hg;
+        c.u0 = __shfl_sync(0xffffffffu, end, 0);
+        c.u1 = __shfl_sync(0xffffffffu, end, 1);
     } else {
         c.b_first = blockIdx.x / Hg;
         const int n = span_of<SUB>(clamp_len(P, c.b_first, true), rows_of<ROWS>(P, c.b_first, true).n, P.window, P.sinks).n;
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(TCfg<D, MODE>::NW * 32, per_sm(MODE)) paged_to
     const int worker = BY_WARP ? warp * gridDim.x + blockIdx.x : blockIdx.x;    // few workers spread over the SMs
     int workers = BY_WARP ? gridDim.x * NW : gridDim.x;
     JoinDesc* jd = reinterpret_cast<JoinDesc*>(P.ws + (size_t)2 * workers * slot_floats(D, cols));
-    const Cut cut = cut_units<NW, MODE, ROWS, PG_SUB>(P, worker, workers, s_scan, pre);
+    const Cut cut = cut_units<NW, MODE, ROWS, PG_SUB, tk_item_units(MODE)>(P, worker, workers, s_scan, pre);
     if (SPLIT && cut.idle) {
         if (BY_WARP ? lane == 0 : tid == 0) jd[worker].pieces = 0;
         return;
