@@ -2,7 +2,8 @@
 //
 // Reading back: out = code * 2^e, rounded once to the output's type (fp32 and bf16 hold it exactly; in fp16 what is beyond
 // 65,504 becomes 65,504). D + 1 bytes in and 2 D or 4 D out per row, so HBM bounds it. A warp takes tiles of 16 tokens of one kv
-// head, K and V: D/16 lanes a row, 16 codes a lane, RD_DEPTH rows of loads in flight per lane before the first is used.
+// head, K and V: 8 codes a lane, so that its 16-byte stores lie side by side, with DEPTH loads of K and of V in flight before the
+// first is used.
 // The tiles of all sequences laid end to end are dealt to the warps from the lengths on the device (one block scan), so
 // one long session and many short ones fill the GPU alike.
 #include "pck_paged_rope_impl.cuh"
@@ -11,49 +12,18 @@ namespace pck {
 namespace {
 
 constexpr int RD_THREADS = 256;
-constexpr int RD_BLOCKS = 3;         // blocks per SM
-constexpr int RD_DEPTH = 4;          // chunks of 16 codes of K, and of V, that a lane has in flight
+// Pieces of 8 codes of K, and of V, that a lane has in flight (DEPTH), and blocks per SM.
+constexpr int R4 = 4, R8 = 2;
+__host__ __device__ constexpr int rd_blocks(int depth) { return depth == 4 ? R4 : R8; }
 
+// 8 codes times 2^e, stored as 8 values.
+__device__ __forceinline__ float held(float x) { return x > 65504.f ? 65504.f : x < -65504.f ? -65504.f : x; }   // (NaN stays)
 template <typename TO>
-struct Out16;   // 16 values stored
-template <>
-struct Out16<float> {
-    static __device__ __forceinline__ void store(float* p, const float (&x)[16]) {
+__device__ __forceinline__ void put8(TO* p, const uint2& c, float s) {
+    const uint32_t w[2] = {c.x, c.y};
+    float x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    }
-};
-template <>
-struct Out16<__half> {
-    static __device__ __forceinline__ float held(float x) { return x > 65504.f ? 65504.f : x < -65504.f ? -65504.f : x; }   // (NaN stays)
-    static __device__ __forceinline__ void store(__half* p, const float (&x)[16]) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = h2_as_u32(__floats2half2_rn(held(x[2 * i]), held(x[2 * i + 1])));
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-};
-template <>
-struct Out16<__nv_bfloat16> {
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[16]) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-};
-
-template <typename TO>
-__device__ __forceinline__ void put16(TO* p, const uint4& c, float s) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         uint32_t a, b;
         half_codes(w[i], a, b);
         const float2 f = __half22float2(u32_as_h2(a)), g = __half22float2(u32_as_h2(b));
@@ -62,7 +32,11 @@ __device__ __forceinline__ void put16(TO* p, const uint4& c, float s) {
         x[4 * i + 2] = g.x * s;
         x[4 * i + 3] = g.y * s;
     }
-    Out16<TO>::store(p, x);
+    if constexpr (std::is_same<TO, __half>::value) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = held(x[i]);
+    }
+    Vec8<TO>::store(p, x);
 }
 
 // What a call reads of a sequence: tokens [lo, len) and, where a window hides what lies between, [0, sinks); in tiles of 16
@@ -104,8 +78,8 @@ __device__ __forceinline__ ReadSpan read_span(const ReadParams& P, int b, bool r
     return s;
 }
 
-template <typename TO>
-__global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) paged_read_kernel(const __grid_constant__ ReadParams P) {
+template <typename TO, int DEPTH>
+__global__ void __launch_bounds__(RD_THREADS, rd_blocks(DEPTH)) paged_read_kernel(const __grid_constant__ ReadParams P) {
     extern __shared__ int pre[];         // tiles before each sequence [B + 1]
     __shared__ int s_scan[RD_THREADS / 32];
     pdl_wait();
@@ -138,11 +112,16 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) paged_read_kernel(const
         if (tid == RD_THREADS - 1) pre[P.B] = run;
         __syncthreads();
     }
-    const int64_t total = (int64_t)pre[P.B] * P.H;
-    const int lpr = P.D / 16, chunks = 16 * lpr;      // lanes of a row, 16-code chunks of a tile
-    for (int64_t it = (int64_t)blockIdx.x * (RD_THREADS / 32) + warp; it < total; it += (int64_t)gridDim.x * (RD_THREADS / 32)) {
-        const int v = static_cast<int>(it / P.H);
-        const int h = static_cast<int>(it - (int64_t)v * P.H);
+    const int64_t total = (int64_t)pre[P.B] * P.H, stride = (int64_t)gridDim.x * (RD_THREADS / 32);
+    const int lpr = P.D / 8, pieces = 16 * lpr;       // pieces of 8 codes of a row, and of a tile
+    const int t_lane = lane / lpr, c_lane = lane - t_lane * lpr, t_step = 32 / lpr, c_step = 32 - t_step * lpr;
+    // Lane i looks up the warp's next tile but i at once: its head, tokens, page and place in the output.
+    int head = 0, first = 0, page = 0, lo = 0, len = 0, sinks = 0, out = -1;      // out -1: nothing to do
+    const auto look_up = [&](int64_t it) {
+        out = -1;
+        if (it >= total) return;
+        const int v = (total >> 32) == 0 ? static_cast<uint32_t>(it) / static_cast<uint32_t>(P.H) : static_cast<int>(it / P.H);
+        head = static_cast<int>(it - (int64_t)v * P.H);
         int b = 0, hi = P.B - 1;
         while (b < hi) {
             const int mid = (b + hi + 1) >> 1;
@@ -151,33 +130,51 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) paged_read_kernel(const
         }
         const ReadSpan s = read_span(P, b, false);
         const int j = v - pre[b];
-        if (j < 0 || j >= s.n) continue;                    // (only where cu_rows made no sense)
-        const int tok = (j < s.ns ? j : j - s.ns + s.w0) * 16;
-        const auto taken = [&](int p) { return p < s.len && (p >= s.lo || static_cast<uint32_t>(p) < static_cast<uint32_t>(s.sinks)); };
-        // the tile's page; a tile in front of the cache (padded rows) has none
-        int64_t pg = 0;
-        int pi = 0;
-        if (tok >= 0) {
-            pi = tok / P.page;
-            pg = P.table[(int64_t)b * P.max_pages + pi];
-            if (pg < 0 || pg >= P.n_pages) {
-                if (lane == 0) set_err(P.err, ERR_PAGE_ID);
-                pg = 0;                                     // read instead: the call's results are invalid
+        if (j < 0 || j >= s.n) return;                      // (only where cu_rows made no sense)
+        first = (j < s.ns ? j : j - s.ns + s.w0) * 16;
+        lo = s.lo;
+        len = s.len;
+        sinks = s.sinks;
+        // a tile in front of the cache (padded rows) has no page
+        page = 0;
+        const int pi = first >= 0 ? first / P.page : 0;
+        if (first >= 0) {
+            page = P.table[(int64_t)b * P.max_pages + pi];
+            if (page < 0 || page >= P.n_pages) {
+                set_err(P.err, ERR_PAGE_ID);
+                page = 0;                                   // read instead: the call's results are invalid
             }
         }
-        const int slot = tok - pi * P.page;
-        TO *ko = static_cast<TO*>(P.Ko), *vo = static_cast<TO*>(P.Vo);
         if (P.pages) {
             const int sp = (s.sinks + P.page - 1) / P.page, wp = s.lo / P.page;
             const int os = wp > sp && pi >= wp ? pi - wp + sp : pi;
-            if (os >= P.slots) continue;                    // (only where kv_len or cu_rows made no sense)
-            const int64_t out_page = (int64_t)b * P.slots + os;
-            if (lane == 0 && h == 0) P.page_map[(int64_t)b * P.max_pages + pi] = static_cast<int32_t>(out_page);
-            const int64_t off = ((out_page * P.H + h) * P.page + slot) * P.D;
+            if (os >= P.slots) return;                      // (only where kv_len or cu_rows made no sense)
+            out = b * P.slots + os;
+            if (head == 0) P.page_map[(int64_t)b * P.max_pages + pi] = out;
+        } else {
+            out = s.r0;
+        }
+    };
+    int left = 0;                        // tiles that lanes have looked up
+    for (int64_t it = (int64_t)blockIdx.x * (RD_THREADS / 32) + warp; it < total; it += stride) {
+        if (left == 0) {
+            look_up(it + lane * stride);
+            left = 32;
+        }
+        const int from = 32 - left--;
+        const int o = __shfl_sync(0xffffffffu, out, from), h = __shfl_sync(0xffffffffu, head, from), tok = __shfl_sync(0xffffffffu, first, from);
+        const int64_t pg = __shfl_sync(0xffffffffu, page, from);
+        const int t_lo = __shfl_sync(0xffffffffu, lo, from), t_len = __shfl_sync(0xffffffffu, len, from), t_sinks = __shfl_sync(0xffffffffu, sinks, from);
+        if (o < 0) continue;
+        const auto taken = [&](int p) { return p < t_len && (p >= t_lo || static_cast<uint32_t>(p) < static_cast<uint32_t>(t_sinks)); };
+        const int slot = tok >= 0 ? tok % P.page : 0;
+        TO *ko = static_cast<TO*>(P.Ko), *vo = static_cast<TO*>(P.Vo);
+        if (P.pages) {
+            const int64_t off = (((int64_t)o * P.H + h) * P.page + slot) * P.D;
             ko += off;
             vo += off;
         } else {
-            const int64_t row = s.r0 + ((int64_t)tok - s.lo);
+            const int64_t row = o + ((int64_t)tok - t_lo);
             ko += row * P.ko_row + h * P.ko_head;
             vo += row * P.vo_row + h * P.vo_head;
         }
@@ -185,46 +182,62 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) paged_read_kernel(const
         const uint8_t* kc = P.K + pg * P.k_page + h * P.k_head + slot * P.k_token;
         const uint8_t* vc = P.V + pg * P.v_page + h * P.v_head + slot * P.v_token;
         const int64_t sc = (pg * P.H + h) * P.page + slot;
-        for (int c0 = 0; c0 < chunks; c0 += 32 * RD_DEPTH) {
-            uint4 k[RD_DEPTH], x[RD_DEPTH];
-            float sk[RD_DEPTH], sv[RD_DEPTH];
-#pragma unroll
-            for (int i = 0; i < RD_DEPTH; ++i) {
-                const int c = c0 + 32 * i + lane, t = c / lpr, d = (c - t * lpr) * 16, p = tok + t;
-                k[i] = x[i] = make_uint4(0, 0, 0, 0);
-                sk[i] = sv[i] = 0.f;
-                if (c < chunks && p >= 0 && taken(p)) {
-                    k[i] = __ldcs(reinterpret_cast<const uint4*>(kc + t * P.k_token + d));
-                    x[i] = __ldcs(reinterpret_cast<const uint4*>(vc + t * P.v_token + d));
-                    sk[i] = scale_up(P.k_scale[sc + t]);
-                    sv[i] = scale_up(P.v_scale[sc + t]);
+        const uint32_t scale = tok >= 0 ? (lane < 16 ? P.k_scale : P.v_scale)[sc + (lane & 15)] : 0;    // of token lane % 16
+        int t0 = t_lane, c0 = c_lane;                       // token and piece of the lane's first load of a round
+        for (int n0 = 0; n0 < pieces; n0 += 32 * DEPTH) {
+            uint2 k[DEPTH], x[DEPTH];
+            int t = t0, c = c0;
+            const auto step = [&]() {
+                t += t_step;
+                c += c_step;
+                if (c >= lpr) {
+                    c -= lpr;
+                    ++t;
                 }
-            }
+            };
 #pragma unroll
-            for (int i = 0; i < RD_DEPTH; ++i) {
-                const int c = c0 + 32 * i + lane, t = c / lpr, d = (c - t * lpr) * 16, p = tok + t;
-                if (c < chunks && taken(p)) {               // (rows in front of the cache too, as zeros)
-                    put16(ko + t * ors + d, k[i], sk[i]);
-                    put16(vo + t * vrs + d, x[i], sv[i]);
+            for (int i = 0; i < DEPTH; ++i) {
+                k[i] = x[i] = make_uint2(0, 0);
+                if (t < 16 && tok >= 0 && taken(tok + t)) {
+                    k[i] = __ldcs(reinterpret_cast<const uint2*>(kc + t * P.k_token + 8 * c));
+                    x[i] = __ldcs(reinterpret_cast<const uint2*>(vc + t * P.v_token + 8 * c));
                 }
+                step();
             }
+            t = t0;
+            c = c0;
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) {
+                const float sk = scale_up(__shfl_sync(0xffffffffu, scale, t & 15)), sv = scale_up(__shfl_sync(0xffffffffu, scale, 16 + (t & 15)));
+                if (t < 16 && taken(tok + t)) {             // (rows in front of the cache too, as zeros)
+                    put8(ko + t * ors + 8 * c, k[i], sk);
+                    put8(vo + t * vrs + 8 * c, x[i], sv);
+                }
+                step();
+            }
+            t0 = t;
+            c0 = c;
         }
     }
 }
 
-template <typename TO>
-cudaError_t launch_read_t(const ReadParams& p, int sms, cudaStream_t st) {
+template <typename TO, int DEPTH>
+cudaError_t launch_read_d(const ReadParams& p, int sms, cudaStream_t st) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms * RD_BLOCKS);
+    cfg.gridDim = dim3(sms * rd_blocks(DEPTH));
     cfg.blockDim = dim3(RD_THREADS);
     cfg.dynamicSmemBytes = 4 * (p.B + 1);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_read_kernel<TO>, p);
+    return cudaLaunchKernelEx(&cfg, paged_read_kernel<TO, DEPTH>, p);
+}
+template <typename TO>
+cudaError_t launch_read_t(const ReadParams& p, int sms, cudaStream_t st) {
+    return p.D <= 64 ? launch_read_d<TO, 4>(p, sms, st) : launch_read_d<TO, 8>(p, sms, st);
 }
 
 }  // namespace
