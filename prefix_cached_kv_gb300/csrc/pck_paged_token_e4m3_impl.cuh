@@ -108,6 +108,20 @@ __device__ __forceinline__ uint32_t pack_out(int dtype, float a, float b) {
     return dtype == PCK_DT_F16 ? Elem<__half>::pack(a, b) : Elem<__nv_bfloat16>::pack(a, b);
 }
 
+// Elements d, d + 1 of a row of O (token x H_q + head), and (first) its LSE.
+__device__ __forceinline__ void finish8(const PagedAttn& P, int64_t row, int D, int d, float a0, float a1, float m, float l, bool first) {
+    const RowEnd r = row_end(P, row, m, l);
+    a0 *= r.wo;
+    a1 *= r.wo;
+    if (r.prior) {
+        const float2 op = *reinterpret_cast<const float2*>(P.O_prior + row * D + d);
+        a0 = fmaf(op.x, r.wp, a0);
+        a1 = fmaf(op.y, r.wp, a1);
+    }
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(P.O) + (row * D + d) * 2) = pack_out(P.dtype, a0, a1);
+    if (first && P.LSE) P.LSE[row] = r.lse;
+}
+
 // NBQ: column blocks of 8, or 0: at most 4 columns, whose weights' lo parts take the other 4 of one block.
 template <int D, int NBQ, int MODE, bool ROWS>
 __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE)) paged_token8_kernel(const __grid_constant__ PagedAttn P) {
@@ -363,25 +377,27 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
                 sk[r] = quick_scale(scale[8 * r]);
                 sv[r] = quick_scale(scale[C::SCB + 8 * r]);
             }
+            // V rows hidden from every column may hold anything (also NaN, which 0 * v would keep): the permutation that pairs tokens
+            // 8 r + 2 lc and + 1 takes zeros for them. (Zeroing them in shared memory, with the fence that the next tile load
+            // then needs, took 2.7 us a unit, and every item ends in such a unit.)
+            uint32_t pick[2 * NS];
             bool spoilt = false;
+            const auto hidden = [&](int t) { return key0 + t >= len || (key0 + t < lo0 && key0 + t >= P.sinks); };
+#pragma unroll
+            for (int r = 0; r < 2 * NS; ++r) pick[r] = 0x3120;
             if (!full) {
-                // V rows hidden from every column may hold anything (also NaN, which 0 * v would keep): zero them
-                for (int t = 0; t < SUB; ++t)
-                    if (key0 + t >= len || (key0 + t < lo0 && key0 + t >= P.sinks))
-                        for (int c = lane; c < KS; c += 32)
-                            *reinterpret_cast<uint4*>(smem + (vs - s_base) + piece_at<SUB, C::CHB>(t, c)) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
                 bool bad = false;
 #pragma unroll
                 for (int r = 0; r < 2 * NS; ++r) {
-                    const int key = key0 + 8 * r + lg;
-                    if (key >= len || (key < lo0 && key >= P.sinks)) sv[r] = 0.f;
+                    if (hidden(8 * r + 2 * lc)) pick[r] = 0x3424;
+                    if (hidden(8 * r + 2 * lc + 1)) pick[r] = pick[r] & 0x0f0f | 0x4040;
+                    if (hidden(8 * r + lg)) sv[r] = 0.f;
                     bad |= sv[r] != sv[r];
                 }
                 // one that some rows see and others do not, and that is NaN (a code, or its scale), must not reach those others
                 if (ROWS && rs.n > 1) {
-                    for (int c = lane; c < SUB * KS; c += 32) bad |= nan_codes(*reinterpret_cast<const uint4*>(smem + (vs - s_base) + c * 16));
+                    for (int c = lane; c < SUB * KS; c += 32)
+                        if (!hidden(c / (C::CHB / 16) % SUB)) bad |= nan_codes(*reinterpret_cast<const uint4*>(smem + (vs - s_base) + c * 16));
                     spoilt = __any_sync(0xffffffffu, bad);
                 }
             }
@@ -543,8 +559,8 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
                         uint32_t af[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            half_codes(__byte_perm(w[2 * h], 0, 0x3120), af[h][0], af[h][1]);
-                            half_codes(__byte_perm(w[2 * h + 1], 0, 0x3120), af[h][2], af[h][3]);
+                            half_codes(__byte_perm(w[2 * h], 0, pick[2 * sb]), af[h][0], af[h][1]);
+                            half_codes(__byte_perm(w[2 * h + 1], 0, pick[2 * sb + 1]), af[h][2], af[h][3]);
                         }
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
@@ -617,7 +633,8 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
                     }
                 }
         } else {
-            // the CTA's warps join: maxima and sums first, then O in JP parts of D per column block
+            // the CTA's warps join: maxima and sums first, then O in JP parts of D per column block (one copy of the code that sums:
+            // a call on a short cache runs it once, and spends its time fetching it)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -627,57 +644,58 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
                         s_l[warp * 16 + nb * 8 + 2 * lane + i] = l[nb][i];
                     }
             __syncthreads();
+            constexpr int DP = D / C::JP, KP = KS / C::JP;
+            constexpr int COPIES = NB == 1 ? 1 : NB * C::JP;         // (rolled up, two column blocks of O would go through memory)
+#pragma unroll COPIES
+            for (int part_i = 0; part_i < NB * C::JP; ++part_i) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float al[2];
+                for (int nb = 0; nb < NB; ++nb) {
+                    if (part_i / C::JP != nb || (QUAD && lc >= 2)) continue;
+                    float al[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float M = -INFINITY;
+                    for (int i = 0; i < 2; ++i) {
+                        float M = M_NONE;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * lc + i]);
-                    al[i] = join_weight(m[nb][i], M);
-                }
-                constexpr int DP = D / C::JP, KP = KS / C::JP;
-#pragma unroll
-                for (int hf = 0; hf < C::JP; ++hf) {
+                        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + nb * 8 + 2 * lc + i]);
+                        al[i] = ex2_approx(m[nb][i] - M);
+                    }
                     float* row = jbuf + (warp * C::JC + 2 * lc) * C::JROW + 2 * lg;
 #pragma unroll
-                    for (int s = 0; s < KP; ++s) {
-                        if (QUAD && lc >= 2) break;
-                        const float (&v)[4] = o[nb][hf * KP + s];
-                        *reinterpret_cast<float2*>(row + 16 * s) = make_float2(v[0] * al[0], v[2] * al[0]);
-                        *reinterpret_cast<float2*>(row + C::JROW + 16 * s) = make_float2(v[1] * al[1], v[3] * al[1]);
+                    for (int s = 0; s < KS; ++s) {
+                        if (part_i % C::JP != s / KP) continue;
+                        const float (&v)[4] = o[nb][s];
+                        *reinterpret_cast<float2*>(row + 16 * (s % KP)) = make_float2(v[0] * al[0], v[2] * al[0]);
+                        *reinterpret_cast<float2*>(row + C::JROW + 16 * (s % KP)) = make_float2(v[1] * al[1], v[3] * al[1]);
                     }
-                    __syncthreads();
-                    for (int i = tid; i < C::JC * (DP / 2); i += NT) {   // (column, pair of elements)
-                        const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
-                        const int lh = nb * 8 + h;
-                        if (lh < nq) {
-                            float M = -INFINITY, L = 0.f;
+                }
+                __syncthreads();
+#pragma unroll 1
+                for (int i = tid; i < C::JC * (DP / 2); i += NT) {   // (column, pair of elements)
+                    const int h = i / (DP / 2), d = 2 * (i - h * (DP / 2));
+                    const int lh = part_i / C::JP * 8 + h;
+                    if (lh < nq) {
+                        float M = M_NONE, L = 0.f;
 #pragma unroll
-                            for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
-                            float a0 = 0.f, a1 = 0.f;
+                        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w * 16 + lh]);
+                        float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-                            for (int w = 0; w < NW; ++w) {
-                                const float mw = s_m[w * 16 + lh];
-                                L += s_l[w * 16 + lh] * join_weight(mw, M);
-                                const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * C::JC + h) * C::JROW + d);
-                                a0 += f.x;
-                                a1 += f.y;
-                            }
-                            const int dd = hf * DP + d;
-                            if (!SPLIT || whole) {
-                                if (P.dtype == PCK_DT_F16) finish2<__half>(P, row_of(lh), D, dd, a0, a1, M, L, dd == 0);
-                                else finish2<__nv_bfloat16>(P, row_of(lh), D, dd, a0, a1, M, L, dd == 0);
-                            } else {
-                                float* pr = part + lh * (D + 4);
-                                *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
-                                if (dd == 0) *reinterpret_cast<float2*>(pr) = make_float2(M, L);
-                            }
+                        for (int w = 0; w < NW; ++w) {
+                            L += s_l[w * 16 + lh] * ex2_approx(s_m[w * 16 + lh] - M);
+                            const float2 f = *reinterpret_cast<const float2*>(jbuf + (w * C::JC + h) * C::JROW + d);
+                            a0 += f.x;
+                            a1 += f.y;
+                        }
+                        const int dd = part_i % C::JP * DP + d;
+                        if (!SPLIT || whole) {
+                            finish8(P, row_of(lh), D, dd, a0, a1, M, L, dd == 0);
+                        } else {
+                            float* pr = part + lh * (D + 4);
+                            *reinterpret_cast<float2*>(pr + 4 + dd) = make_float2(a0, a1);
+                            if (dd == 0) *reinterpret_cast<float2*>(pr) = make_float2(M, L);
                         }
                     }
-                    __syncthreads();
                 }
+                __syncthreads();
             }
         }
         u = pe;
@@ -687,6 +705,66 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
         set_err(P.err, ERR_PAGED_TOKEN);
         for (k = k_failed; k < kp; ++k)   // copies still in flight, waited for with the same limit
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar + 8 * (k % ST), (k / ST) & 1))) break;
+    }
+}
+
+// Joins the partials of split items: a warp per (range in which one begins, column). Most ranges of a ragged batch begin
+// none or one of two or three pieces, so a CTA for each (the 16-bit kernel's way) is mostly CTAs that look and leave: 64 ragged sequences in
+// 2,432 ranges of 4 columns took 12 us from the last range's end to the next call.
+template <int D>
+__global__ void __launch_bounds__(256) paged_token8_join_kernel(const __grid_constant__ PagedAttn P, int ranges) {
+    constexpr int V = D >= 128 ? 4 : 2, NV = (D + 32 * V - 1) / (32 * V);   // floats of a lane's load, and loads of a row
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x & 31, cols = P.cols, heads = P.heads_per_group;
+    const int id = blockIdx.x * 8 + (threadIdx.x >> 5), c = id / cols, h = id - c * cols;
+    if (c >= ranges) return;
+    const JoinDesc d = reinterpret_cast<const JoinDesc*>(P.ws + (size_t)2 * ranges * slot_floats(D, cols))[c];
+    if (d.pieces == 0) return;
+    const int g = d.x / P.n_groups, grp = d.x - g * P.n_groups;
+    const int nh = min(heads, P.G - grp * heads);
+    if (h >= nh * d.rows) return;
+    const int64_t row = (int64_t)(d.r0 + h / nh) * P.H_q + g * P.G + grp * heads + h % nh;
+    // piece i: slot 2 c + 1 for the first, 2 (c + i) for the others
+    auto part = [&](int i) { return P.ws + (size_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_floats(D, cols) + h * (D + 4); };
+    float M = M_NONE;
+    for (int i = lane; i < d.pieces; i += 32) M = fmaxf(M, part(i)[0]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int i = lane; i < d.pieces; i += 32) {
+        const float2 ml = *reinterpret_cast<const float2*>(part(i));
+        L += ml.y * ex2_approx(ml.x - M);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float acc[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < d.pieces; ++i) {
+        const float* p = part(i);
+        const float w = ex2_approx(p[0] - M);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int at = (j * 32 + lane) * V;
+            if (D % (32 * V) && at >= D) continue;
+#pragma unroll
+            for (int q = 0; q < V; q += 2) {
+                const float2 v = *reinterpret_cast<const float2*>(p + 4 + at + q);
+                acc[j][q] = fmaf(w, v.x, acc[j][q]);
+                acc[j][q + 1] = fmaf(w, v.y, acc[j][q + 1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int at = (j * 32 + lane) * V;
+        if (D % (32 * V) && at >= D) continue;
+#pragma unroll
+        for (int q = 0; q < V; q += 2) finish8(P, row, D, at + q, acc[j][q], acc[j][q + 1], M, L, at + q == 0);
     }
 }
 
@@ -709,9 +787,15 @@ cudaError_t launch8_t(PagedAttn& p, cudaStream_t st) {
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_token8_kernel<D, NBQ, MODE, ROWS>, p);
     if (e != cudaSuccess || !SPLIT) return e;
-    cfg.gridDim = dim3(p.n_ctas, p.cols, MODE == TK_WARP ? C::NW : 1);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
+    if (MODE != TK_CTA) {
+        const int ranges = p.n_ctas * (MODE == TK_WARP ? C::NW : 1);
+        cfg.gridDim = dim3((ranges * p.cols + 7) / 8);
+        return cudaLaunchKernelEx(&cfg, paged_token8_join_kernel<D>, p, ranges);
+    }
+    // few items, each in many pieces: a CTA per (range, column), its threads over the pieces
+    cfg.gridDim = dim3(p.n_ctas, p.cols, 1);
     return p.dtype == PCK_DT_F16 ? cudaLaunchKernelEx(&cfg, paged_token_join_kernel<__half, D>, p)
                                  : cudaLaunchKernelEx(&cfg, paged_token_join_kernel<__nv_bfloat16, D>, p);
 }
