@@ -348,13 +348,14 @@ int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* 
 }
 
 // Attention over a quantised cache. One row of a sequence, or a few: over the codes. More: through 16-bit pages: what the rows see is read back into pages of the workspace (of Q's
-// type, in the order of the sequences), and those are attended to.
+// type, in the order of the sequences or, where the tables are wide, at their own numbers), and those are attended to.
 struct Expanded {
     PagedAttn p;                     // over the codes: its shape
     bool direct;
     pck_paged_cache cache;           // of the workspace; K and V are set by the call
     pck_paged_batch batch;           // its table is the workspace's page map
     int slots;                       // pages of a sequence
+    bool by_page;                    // as many pages as the cache has: fewer than the sequences' tables could name
     size_t off_v, off_map, off_inner, total;    // workspace: K, V, page map, the attention's own
 };
 
@@ -384,8 +385,8 @@ int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batc
         const int64_t some = (sinks + page - 1) / page + (window + rows) / page + 2;
         if (some < slots) slots = some;
     }
-    const int64_t pages = b->B * slots;
-    if (pages >= (int64_t(1) << 31)) return ctx_fail(c, PCK_EUNSUPPORTED, "B=%d sequences of up to %lld pages", b->B, (long long)slots);
+    x.by_page = k->n_pages < b->B * slots;
+    const int64_t pages = x.by_page ? k->n_pages : b->B * slots;
     x.slots = static_cast<int>(slots);
     x.cache.n_pages = pages;
     const size_t side = (size_t)pages * k->H_kv * page * k->D * 2;       // a multiple of 512 bytes
@@ -548,6 +549,7 @@ int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const p
     p.Vo = x.cache.V;
     p.pages = 1;
     p.slots = x.slots;
+    p.by_page = x.by_page;
     p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
     p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
     p.page_map = reinterpret_cast<int32_t*>(ws + x.off_map);

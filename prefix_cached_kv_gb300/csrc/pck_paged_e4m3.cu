@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(RD_THREADS, rd_blocks(DEPTH)) paged_read_kerne
         if (P.pages) {
             const int sp = (s.sinks + P.page - 1) / P.page, wp = s.lo / P.page;
             const int os = wp > sp && pi >= wp ? pi - wp + sp : pi;
-            if (os >= P.slots) return;                      // (only where kv_len or cu_rows made no sense)
-            out = b * P.slots + os;
+            if (!P.by_page && os >= P.slots) return;        // (only where kv_len or cu_rows made no sense)
+            out = P.by_page ? page : b * P.slots + os;
             if (head == 0) P.page_map[(int64_t)b * P.max_pages + pi] = out;
         } else {
             out = s.r0;

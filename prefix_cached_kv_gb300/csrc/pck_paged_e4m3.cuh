@@ -51,8 +51,9 @@ struct ReadParams {
     void *Ko, *Vo;
     int64_t ko_row, ko_head, vo_row, vo_head;   // rows: strides of the outputs in elements
     // pages: the tokens that the rows see, sequence b's page i at slot i (behind the sinks' pages: counted from the window's
-    // first) of its `slots` output pages [slot][head][token][D], whose numbers go to page_map [B, max_pages]
-    int pages, slots, window, sinks;
+    // first) of its `slots` output pages [slot][head][token][D], whose numbers go to page_map [B, max_pages]; or (by_page) a page of
+    // the cache at its own number, which sequences that share it write alike
+    int pages, by_page, slots, window, sinks;
     int32_t* page_map;
 };
 cudaError_t launch_paged_read(const ReadParams& p, int out_dtype, int sms, cudaStream_t st);

@@ -36,9 +36,9 @@ namespace {
 constexpr float EV_LOW = -40.f;      // values of V below 2^-40 * 448 lose bits where no larger ones are seen
 constexpr float M_NONE = -1e30f;     // m before a visible key: finite, so that a hidden one's 2^(-inf - m) is 0
 constexpr float W_TOP = 61440.f, L_TOP = 1e30f;      // the largest weight (fp16 ends at 65,504), and sum of a unit's p
-// What an item costs beside its units, in units (as tk_item_units): a range per half CTA, 64 ragged sequences of 8 kv heads of 64,
-// 87 us with 12, 70 with 24, 86 with 48; per warp 73 with 2, 63 with 4, 61 with 6 and 10.
-__host__ __device__ constexpr int item_units8(int mode) { return mode == TK_WARP ? 5 : 24; }
+// What an item costs beside its units, in units (as tk_item_units). Ranges per half CTA, 24 x 1-4000 tokens: 19.3 us with 12, 19.4 with 16, 21.9
+// with 24; ranges per warp, 600 x 1-1000 tokens 39 with 3, 45 with 5, 49 with 8, and 64 ragged sequences 57, 58, 59.
+__host__ __device__ constexpr int item_units8(int mode) { return mode == TK_WARP ? 3 : 16; }
 // Tokens of a unit. At D = 64 what a unit costs whatever its size (its loads' addresses, its scales, votes) is a visible share:
 // 16 caches of 30,000 tokens 135 us with 32, 91 with 64; but short items then end in half-empty units (600 x 100 tokens 44 us
 // with 32, 56 with 64).
