@@ -419,8 +419,14 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
                           const pck_rows *Q, const pck_rows *K, const pck_rows *V, int norm, float eps,
                           const pck_rotary *rope, void *stream);
 
-/* pck_paged_attend over the values of a quantised cache. q_dtype: of Q and O, F16 or BF16. The workspace holds what the
- * rows see as 16-bit values of q_dtype (bf16 holds them exactly; fp16 those within its range, beyond which they are 65,504). */
+/* pck_paged_attend over the values of a quantised cache: rows, window, sinks, priors, outputs and limits as there. q_dtype: of
+ * Q and O, F16 or BF16.
+ * One row per sequence, or a few (as there): the codes are multiplied as they are, exactly, and the scales applied to the
+ * scores and to the weights, in fp32. Weights times their V scale are held as fp16 pairs, to 2^-37 of a head's largest (so V rows all
+ * of whose scales are below 2^-50 lose bits); a bf16 q to 2^-39 of the row's largest element.
+ * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: at most
+ * as many as the cache has, at most max_pages per sequence, with a window only those that it reaches. bf16 holds the values
+ * exactly, fp16 those within its range. */
 int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,
                           const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
                           const float *O_prior, const float *LSE_prior, void *O, float *LSE,

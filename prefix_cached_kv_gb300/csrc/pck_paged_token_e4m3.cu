@@ -5,9 +5,9 @@ namespace pck {
 
 int paged_token_e4m3_box(const PagedAttn& p, int D) { return sub8(D, p.mode); }
 
-// Items per SM above which a range is a warp's: where an item could have a CTA of its own (64 x 500 tokens, 3.4 per SM: 27 us with
-// one, 37 with a range per warp), and where it could not (64 ragged sequences of 100-16k tokens at D = 64: 63 us with a range per warp, 70
-// per half CTA; at D = 128 81 against 82, pages of 16 tokens 87 against 90).
+// Items per SM above which a range is a warp's: where an item could have a CTA of its own (64 x 500 tokens, 3.4 per SM: 23.2 us with
+// one, 25.2 with a range per warp), and where it could not (64 ragged sequences of 100-16k tokens at D = 64: 57 us with a range per
+// warp, 59 per half CTA; at D = 128 with pages of 16 tokens 84 against 86, of 64 78.5 against 77.8).
 constexpr int T8_FEW_SHORT = 6, T8_FEW = 2;
 // Tokens up to which an item gets a CTA: by the table's width (one sequence of 1000 tokens 12.3 us, of 2000, cut, 12.6), and where a window
 // bounds them, so that most items have that length, and they fill the CTAs (32 windows of 2048 tokens, 8 kv heads: 29.6 us against 34.1

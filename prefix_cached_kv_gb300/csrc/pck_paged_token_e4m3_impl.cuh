@@ -21,10 +21,10 @@
 //    the largest of s + ev (a token's largest share of O) is TOP, and moves only when a weight passes W_TOP: that is seen on
 //    the weights themselves, not on the scores. ev counts from EV_LOW up in m, which keeps l within fp32.
 //  * Up to 4 columns (4 q heads per kv head): the weights' lo parts take columns 4-7 of the MMA's 8, one MMA instead of two.
-// Measured (graph replays): one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 48 us, 5.6 TB/s; 16 caches of 30-65k
-// tokens (2 kv heads of 256) 124 us, 6.1 TB/s; 64 ragged sequences (8 kv heads of 64, prior) 63 us, 3.7 TB/s; 32 windows of up to 2048
-// tokens (8 kv heads of 128, 8 q heads each) 36 us, 3.3 TB/s; 300 tokens 8.8 us. What is left: the start (lengths, page table and first loads one after
-// another, 5-7 us), the end of the slowest range and the join (3-5 us); in between the loads run at 5.5-6.3 TB/s.
+// Measured (graph replays): one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 47.6 us, 5.7 TB/s; 16 caches of 30-65k
+// tokens (2 kv heads of 256) 125 us, 6.0 TB/s; 64 ragged sequences (8 kv heads of 64, prior) 57 us, 4.1 TB/s; 32 windows of up to
+// 2048 tokens (8 kv heads of 128, 8 q heads each) 32 us, 3.7 TB/s; 300 tokens 6.5 us. What is left: the start (lengths, page table and
+// first loads one after another, 5-8 us), the slowest range's end and the join (3-5 us); in between the loads run at 5.5-6.3 TB/s.
 #pragma once
 
 #include "pck_paged_e4m3.cuh"
@@ -46,7 +46,7 @@ __host__ __device__ constexpr int sub8(int D, int mode) {
     return D > 128 ? 16 : D == 64 && (mode == TK_CTA || mode == TK_CTA_HALF) ? 64 : 32;
 }
 // Warps per SM: 192 KB of ring, 3 stages each (4 at D = 192). 12 warps of 2 stages: one cache of 131k tokens 49.7 us against
-// 48.0, 32 windows of 2048 tokens 36 us either way, 4 rows on 20-32k tokens 90 against 63 (registers).
+// 48.0, 4 rows on 20-32k tokens 90 against 63 (registers).
 __host__ __device__ constexpr int warps_sm8(int D, int mode) { return D == 64 && sub8(D, mode) == 32 ? 16 : 8; }
 
 template <int D, int MODE, bool QUAD>
