@@ -565,21 +565,21 @@ def row_prefill(ctx, torch, pk, reps=10, fmt=0):
             "frac_tensor_bf16_peak": round(tf / pk["bf16"], 4), "gflop_per_layer": round(flops_layer / 1e9, 3)}
 
 
-def paged_case(name):
-    """A case of perf/operators.py with the framework's calls: the module and the case."""
+def paged_case(name, file="operators"):
+    """A case (None: all) of perf/operators.py, or of perf/more_operators.py, with the framework's calls: the module and the cases."""
     import importlib.util
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    spec = importlib.util.spec_from_file_location(file, os.path.join(ROOT, "perf", file + ".py"))
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     mod.own = True
     return mod, [c for c in mod.listed() if name is None or c["name"] == name]
 
 
-def row_paged(ctx, torch, pk, calls=12):
-    """The paged-tail operators over the cases of perf/operators.py: device time per call in a captured graph of 12
+def row_paged(ctx, torch, pk, file="operators", calls=12):
+    """The paged-tail operators over the cases of perf/operators.py (or, in 8 bits, of perf/more_operators.py): device time per call in a captured graph of 12
     calls that rotate over three states, against the larger of the bytes' and the operations' time at the measured peaks.
     (States of the largest cases are larger than L2; the smallest are launch-bound whatever the cache holds.)"""
-    mod, cases = paged_case(None)
+    mod, cases = paged_case(None, file)
     out = {}
     for c in cases:
         states = [mod.prepare(c, k) for k in range(3)]
@@ -601,9 +601,12 @@ def row_paged(ctx, torch, pk, calls=12):
 
 # ------------------------------------------------------------------ single launches for Nsight Compute
 
-# profile rows of the paged tail: cases of perf/operators.py
-PAGED_PROFILES = {"norm_rope": "norm_rope long prompt", "paged_append": "append ragged prompts",
-                  "paged_token": "token, ragged batch, prefix", "paged_rows": "prompts, window and sinks"}
+# profile rows of the paged tail: cases of perf/operators.py, and in 8 bits of perf/more_operators.py
+PAGED_PROFILES = {"norm_rope": ("norm_rope long prompt",), "paged_append": ("append ragged prompts",),
+                  "paged_token": ("token, ragged batch, prefix",), "paged_rows": ("prompts, window and sinks",),
+                  "append_e4m3": ("append ragged prompts", "more_operators"), "read_e4m3": ("read long sessions", "more_operators"),
+                  "token_e4m3": ("token, ragged batch, prefix", "more_operators"), "long_e4m3": ("token, one long cache", "more_operators"),
+                  "window_e4m3": ("token, window and sinks", "more_operators")}
 
 
 def profile_row(row, ctx, torch):
@@ -613,7 +616,7 @@ def profile_row(row, ctx, torch):
     gather decode, merge); quant = one cartridge layer's K and V (354 MB in); warm = the same
     layer's records dequantised to fp16; prefill = one batched-Q layer (fp16 prefix);
     prefill_mlx = the same over an mlx4g32 prefix; norm_rope, paged_append, paged_token and paged_rows = one call of
-    that paged-tail operator."""
+    that paged-tail operator; the *_e4m3 rows = the same in 8 bits, and its rows read back."""
     from prefix_cached_kv_gb300 import binding, synth
     if row == "fp16":
         H, N, D, R = 8, 2048, 128, 64
@@ -659,7 +662,7 @@ def profile_row(row, ctx, torch):
         Vs = torch.randn((H_kv, S, D), device="cuda").half()
         fn = lambda: ctx.query_fused("pp", 0, Q, Ks, Vs)
     elif row in PAGED_PROFILES:
-        mod, (case,) = paged_case(PAGED_PROFILES[row])
+        mod, (case,) = paged_case(*PAGED_PROFILES[row])
         state = mod.prepare(case, 0)
         fn = lambda: mod.run(state)
     else:
@@ -837,10 +840,10 @@ def main():
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--rows", default="all",
                     help="all | comma list of main,fp16,dims,sparse,prefill,prefill_mlx,cartridge (main = the headline line), "
-                         "and paged (not in all): the paged-tail operators")
+                         "and paged, paged_e4m3 (not in all): the paged-tail operators")
     ap.add_argument("--profile", default=None,
                     help="fp16 | sparse | quant | warm | prefill | prefill_mlx | norm_rope | paged_append | paged_token | "
-                         "paged_rows: one capture-sized run of that row")
+                         "paged_rows | append_e4m3 | read_e4m3 | token_e4m3 | long_e4m3 | window_e4m3: one capture-sized run of that row")
     args = ap.parse_args()
     if args.impl == "reference":
         run_reference(args)
@@ -886,6 +889,8 @@ def main():
         rows["A1_A3_N2_cartridge"] = row_cartridge(ctx, torch, pk)
     if "paged" in want:
         rows["paged_tail"] = row_paged(ctx, torch, pk)
+    if "paged_e4m3" in want:
+        rows["paged_tail_e4m3"] = row_paged(ctx, torch, pk, "more_operators")
     ctx.close()
     if rank() != 0:
         return
