@@ -423,7 +423,8 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
  * Q and O, F16 or BF16.
  * One row per sequence, or a few (as there): the codes are multiplied as they are, exactly, and the scales applied to the
  * scores and to the weights, in fp32. Weights times their V scale are held as fp16 pairs, to 2^-37 of a head's largest (so V rows all
- * of whose scales are below 2^-50 lose bits); a bf16 q to 2^-39 of the row's largest element.
+ * of whose scales are below 2^-50 lose bits); a bf16 q to 2^-39 of the row's largest element; a scale of 2^-127 (byte 0, which an append
+ * never writes) counts as 0.
  * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: at most
  * as many as the cache has, at most max_pages per sequence, with a window only those that it reaches. bf16 holds the values
  * exactly, fp16 those within its range. */

@@ -1,15 +1,260 @@
 // pck_paged_e4m3.cu -- the append to a quantised paged cache, and rows of that cache read back.
 //
+// The append: y = rope(x * rsqrt(mean(x^2) + eps) * w) for q and k, v as it is (pck_paged_rope_impl.cuh), all in fp32; q is rounded
+// to its type; a k or v head row becomes codes and one exponent byte: with a = max |y| over the finite elements, the least e with
+// a 2^-e <= 448 (e held to -126 .. 120) and codes rn(y 2^-e). A shift of exponents rounds nothing, so a code is y's one
+// rounding. HBM bounds it. Rows are held as in the 16-bit append (D/16 lanes, two vectors of 8), with a loop of its own per kind of
+// head, packed fp32 arithmetic, and each lane's next heads on their way into shared memory by asynchronous copies: a thread goes
+// through a dozen heads, each a round trip to memory, and more of them in registers cost the warps that would hide them. 8
+// ragged prompts, 32 + 8 + 8 heads of 128: 61.5 us as the 16-bit kernel with another store (two heads in registers, 65 % of the issue slots),
+// 61.4 with a loop per kind and packed arithmetic, 51 with the copies, at three blocks an SM; four blocks spill (62), two 57.
+//
 // Reading back: out = code * 2^e, rounded once to the output's type (fp32 and bf16 hold it exactly; in fp16 what is beyond
 // 65,504 becomes 65,504). D + 1 bytes in and 2 D or 4 D out per row, so HBM bounds it. A warp takes tiles of 16 tokens of one kv
 // head, K and V: 8 codes a lane, so that its 16-byte stores lie side by side, with DEPTH loads of K and of V in flight before the
 // first is used: 6.1 TB/s read and written on the long sessions (0.90 of a copy).
 // The tiles of all sequences laid end to end are dealt to the warps from the lengths on the device (one block scan), so
 // one long session and many short ones fill the GPU alike.
+#include <type_traits>
+
+#include "pck_paged_e4m3.cuh"
 #include "pck_paged_rope_impl.cuh"
 
 namespace pck {
 namespace {
+
+// ---------------------------------------------------------------- append
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{ .reg .b64 x, y, w, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 w, {%6, %7}; fma.rn.f32x2 z, x, y, w; mov.b64 {%0, %1}, z; }"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// Codes of 8 values times `down`.
+__device__ __forceinline__ void store_codes(uint8_t* p, const float2 (&x)[4], float2 down) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = mul2(x[i], down);
+        w[i] = codes2(y.x, y.y);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+template <typename TI>
+__device__ __forceinline__ void unpack8(const typename Vec8<TI>::Raw& r, float2 (&x)[4]) {
+    float f[8];
+    Vec8<TI>::unpack(r, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+
+// Blocks per SM, and heads whose copies a lane has in flight.
+constexpr int A8_BLOCKS = 3;
+template <typename TI> __host__ __device__ constexpr int a8_depth() { return sizeof(TI) == 4 ? 2 : 3; }
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <typename TI, int L>
+__global__ void __launch_bounds__(NR_THREADS, A8_BLOCKS) append8_kernel(const __grid_constant__ RopeParams P) {
+    typedef typename Vec8<TI>::Raw Raw;
+    constexpr int SUBS = NR_THREADS / L;
+    pdl_wait();
+    pdl_release();
+    const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+    const int64_t t64 = (int64_t)blockIdx.x * (SUBS / P.spt) + sub / P.spt;
+    const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
+    if (t64 >= P.T) return;
+    const int t = static_cast<int>(t64), h0 = sub % P.spt;
+    if (h0 >= P.q.H + P.k.H + P.v.H) return;
+    const bool active = lane < P.D / 16;
+    const int rv = P.R / 16;
+    const bool rot = lane < rv;
+    const int s0 = rot ? lane : P.R / 8 + (lane - rv);            // the lane's two vectors
+    const int s1 = rot ? lane + rv : s0 + (P.D - P.R) / 16;
+    // The thread's heads, those of all kinds one behind the other: its n-th is h0 + n spt. Each lane copies its two vectors of the
+    // next DEPTH of them into shared memory, the first while the row's sequence, page and angles are looked up one after another.
+    constexpr int DEPTH = a8_depth<TI>();
+    __shared__ __align__(16) Raw ring[NR_THREADS / 32][DEPTH][2][32];
+    Raw(*mine)[2][32] = ring[threadIdx.x >> 5];
+    const int in_warp = threadIdx.x & 31, Hqk = P.q.H + P.k.H, Ht = Hqk + P.v.H;
+    int next = h0, put = 0, get = 0;
+    const auto fetch = [&]() {
+        if (next < Ht && active) {
+            const RowsArg& A = next < P.q.H ? P.q : next < Hqk ? P.k : P.v;
+            const int h = next - (next < P.q.H ? 0 : next < Hqk ? P.q.H : Hqk);
+            const TI* src = static_cast<const TI*>(A.in) + (int64_t)t * A.in_row + (int64_t)h * A.in_head;
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(Raw); i += 16) {
+                copy16(reinterpret_cast<uint8_t*>(&mine[put][0][in_warp]) + i, reinterpret_cast<const uint8_t*>(src + 8 * s0) + i);
+                copy16(reinterpret_cast<uint8_t*>(&mine[put][1][in_warp]) + i, reinterpret_cast<const uint8_t*>(src + 8 * s1) + i);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next += P.spt;
+        put = put + 1 == DEPTH ? 0 : put + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < DEPTH; ++i) fetch();
+    RowPlace at = {};
+    if (!place_row<TI, L>(P, t, lane, mask, h0, at)) return;
+    float co[8], si[8];
+    if (P.R > 0 && !load_angles(P, t, lane, at.pos, rot, s0, s1, co, si)) return;
+
+    // KIND 0: q, 1: k, 2: v. The heads of all kinds one behind the other are dealt to the token's subwarps in turn.
+    const auto heads = [&](auto kind, const RowsArg& A, int first) {
+        constexpr int KIND = decltype(kind)::value;
+        Raw w0 = Raw{}, w1 = Raw{};
+        const bool norm = KIND != 2 && A.norm, weight = norm && A.w;
+        if (weight && active && first < A.H) {
+            w0 = *reinterpret_cast<const Raw*>(static_cast<const TI*>(A.w) + 8 * s0);
+            w1 = *reinterpret_cast<const Raw*>(static_cast<const TI*>(A.w) + 8 * s1);
+        }
+#pragma unroll 1
+        for (int h = first; h < A.H; h += P.spt) {
+            float2 x[4], y[4];
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+            unpack8<TI>(active ? mine[get][0][in_warp] : Raw{}, x);
+            unpack8<TI>(active ? mine[get][1][in_warp] : Raw{}, y);
+            get = get + 1 == DEPTH ? 0 : get + 1;
+            fetch();          // into the place just read
+            if (norm) {
+                float2 ss = mul2(x[0], x[0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ss = fma2(y[i], y[i], ss);
+                float sum = ss.x + ss.y;
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(mask, sum, o, L);
+                const float r = rsqrtf(sum * P.inv_d + P.eps);
+                const float2 rr = make_float2(r, r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = mul2(x[i], rr);
+                    y[i] = mul2(y[i], rr);
+                }
+                if (weight) {
+                    float2 u[4], v[4];
+                    unpack8<TI>(w0, u);
+                    unpack8<TI>(w1, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = mul2(x[i], u[i]);
+                        y[i] = mul2(y[i], v[i]);
+                    }
+                }
+            }
+            if (KIND != 2 && rot) {
+                if (P.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = x[i], b = y[i];
+                        x[i] = make_float2(a.x * co[i] - a.y * si[i], a.y * co[i] + a.x * si[i]);
+                        y[i] = make_float2(b.x * co[4 + i] - b.y * si[4 + i], b.y * co[4 + i] + b.x * si[4 + i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 c = make_float2(co[2 * i], co[2 * i + 1]), s = make_float2(si[2 * i], si[2 * i + 1]);
+                        const float2 a = x[i], b = y[i], nb = make_float2(-b.x, -b.y);
+                        x[i] = fma2(nb, s, mul2(a, c));
+                        y[i] = fma2(a, s, mul2(b, c));
+                    }
+                }
+            }
+            if (KIND == 0) {
+                if (!active) continue;
+                float f[8], g[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f[2 * i] = x[i].x;
+                    f[2 * i + 1] = x[i].y;
+                    g[2 * i] = y[i].x;
+                    g[2 * i + 1] = y[i].y;
+                }
+                TI* dst = static_cast<TI*>(A.out) + (int64_t)t * A.out_row + (int64_t)h * A.out_head;
+                Vec8<TI>::store(dst + 8 * s0, f);
+                Vec8<TI>::store(dst + 8 * s1, g);
+                continue;
+            }
+            const auto largest = [&]() {               // (fmaxf passes over NaN)
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a = fmaxf(a, fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(y[i].x), fabsf(y[i].y))));
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o, L));
+                return a;
+            };
+            float a = largest();
+            if (a == INFINITY) {                       // e4m3 has no infinity: those elements become NaN, the scale is the others'
+                const auto finite = [](float v) { return fabsf(v) == INFINITY ? NAN : v; };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = make_float2(finite(x[i].x), finite(x[i].y));
+                    y[i] = make_float2(finite(y[i].x), finite(y[i].y));
+                }
+                a = largest();
+            }
+            const int e = scale_byte(a);
+            if (active) {
+                const float down = scale_down(e);
+                const float2 d2 = make_float2(down, down);
+                uint8_t* dst = static_cast<uint8_t*>(A.out) + (KIND == 1 ? at.k : at.v) + (int64_t)h * A.out_head;
+                store_codes(dst + 8 * s0, x, d2);
+                store_codes(dst + 8 * s1, y, d2);
+            }
+            if (lane == 0) (KIND == 1 ? P.k_scale : P.v_scale)[at.s + (int64_t)h * P.page] = static_cast<uint8_t>(e);
+        }
+    };
+    heads(std::integral_constant<int, 0>{}, P.q, h0);
+    heads(std::integral_constant<int, 1>{}, P.k, (h0 - P.q.H) & (P.spt - 1));                  // (spt is a power of two)
+    heads(std::integral_constant<int, 2>{}, P.v, (h0 - P.q.H - P.k.H) & (P.spt - 1));
+}
+
+template <typename TI, int L>
+cudaError_t launch_append_l(RopeParams p, int sms, cudaStream_t st) {
+    constexpr int SUBS = NR_THREADS / L;
+    const int Ht = p.q.H + p.k.H + p.v.H;
+    int spt = 32 / L;                    // as the 16-bit append's
+    while (spt < SUBS && spt < Ht && (int64_t)p.T * spt < (int64_t)sms * (2048 / L)) spt *= 2;
+    p.spt = spt;
+    p.inv_d = 1.0f / p.D;
+    const int tpb = SUBS / spt;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((p.T + tpb - 1) / tpb);
+    cfg.blockDim = dim3(NR_THREADS);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append8_kernel<TI, L>, p);
+}
+
+template <typename TI>
+cudaError_t launch_append_t(const RopeParams& p, int sms, cudaStream_t st) {
+    const int l = p.D / 16;
+    if (l <= 2) return launch_append_l<TI, 2>(p, sms, st);
+    if (l <= 4) return launch_append_l<TI, 4>(p, sms, st);
+    if (l <= 8) return launch_append_l<TI, 8>(p, sms, st);
+    if (l <= 16) return launch_append_l<TI, 16>(p, sms, st);
+    return launch_append_l<TI, 32>(p, sms, st);
+}
+
+// ---------------------------------------------------------------- reading back
 
 constexpr int RD_THREADS = 256;
 // Pieces of 8 codes of K, and of V, that a lane has in flight (DEPTH), and blocks per SM.
@@ -250,9 +495,9 @@ cudaError_t launch_paged_read(const ReadParams& p, int out_dtype, int sms, cudaS
 }
 
 cudaError_t launch_append_e4m3(const RopeParams& p, int in_dtype, int sms, cudaStream_t st) {
-    if (in_dtype == PCK_DT_F16) return launch_t<__half, E4m3>(p, sms, st);
-    if (in_dtype == PCK_DT_BF16) return launch_t<__nv_bfloat16, E4m3>(p, sms, st);
-    return launch_t<float, E4m3>(p, sms, st);
+    if (in_dtype == PCK_DT_F16) return launch_append_t<__half>(p, sms, st);
+    if (in_dtype == PCK_DT_BF16) return launch_append_t<__nv_bfloat16>(p, sms, st);
+    return launch_append_t<float>(p, sms, st);
 }
 
 }  // namespace pck

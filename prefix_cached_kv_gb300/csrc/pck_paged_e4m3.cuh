@@ -11,10 +11,6 @@
 
 namespace pck {
 
-struct E4m3 {
-    uint8_t bits;
-};
-
 // Two codes, the first in the low byte (NaN stays NaN; what is beyond 448 becomes 448).
 __device__ __forceinline__ uint32_t codes2(float x0, float x1) {
     uint16_t r;

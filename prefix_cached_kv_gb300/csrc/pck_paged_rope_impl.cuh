@@ -1,15 +1,11 @@
 // pck_paged_rope_impl.cuh -- head norms with the rotary rotation, and the append of new keys and values to a
-// paged cache, in 16 bits or quantised to e4m3.
+// paged cache (the quantising append shares what places a row and its angles).
 //
 // Per row x (one token, one head, D elements) and position t:
 //   y = x * rsqrt(mean(x^2) + eps) * w                       (q and k heads with a norm)
 //   (a, b) -> (a cos - b sin, b cos + a sin)                 for the R/2 pairs of the first R elements
 // with cos and sin read from the caller's fp32 table row t. Norm, weight and rotation stay in fp32
 // and are rounded once, to the output's type. V rows are copied (converted where the types differ).
-// A quantised cache takes each k or v head row as codes and one exponent byte: with a = max |y| over the finite
-// elements, the least e with a 2^-e <= 448 (e4m3's largest value; e held to -126 .. 120) and codes rn(y 2^-e), all from the
-// fp32 row: a shift of exponents rounds nothing, so a code is y's one rounding. The maximum takes log2 L more shuffles, and what it adds shows: 8 ragged prompts,
-// 32 + 8 + 8 heads of 128, 61.6 us (4.9 TB/s, 65 % of the issue slots) where 16-bit pages take 59 with 9 % more bytes.
 //
 // Every byte is read and written once, so HBM bounds it. A row is held by L = D/16 lanes (a power
 // of two at least), each with two vectors of 8 elements: vector p and vector p + R/16 of the
@@ -21,10 +17,7 @@
 // written (0.85 of a copy); an append of 8 ragged prompts, 32 + 8 + 8 heads: 59 us, 5.5 TB/s.
 #pragma once
 
-#include <type_traits>
-
 #include "pck_paged.cuh"
-#include "pck_paged_e4m3.cuh"
 
 namespace pck {
 namespace {
@@ -96,13 +89,77 @@ struct Vec8<float> {
     }
 };
 
-// Codes of 8 values times `down`.
-__device__ __forceinline__ void store_codes(E4m3* p, const float (&x)[8], float down) {
-    uint32_t w[2];
+// Where an append puts a row: offsets into the cache (of head 0), and its cache position. False: the row is not to be stored.
+struct RowPlace {
+    int64_t k, v, s;                 // s: of the scale bytes, [page][head][slot]
+    int pos;
+};
+template <typename TI, int L>
+__device__ __forceinline__ bool place_row(const RopeParams& P, int t, int lane, uint32_t mask, int h0, RowPlace& at) {
+    int b = t, n_b_left = 1;
+    if (P.cu_rows) {
+        int cnt = 0;   // sequences whose rows start at or before t
+        bool bad = false;
+        for (int i = lane; i <= P.B; i += L) {
+            const int r0 = P.cu_rows[i];
+            cnt += r0 <= t;
+            if (blockIdx.x == 0 && i < P.B) bad |= !rows_sound(r0, P.cu_rows[i + 1], P.T);
+        }
+        if (bad) set_err(P.err, ERR_KV_LEN);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = codes2(x[4 * i] * down, x[4 * i + 1] * down) | codes2(x[4 * i + 2] * down, x[4 * i + 3] * down) << 16;
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        for (int o = L / 2; o; o >>= 1) cnt += __shfl_xor_sync(mask, cnt, o, L);
+        b = cnt - 1;
+        if (b < 0 || b >= P.B) return false;   // a row of no sequence
+        const int r1 = P.cu_rows[b + 1];
+        if (P.cu_rows[b] > t || r1 <= t) return false;   // (nor here: cu_rows does not ascend)
+        n_b_left = r1 - t;
+    }
+    const int64_t p = (int64_t)P.kv_len[b] - n_b_left;
+    if (p < 0) {                                // no such token: a padded sequence stores nothing, and its q is 0
+        const float zero[8] = {};
+        if (lane < P.D / 16)
+            for (int h = h0; h < P.q.H; h += P.spt) {
+                TI* dst = static_cast<TI*>(P.q.out) + (int64_t)t * P.q.out_row + (int64_t)h * P.q.out_head + 16 * lane;
+                Vec8<TI>::store(dst, zero);
+                Vec8<TI>::store(dst + 8, zero);
+            }
+        return false;
+    }
+    if (p >= (int64_t)P.max_pages * P.page) {
+        if (lane == 0) set_err(P.err, ERR_KV_LEN);
+        return false;
+    }
+    const int pi = static_cast<int>(p) / P.page, slot = static_cast<int>(p) - pi * P.page;
+    const int pg = P.table[(int64_t)b * P.max_pages + pi];
+    if (pg < 0 || pg >= P.n_pages) {
+        if (lane == 0) set_err(P.err, ERR_PAGE_ID);
+        return false;
+    }
+    at.k = pg * P.k_page + slot * P.k.out_row;
+    at.v = pg * P.v_page + slot * P.v.out_row;
+    at.s = (int64_t)pg * P.k.H * P.page + slot;
+    at.pos = static_cast<int>(p);
+    return true;
+}
+
+// The lane's cosines and sines: false where the position has no row of the table.
+__device__ __forceinline__ bool load_angles(const RopeParams& P, int t, int lane, int pos, bool rot, int s0, int s1, float (&co)[8],
+                                            float (&si)[8]) {
+    if (P.positions) pos = P.positions[t];
+    if (pos < 0 || pos >= P.n_pos) {
+        if (lane == 0) set_err(P.err, ERR_ROPE_POS);
+        return false;
+    }
+    if (rot) {
+        const float* row = P.cos_sin + (int64_t)pos * P.R;
+        // pairs 8 lane .. +7 of split halves; pairs 4 s0 .. and 4 s1 .. of adjacent ones
+        const int i0 = P.interleaved ? 4 * s0 : 8 * lane, i1 = P.interleaved ? 4 * s1 : 8 * lane + 4;
+        *reinterpret_cast<float4*>(co) = *reinterpret_cast<const float4*>(row + i0);
+        *reinterpret_cast<float4*>(co + 4) = *reinterpret_cast<const float4*>(row + i1);
+        *reinterpret_cast<float4*>(si) = *reinterpret_cast<const float4*>(row + P.R / 2 + i0);
+        *reinterpret_cast<float4*>(si + 4) = *reinterpret_cast<const float4*>(row + P.R / 2 + i1);
+    }
+    return true;
 }
 
 // L: lanes per row. TI: type of the rows read (and of q written); TC: type of the cache (append).
@@ -121,54 +178,10 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
     const int Ht = P.q.H + P.k.H + P.v.H;
     if (h0 >= Ht) return;
 
-    // ---- the row's sequence, cache position and page slot
-    int64_t kbase = 0, vbase = 0, sbase = 0;
-    int pos = 0;
-    if (P.append) {
-        int b = t, n_b_left = 1;
-        if (P.cu_rows) {
-            int cnt = 0;   // sequences whose rows start at or before t
-            bool bad = false;
-            for (int i = lane; i <= P.B; i += L) {
-                const int r0 = P.cu_rows[i];
-                cnt += r0 <= t;
-                if (blockIdx.x == 0 && i < P.B) bad |= !rows_sound(r0, P.cu_rows[i + 1], P.T);
-            }
-            if (bad) set_err(P.err, ERR_KV_LEN);
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) cnt += __shfl_xor_sync(mask, cnt, o, L);
-            b = cnt - 1;
-            if (b < 0 || b >= P.B) return;         // a row of no sequence
-            const int r1 = P.cu_rows[b + 1];
-            if (P.cu_rows[b] > t || r1 <= t) return;   // (nor here: cu_rows does not ascend)
-            n_b_left = r1 - t;
-        }
-        const int64_t p = (int64_t)P.kv_len[b] - n_b_left;
-        if (p < 0) {                                // no such token: a padded sequence stores nothing, and its q is 0
-            const float zero[8] = {};
-            if (lane < P.D / 16)
-                for (int h = h0; h < P.q.H; h += P.spt) {
-                    TI* dst = static_cast<TI*>(P.q.out) + (int64_t)t * P.q.out_row + (int64_t)h * P.q.out_head + 16 * lane;
-                    Vec8<TI>::store(dst, zero);
-                    Vec8<TI>::store(dst + 8, zero);
-                }
-            return;
-        }
-        if (p >= (int64_t)P.max_pages * P.page) {
-            if (lane == 0) set_err(P.err, ERR_KV_LEN);
-            return;
-        }
-        const int pi = static_cast<int>(p) / P.page, slot = static_cast<int>(p) - pi * P.page;
-        const int pg = P.table[(int64_t)b * P.max_pages + pi];
-        if (pg < 0 || pg >= P.n_pages) {
-            if (lane == 0) set_err(P.err, ERR_PAGE_ID);
-            return;
-        }
-        kbase = pg * P.k_page + slot * P.k.out_row;
-        vbase = pg * P.v_page + slot * P.v.out_row;
-        sbase = (int64_t)pg * P.k.H * P.page + slot;      // of the scale bytes, [page][head][slot]
-        pos = static_cast<int>(p);
-    }
+    RowPlace at = {};
+    if (P.append && !place_row<TI, L>(P, t, lane, mask, h0, at)) return;
+    const int64_t kbase = at.k, vbase = at.v;
+    int pos = at.pos;
     const bool active = lane < P.D / 16;
     const int rv = P.R / 16;
     const bool rot = lane < rv;
@@ -177,24 +190,11 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
     const int s1 = rot ? lane + rv : s0 + (P.D - P.R) / 16;
     float co[8], si[8];
     if (P.R > 0) {
-        if (P.positions) pos = P.positions[t];
-        if (pos < 0 || pos >= P.n_pos) {
-            if (lane == 0) set_err(P.err, ERR_ROPE_POS);
-            return;
-        }
-        if (rot) {
-            const float* row = P.cos_sin + (int64_t)pos * P.R;
-            // pairs 8 lane .. +7 of split halves; pairs 4 s0 .. and 4 s1 .. of adjacent ones
-            const int i0 = P.interleaved ? 4 * s0 : 8 * lane, i1 = P.interleaved ? 4 * s1 : 8 * lane + 4;
-            *reinterpret_cast<float4*>(co) = *reinterpret_cast<const float4*>(row + i0);
-            *reinterpret_cast<float4*>(co + 4) = *reinterpret_cast<const float4*>(row + i1);
-            *reinterpret_cast<float4*>(si) = *reinterpret_cast<const float4*>(row + P.R / 2 + i0);
-            *reinterpret_cast<float4*>(si + 4) = *reinterpret_cast<const float4*>(row + P.R / 2 + i1);
-        }
+        if (!load_angles(P, t, lane, pos, rot, s0, s1, co, si)) return;
     }
 
     typedef typename Vec8<TI>::Raw Raw;
-    auto at = [&](const void* p, int64_t off) { return static_cast<const TI*>(p) + off; };
+    auto elem = [&](const void* p, int64_t off) { return static_cast<const TI*>(p) + off; };
     // NR_HEADS heads at a time, all of their loads in flight before the first is used
     for (int hb = h0; hb < Ht; hb += NR_HEADS * P.spt) {
         Raw r0[NR_HEADS], r1[NR_HEADS];
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
                 const int cls = hh < P.q.H ? 0 : hh < P.q.H + P.k.H ? 1 : 2;
                 const RowsArg& A = cls == 0 ? P.q : cls == 1 ? P.k : P.v;
                 const int h = hh - (cls == 0 ? 0 : cls == 1 ? P.q.H : P.q.H + P.k.H);
-                const TI* src = at(A.in, (int64_t)t * A.in_row + (int64_t)h * A.in_head);
+                const TI* src = elem(A.in, (int64_t)t * A.in_row + (int64_t)h * A.in_head);
                 r0[k] = *reinterpret_cast<const Raw*>(src + 8 * s0);
                 r1[k] = *reinterpret_cast<const Raw*>(src + 8 * s1);
             }
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
                 const float r = rsqrtf(ss * P.inv_d + P.eps);
                 if (A.w && active) {
                     float w0[8], w1[8];
-                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(at(A.w, 8 * s0)), w0);
-                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(at(A.w, 8 * s1)), w1);
+                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(elem(A.w, 8 * s0)), w0);
+                    Vec8<TI>::unpack(*reinterpret_cast<const Raw*>(elem(A.w, 8 * s1)), w1);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         x[i] = x[i] * r * w0[i];
@@ -264,47 +264,16 @@ __global__ void __launch_bounds__(NR_THREADS, nr_blocks<TI>()) norm_rope_kernel(
                     }
                 }
             }
-            if constexpr (std::is_same<TC, E4m3>::value) {
-                if (cls != 0) {
-                    float a = 0.f;                     // (fmaxf passes over NaN)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a = fmaxf(a, fmaxf(fabsf(x[i]), fabsf(y[i])));
-#pragma unroll
-                    for (int o = L / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o, L));
-                    if (a == INFINITY) {               // e4m3 has no infinity: those elements become NaN, the scale is the others'
-                        a = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x[i] = fabsf(x[i]) == INFINITY ? NAN : x[i];
-                            y[i] = fabsf(y[i]) == INFINITY ? NAN : y[i];
-                            a = fmaxf(a, fmaxf(fabsf(x[i]), fabsf(y[i])));
-                        }
-#pragma unroll
-                        for (int o = L / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(mask, a, o, L));
-                    }
-                    const int e = scale_byte(a);
-                    const float down = scale_down(e);
-                    if (active) {
-                        E4m3* dst = static_cast<E4m3*>(A.out) + (cls == 1 ? kbase : vbase) + (int64_t)h * A.out_head;
-                        store_codes(dst + 8 * s0, x, down);
-                        store_codes(dst + 8 * s1, y, down);
-                    }
-                    if (lane == 0) (cls == 1 ? P.k_scale : P.v_scale)[sbase + (int64_t)h * P.page] = static_cast<uint8_t>(e);
-                    continue;
-                }
-            }
             if (!active) continue;
-            if constexpr (!std::is_same<TC, E4m3>::value) {
-                if (P.append && cls != 0) {
-                    TC* dst = static_cast<TC*>(A.out) + (cls == 1 ? kbase : vbase) + (int64_t)h * A.out_head;
-                    Vec8<TC>::store(dst + 8 * s0, x);
-                    Vec8<TC>::store(dst + 8 * s1, y);
-                    continue;
-                }
+            if (P.append && cls != 0) {
+                TC* dst = static_cast<TC*>(A.out) + (cls == 1 ? kbase : vbase) + (int64_t)h * A.out_head;
+                Vec8<TC>::store(dst + 8 * s0, x);
+                Vec8<TC>::store(dst + 8 * s1, y);
+            } else {
+                TI* dst = static_cast<TI*>(A.out) + (int64_t)t * A.out_row + (int64_t)h * A.out_head;
+                Vec8<TI>::store(dst + 8 * s0, x);
+                Vec8<TI>::store(dst + 8 * s1, y);
             }
-            TI* dst = static_cast<TI*>(A.out) + (int64_t)t * A.out_row + (int64_t)h * A.out_head;
-            Vec8<TI>::store(dst + 8 * s0, x);
-            Vec8<TI>::store(dst + 8 * s1, y);
         }
     }
 }
