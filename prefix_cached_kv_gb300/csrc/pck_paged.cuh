@@ -89,7 +89,7 @@ struct PagedAttn {
     int mode;                        // how the call is cut
     int n_ctas;
     const uint8_t *k_scale, *v_scale;   // a quantised cache's scales [n_pages, H_kv, page]
-    int halves;                      // its pages are no multiples of a unit: loaded in halves of 16 tokens
+    int pieces;                      // its pages are no multiples of a unit: loaded 16 tokens at a time, by the lanes
     // row kernel
     int n_split, row_tiles, box;     // key splits, row tiles of the grid, tokens of a TMA box
     const void *k_base, *v_base;

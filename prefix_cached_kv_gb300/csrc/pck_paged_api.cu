@@ -530,7 +530,7 @@ int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const p
         DeviceScope dev(v.device);
         if (!dev.ok) return ctx_fail(c, PCK_ECUDA, "cannot select device %d", v.device);
         const int rows = paged_token_e4m3_box(p, cache->D);     // (pages in pieces are not loaded by tiles)
-        if (!p.halves && (!encode_codes(&p.tm_k, cache->K, p.page, cache->D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows) ||
+        if (!p.pieces && (!encode_codes(&p.tm_k, cache->K, p.page, cache->D, p.H_kv, cache->n_pages, cache->k_token, cache->k_head, cache->k_page, rows) ||
             !encode_codes(&p.tm_v, cache->V, p.page, cache->D, p.H_kv, cache->n_pages, cache->v_token, cache->v_head, cache->v_page, rows)))
             return ctx_fail(c, PCK_ECUDA, "the driver refused the cache's tensor map");
         const cudaError_t e = launch_paged_token_e4m3(p, cache->D, static_cast<cudaStream_t>(stream));

@@ -14,7 +14,7 @@ constexpr int T8_FEW_SHORT = 6, T8_FEW = 2;
 // cut, of 4000 51 against 54).
 constexpr int T8_ITEM = 1024, T8_ITEM_WINDOW = 4096;
 
-// How a call is cut; fills heads_per_group, n_groups, cols, mode, halves and n_ctas, and returns the workspace bytes.
+// How a call is cut; fills heads_per_group, n_groups, cols, mode, pieces and n_ctas, and returns the workspace bytes.
 size_t paged_token_e4m3_plan(PagedAttn& p, int D, int sms) {
     const int most = paged_token_cols(D);
     const int rows = p.cu_rows ? p.max_rows : 1;
@@ -33,7 +33,7 @@ size_t paged_token_e4m3_plan(PagedAttn& p, int D, int sms) {
              : bound <= direct           ? (spread ? TK_ITEM_HALF : TK_ITEM)
              : items > (int64_t)T8_FEW * sms ? TK_WARP
                                            : (spread ? TK_CTA_HALF : TK_CTA);
-    p.halves = p.page % sub8(D, p.mode) != 0;
+    p.pieces = p.page % sub8(D, p.mode) != 0;
     p.n_ctas = is_split(p.mode) ? sms * per_sm(p.mode) : static_cast<int>(items);
     const size_t ranges = is_split(p.mode) ? (size_t)p.n_ctas * (p.mode == TK_WARP ? warps_sm8(D, TK_WARP) : 1) : 0;
     return ranges * (2 * slot_floats(D, p.cols) * sizeof(float) + sizeof(JoinDesc));

@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
     const uint8_t* s_sc = smem + C::OFF_SC + warp * ST * 2 * C::SCB;
     if (lane == 0) {
         // arrivals of a phase: the lanes' (all that copy pieces; those of the scales) and, with tile loads, that of their bytes
-        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, P.halves ? 32 : SC_LANES + 1);
+        for (int i = 0; i < ST; ++i) mbar_init(bar + 8 * i, P.pieces ? 32 : SC_LANES + 1);
         fence_mbar_init();
-        if (!P.halves) {
+        if (!P.pieces) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_k) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(&P.tm_v) : "memory");
         }
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
     const int nseq = SPLIT ? P.B : 1;     // sequences in pre[]
 
     // ---- a warp's units: u0 + k of its own range, u0 + warp + k NW of its CTA's. Lane i resolves unit k0 + i: coordinates of
-    // its loads (of both halves of 16 tokens where pages are no multiples of a unit)
+    // its loads (of each 16 tokens where pages are no multiples of a unit)
     const int64_t uf = BY_WARP ? u0 : u0 + warp;
     constexpr int STEP = BY_WARP ? 1 : NW;
     const uint64_t pol = l2_evict_first();
@@ -203,12 +203,12 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
             pl_head = x / P.n_groups;
 #pragma unroll
             for (int h = 0; h < NS; ++h) {
-                if (h > 0 && !P.halves) break;
+                if (h > 0 && !P.pieces) break;
                 const int tok = tok0 + 16 * h, pi = tok / P.page;
                 pl_tok[h] = tok - pi * P.page;
                 pl_page[h] = 0;
-                // a half that no row sees is not looked up (its page may not exist): the first page is read in its place
-                const bool seen = !P.halves || (tok < len && (tok + 16 > lo0 || tok < P.sinks));
+                // 16 tokens that no row sees are not looked up (their page may not exist): the first page is read in their place
+                const bool seen = !P.pieces || (tok < len && (tok + 16 > lo0 || tok < P.sinks));
                 if (len > 0 && rows > 0 && pi < P.max_pages && seen) {
                     const int pg = P.table[(int64_t)b * P.max_pages + pi];
                     if (pg < 0 || pg >= P.n_pages) set_err(P.err, ERR_PAGE_ID);   // and page 0 is read instead
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
             tok[h] = __shfl_sync(0xffffffffu, pl_tok[h], kp & 31);
             page[h] = __shfl_sync(0xffffffffu, pl_page[h], kp & 31);
         }
-        if (P.halves) {
+        if (P.pieces) {
             const uint8_t *kc[NS], *vc[NS];
 #pragma unroll
             for (int h = 0; h < NS; ++h) {
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
             }
 #pragma unroll
             for (int i = 0; i < SUB * KS / 32; ++i) {
-                const int t = (lane + 32 * i) / KS, c = (lane + 32 * i) % KS, h = 32 * i / KS / 16;     // (a step stays in a half)
+                const int t = (lane + 32 * i) / KS, c = (lane + 32 * i) % KS, h = 32 * i / KS / 16;     // (a step stays in one 16)
                 const uint32_t at = dst + piece_at<SUB, C::CHB>(t, c);
                 cp_async16(at, kc[h] + (t & 15) * P.kv_stride[2] + 16 * c, pol);
                 cp_async16(at + C::UNIT, vc[h] + (t & 15) * P.kv_stride[5] + 16 * c, pol);
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
             int pg = page[0], at = tok[0] + t;
 #pragma unroll
             for (int h = 1; h < NS; ++h)
-                if (P.halves && t >= 16 * h) {
+                if (P.pieces && t >= 16 * h) {
                     pg = page[h];
                     at = tok[h] + t - 16 * h;
                 }
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(TCfg8<D, MODE, NBQ == 0>::NW * 32, per_sm(MODE
             cp_async4(s_base + C::OFF_SC + (warp * ST + st) * 2 * C::SCB + (lane < SUB / 4 ? 0 : C::SCB) + t,
                       (lane < SUB / 4 ? P.k_scale : P.v_scale) + so);
         }
-        if (P.halves || lane < SC_LANES) cp_async_arrive(b);
+        if (P.pieces || lane < SC_LANES) cp_async_arrive(b);
         ++kp;
     };
 #pragma unroll 1
