@@ -46,7 +46,8 @@ __host__ __device__ constexpr int sub8(int D, int mode) {
     return D > 128 ? 16 : D == 64 && (mode == TK_CTA || mode == TK_CTA_HALF) ? 64 : 32;
 }
 // Warps per SM: 192 KB of ring, 3 stages each (4 at D = 192). 12 warps of 2 stages: one cache of 131k tokens 49.7 us against
-// 48.0, 4 rows on 20-32k tokens 90 against 63 (registers).
+// 48.0, 4 rows on 20-32k tokens 90 against 63 (registers). At D = 64 units of 32 tokens have 16 warps of 3 stages: 64 ragged sequences
+// 57 us, 600 x 1-1000 tokens 39; with 8 of 6 stages 69 and 48, with 12 of 4 57 and 40.
 __host__ __device__ constexpr int warps_sm8(int D, int mode) { return D == 64 && sub8(D, mode) == 32 ? 16 : 8; }
 
 template <int D, int MODE, bool QUAD>
@@ -794,7 +795,8 @@ cudaError_t launch8_t(PagedAttn& p, cudaStream_t st) {
         cfg.gridDim = dim3((ranges * p.cols + 7) / 8);
         return cudaLaunchKernelEx(&cfg, paged_token8_join_kernel<D>, p, ranges);
     }
-    // few items, each in many pieces: a CTA per (range, column), its threads over the pieces
+    // few items, each in many pieces: a CTA per (range, column), its threads over the pieces (one cache of 131k tokens 48.4 us, with a
+    // warp per range and column 51.2; 2000 tokens 10.8 against 11.4)
     cfg.gridDim = dim3(p.n_ctas, p.cols, 1);
     return p.dtype == PCK_DT_F16 ? cudaLaunchKernelEx(&cfg, paged_token_join_kernel<__half, D>, p)
                                  : cudaLaunchKernelEx(&cfg, paged_token_join_kernel<__nv_bfloat16, D>, p);
