@@ -199,3 +199,18 @@ def test_a_dominant_token_leaves_the_others_their_bits(ctx, dtype):   # noqa: F8
                 tol = (ref.HALF_STEP[dtype] + 2 * want[2][..., None] + 2.0 ** -18) * want[0] + torch.finfo(dtype).smallest_normal
                 assert ((O.double() - want[0]).abs() <= tol).all(), f"{down}"
     ctx.sync()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,H_kv,P", [(64, 2, 64), (64, 2, 16), (128, 2, 32), (256, 1, 16)])
+def test_long_windows(ctx, dtype, D, H_kv, P):   # noqa: F811
+    """Windows longer than a CTA takes whole, with sinks that end inside a page, at caches shorter and longer than they are."""
+    lens = [9000, 4000, 20, 5071]
+    pg = r8.Pages8(6, lens, H_kv, D, P)
+    for news in ([1] * 4, [2, 1, 2, 2]):
+        Q = _rand(3, sum(news), 2 * H_kv, D, dtype=dtype)
+        for W, sinks in ((3000, 0), (5000, 70), (4097, 33), (65, 4000)):
+            O, L = ctx.paged_attend(pg.cache(), pg.table, pg.lens, Q, cu_rows=None if max(news) == 1 else _cu(news), max_rows=max(news),
+                                    window=W, sinks=sinks)
+            ref.check_attend(O, L, r8.attend(pg, lens, news, Q, window=W, sinks=sinks), dtype, PAIR, f"{W} {sinks}")
+    ctx.sync()
