@@ -107,9 +107,11 @@ __global__ void __launch_bounds__(NR_THREADS, A8_BLOCKS) append8_kernel(const __
 #pragma unroll 1
     for (int i = 0; i < DEPTH; ++i) fetch();
     RowPlace at = {};
-    if (!place_row<TI, L>(P, t, lane, mask, h0, at)) return;
     float co[8], si[8];
-    if (P.R > 0 && !load_angles(P, t, lane, at.pos, rot, s0, s1, co, si)) return;
+    if (!place_row<TI, L>(P, t, lane, mask, h0, at) || (P.R > 0 && !load_angles(P, t, lane, at.pos, rot, s0, s1, co, si))) {
+        asm volatile("cp.async.wait_all;" ::: "memory");         // the copies land before the block can end
+        return;
+    }
 
     // KIND 0: q, 1: k, 2: v. The heads of all kinds one behind the other are dealt to the token's subwarps in turn.
     const auto heads = [&](auto kind, const RowsArg& A, int first) {
