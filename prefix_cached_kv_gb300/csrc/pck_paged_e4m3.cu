@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(NR_THREADS, A8_BLOCKS) append8_kernel(const __
     if (t64 >= P.T) return;
     const int t = static_cast<int>(t64), h0 = sub % P.spt;
     if (h0 >= P.q.H + P.k.H + P.v.H) return;
+    // rows in front of the first sequence and behind the last are not read: they need not exist
+    const bool owned = !P.cu_rows || (t >= P.cu_rows[0] && t < P.cu_rows[P.B]);
     const bool active = lane < P.D / 16;
     const int rv = P.R / 16;
     const bool rot = lane < rv;
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(NR_THREADS, A8_BLOCKS) append8_kernel(const __
     __shared__ __align__(16) Raw ring[NR_THREADS / 32][DEPTH][2][32];
     Raw(*mine)[2][32] = ring[threadIdx.x >> 5];
     const int in_warp = threadIdx.x & 31, Hqk = P.q.H + P.k.H, Ht = Hqk + P.v.H;
-    int next = h0, put = 0, get = 0;
+    int next = owned ? h0 : Ht, put = 0, get = 0;
     const auto fetch = [&]() {
         if (next < Ht && active) {
             const RowsArg& A = next < P.q.H ? P.q : next < Hqk ? P.k : P.v;

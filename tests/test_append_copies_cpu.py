@@ -33,3 +33,14 @@ def test_no_return_leaves_copies_in_flight():
         assert "cp.async.wait_all;" in after[:at].rsplit("{", 1)[-1], after[max(0, at - 120):at + 7]
     # and the loop over the heads waits for every head that was asked for before it uses it
     assert re.search(r'cp\.async\.wait_group %0;" ::"n"\(DEPTH - 1\)', after)
+
+
+def test_no_row_is_read_before_it_is_known_to_be_a_sequences():
+    """Rows in front of the first sequence and behind the last are neither read nor written: they need not exist."""
+    body = _kernel()
+    before = body[:_started(body)]
+    m = re.search(r"const bool owned = !P\.cu_rows \|\| \(t >= P\.cu_rows\[0\] && t < P\.cu_rows\[P\.B\]\);", before)
+    assert m, "a row's copies begin before it is known to be a sequence's"
+    assert "A.in" not in before[:m.start()]
+    # the copies of the thread's n-th head are those of head next, which starts behind the last head where the row is no one's
+    assert re.search(r"int next = owned \? h0 : Ht\b", before) and re.search(r"if \(next < Ht && active\)", before)
