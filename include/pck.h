@@ -427,7 +427,8 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
  * never writes) counts as 0.
  * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: at most
  * as many as the cache has, at most max_pages per sequence, with a window only those that it reaches. bf16 holds the values
- * exactly, fp16 those within its range. */
+ * exactly. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one above 65,536 that a row
+ * sees makes the call's results invalid (pck_sync reports PCK_ECUDA with code 16): such a cache takes a bf16 q. */
 int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,
                           const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
                           const float *O_prior, const float *LSE_prior, void *O, float *LSE,

@@ -750,7 +750,8 @@ class Context:
         """Attention of Q [T, H_q, D] over the cached tokens of its sequences (see pck_paged_attend); prior: (O, LSE)
         of the same rows over other keys, fp32, merged in. max_rows bounds the rows of a sequence (default: T with
         cu_rows, else 1). Outputs and the workspace are allocated when not given; over a QuantizedPagedCache O is of
-        Q's type, fp16 or bf16. Returns (O, LSE)."""
+        Q's type, fp16 or bf16 (more than a few rows of a sequence see its values in that type: one above 65,536 under an
+        fp16 Q is reported by sync). Returns (O, LSE)."""
         if Q.dim() != 3 or Q.shape[2] != cache.D:
             raise ValueError(f"Q must be [T, H_q, {cache.D}]")
         T, H_q, _ = shape = Q.shape

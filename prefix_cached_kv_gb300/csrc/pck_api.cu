@@ -1187,9 +1187,10 @@ int pck_sync(pck_ctx* c, void* stream) {
         cudaMemset(c->dev_err, 0, sizeof(int));
         cudaMemset(c->counters, 0, WS_COUNTERS * sizeof(int));
         cudaDeviceSynchronize();
-        if (herr >= ERR_PAGE_ID && herr <= ERR_KV_LEN)
+        if ((herr >= ERR_PAGE_ID && herr <= ERR_KV_LEN) || herr == ERR_FP16_RANGE)
             return fail(c, PCK_ECUDA, "a value on the device is out of range (code %d: %s); results of the affected calls are invalid",
-                        herr, herr == ERR_PAGE_ID ? "page number" : herr == ERR_ROPE_POS ? "rotary position" : "cache length or row count");
+                        herr, herr == ERR_PAGE_ID ? "page number" : herr == ERR_ROPE_POS ? "rotary position"
+                        : herr == ERR_KV_LEN ? "cache length or row count" : "a quantised cache's value beyond fp16, for rows with an fp16 q");
         return fail(c, PCK_ECUDA, "a device wait gave up (code %d); results of the affected calls are invalid", herr);
     }
     return PCK_OK;

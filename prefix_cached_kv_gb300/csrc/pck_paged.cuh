@@ -26,6 +26,7 @@ constexpr int ERR_ROWS_LOAD = 12;    // row attention: producer, MMA warp, softm
 constexpr int ERR_ROWS_MMA = 13;
 constexpr int ERR_ROWS_SOFTMAX = 14;
 constexpr int ERR_ROWS_O = 15;
+constexpr int ERR_FP16_RANGE = 16;   // row attention over a quantised cache with an fp16 q: a value that fp16 cannot hold
 
 constexpr float PG_LN2 = 0.69314718055994530942f;
 constexpr float PG_LOG2E = 1.4426950408889634074f;
