@@ -425,8 +425,11 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
  * scores and to the weights, in fp32. Weights times their V scale are held as fp16 pairs, to 2^-37 of a head's largest (so V rows all
  * of whose scales are below 2^-50 lose bits); a bf16 q to 2^-39 of the row's largest element; a scale of 2^-127 (byte 0, which an append
  * never writes) counts as 0.
- * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: at most
- * as many as the cache has, at most max_pages per sequence, with a window only those that it reaches. bf16 holds the values
+ * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: as many as
+ * max_pages and B name (with a window only those that it reaches), at most as many as the cache has. Where these would
+ * take more than 4 GiB and more than half of the codes' bytes, the call goes through its kv heads, and then its sequences, some at a
+ * time, down to one sequence's pages of one kv head. So the peak is the codes and half of them again (or 4 GiB), and a table no
+ * wider than its sequences need keeps the workspace small and the call whole. bf16 holds the values
  * exactly. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one above 65,536 that a row
  * sees makes the call's results invalid (pck_sync reports PCK_ECUDA with code 16): such a cache takes a bf16 q. */
 int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,

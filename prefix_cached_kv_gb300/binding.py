@@ -751,7 +751,7 @@ class Context:
         of the same rows over other keys, fp32, merged in. max_rows bounds the rows of a sequence (default: T with
         cu_rows, else 1). Outputs and the workspace are allocated when not given; over a QuantizedPagedCache O is of
         Q's type, fp16 or bf16 (more than a few rows of a sequence see its values in that type: one above 65,536 under an
-        fp16 Q is reported by sync). Returns (O, LSE)."""
+        fp16 Q is reported by sync; their workspace is sized by the table's width, see pck_paged_attend_e4m3). Returns (O, LSE)."""
         if Q.dim() != 3 or Q.shape[2] != cache.D:
             raise ValueError(f"Q must be [T, H_q, {cache.D}]")
         T, H_q, _ = shape = Q.shape

@@ -93,6 +93,7 @@ struct PagedAttn {
     int pieces;                      // its pages are no multiples of a unit: loaded 16 tokens at a time, by the lanes
     // row kernel
     int n_split, row_tiles, box;     // key splits, row tiles of the grid, tokens of a TMA box
+    int row_heads;                   // heads of a row of O, LSE and the priors: H_q, or more where a call takes some kv heads at a time
     const void *k_base, *v_base;
     int64_t kv_stride[6];            // k page, head, token; v page, head, token (elements)
 };

@@ -313,7 +313,8 @@ int check_attend_rows(pck_ctx* c, int T, int H_q, const void* Q, int64_t q_row, 
     return PCK_OK;
 }
 
-int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, const void* Q, int64_t q_row,
+// row_heads: heads of a row of O, LSE and the priors, of which the call's H_q are neighbours (tiled rows only: else H_q).
+int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* batch, int H_q, int row_heads, const void* Q, int64_t q_row,
                int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O, float* LSE,
                void* workspace, size_t workspace_bytes, void* stream) {
     PagedAttn p = {};
@@ -328,6 +329,7 @@ int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* 
     if (workspace_bytes < need || (need && !workspace))
         return ctx_fail(c, PCK_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     attend_args(p, v, batch, D, Q, q_row, q_head, O_prior, LSE_prior, O, LSE, workspace);
+    p.row_heads = row_heads;
     p.k_base = cache->K;
     p.v_base = cache->V;
     const int64_t strides[6] = {cache->k_page, cache->k_head, cache->k_token, cache->v_page, cache->v_head, cache->v_token};
@@ -343,21 +345,38 @@ int attend_run(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_batch* 
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = ragged ? launch_paged_rows(p, D, st) : launch_paged_token(p, D, st);
     if (e != cudaSuccess) return ctx_fail(c, PCK_ECUDA, "launch: %s", cudaGetErrorString(e));
-    ctx_count_query(c);
     return PCK_OK;
 }
 
-// Attention over a quantised cache. One row of a sequence, or a few: over the codes. More: through 16-bit pages: what the rows see is read back into pages of the workspace (of Q's
-// type, in the order of the sequences or, where the tables are wide, at their own numbers), and those are attended to.
+// Attention over a quantised cache. One row of a sequence, or a few: over the codes. More: through 16-bit pages: what the rows see is read back
+// into pages of the workspace (of Q's type, in the order of the sequences or, where the tables are wide, at their own numbers), and those
+// are attended to.
+// The tables' width, which is all that the host knows, may name far more pages than the rows see. So a call whose pages could take more
+// than EXPAND_BYTES, or half of the cache's codes where that is more, goes through its kv heads some at a time, and through its sequences
+// where one head's pages are still too many: a large cache and the workspace together stay below the bytes of a 16-bit cache. A part costs its
+// launches and a wave that it may not fill: 24 prompts of 300 tokens (32 / 8 heads of 128) in tables of 131k tokens over 6.1 GiB of codes
+// take 126 us in 4 parts with 3 GiB, 86 in one with 12 GiB, 179 in 8 with 1.5 GiB (a quarter of the codes).
+constexpr int64_t EXPAND_BYTES = int64_t(4) << 30;
+
 struct Expanded {
     PagedAttn p;                     // over the codes: its shape
     bool direct;
-    pck_paged_cache cache;           // of the workspace; K and V are set by the call
-    pck_paged_batch batch;           // its table is the workspace's page map
+    int heads, seqs;                 // kv heads and sequences of a part: all of them, or fewer
+    pck_paged_cache cache;           // a part's pages in the workspace (of `heads` kv heads); K and V are set by the call
     int slots;                       // pages of a sequence
-    bool by_page;                    // as many pages as the cache has: fewer than the sequences' tables could name
+    bool by_page;                    // as many pages as the cache has: fewer than a part's tables could name
     size_t off_v, off_map, off_inner, total;    // workspace: K, V, page map, the attention's own
 };
+
+// A part of a call: sequences from b0 on.
+pck_paged_batch part_of(const pck_paged_batch* b, int b0, int seqs) {
+    pck_paged_batch x = *b;
+    x.B = seqs;
+    x.cu_rows += b0;                 // (tiled rows have them)
+    x.kv_len += b0;
+    x.table += (int64_t)b0 * b->max_pages;
+    return x;
+}
 
 int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batch* b, int q_dtype, int H_q, int window, int sinks, Expanded& x) {
     x = Expanded{};
@@ -371,29 +390,53 @@ int expand_shape(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batc
     void* const some = reinterpret_cast<void*>(256);                     // stands for the workspace
     x.cache = pck_paged_cache{some, some, q_dtype, k->H_kv, k->D, k->page_size, k->n_pages,
                               k->H_kv * page * k->D, page * k->D, k->D, k->H_kv * page * k->D, page * k->D, k->D};
-    x.batch = *b;
     if ((rc = attend_shape(c, &x.cache, b, H_q, window, sinks, x.p)) != PCK_OK) return rc;
     if (x.p.B == 0 || x.p.T == 0) return PCK_OK;
     x.direct = !tiled_rows(x.p, k->D);
+    const int sms = ctx_view(c).sms;
     if (x.direct) {
-        x.total = paged_token_e4m3_plan(x.p, k->D, ctx_view(c).sms);
+        x.total = paged_token_e4m3_plan(x.p, k->D, sms);
         return PCK_OK;
     }
     int64_t slots = b->max_pages;
     if (window > 0) {
-        const int64_t rows = b->cu_rows ? (b->max_rows < b->T ? b->max_rows : b->T) : 1;
+        const int64_t rows = b->max_rows < b->T ? b->max_rows : b->T;
         const int64_t some = (sinks + page - 1) / page + (window + rows) / page + 2;
         if (some < slots) slots = some;
     }
-    x.by_page = k->n_pages < b->B * slots;
-    const int64_t pages = x.by_page ? k->n_pages : b->B * slots;
+    const int64_t one = page * k->D * 4;                                 // bytes of a page of one kv head, K and V
+    const auto pages_of = [&](int64_t seqs) { return k->n_pages < seqs * slots ? k->n_pages : seqs * slots; };
+    const int64_t half = k->n_pages * k->H_kv * page * k->D, budget = half > EXPAND_BYTES ? half : EXPAND_BYTES;
+    // as many as the budget holds, at least one, and the parts as even as they come
+    const auto even = [](int n, int64_t most) {
+        const int64_t m = most < 1 ? 1 : most > n ? n : most, parts = (n + m - 1) / m;
+        return static_cast<int>((n + parts - 1) / parts);
+    };
+    x.heads = even(k->H_kv, budget / (pages_of(b->B) * one));
+    x.seqs = pages_of(b->B) * one <= budget ? b->B : even(b->B, budget / (slots * one));
+    x.by_page = k->n_pages < x.seqs * slots;
     x.slots = static_cast<int>(slots);
-    x.cache.n_pages = pages;
-    const size_t side = (size_t)pages * k->H_kv * page * k->D * 2;       // a multiple of 512 bytes
+    const int64_t pages = pages_of(x.seqs), H = x.heads;
+    x.cache = pck_paged_cache{some, some, q_dtype, x.heads, k->D, k->page_size, pages,
+                              H * page * k->D, page * k->D, k->D, H * page * k->D, page * k->D, k->D};
+    const size_t side = (size_t)pages * H * page * k->D * 2;             // a multiple of 512 bytes
     x.off_v = side;
     x.off_map = 2 * side;
-    x.off_inner = x.off_map + (((size_t)b->B * b->max_pages * 4 + 255) & ~size_t(255));
-    x.total = x.off_inner + paged_rows_plan(x.p, k->D, ctx_view(c).sms);
+    x.off_inner = x.off_map + (((size_t)x.seqs * b->max_pages * 4 + 255) & ~size_t(255));
+    // the attention's own: the most that a part takes (the last ones may be smaller, and are then split further)
+    size_t inner = 0;
+    const int G = H_q / k->H_kv, last_h = k->H_kv - (k->H_kv - 1) / x.heads * x.heads, last_b = b->B - (b->B - 1) / x.seqs * x.seqs;
+    for (const int nh : {x.heads, last_h})
+        for (const int nb : {x.seqs, last_b}) {
+            PagedAttn p = {};
+            pck_paged_cache part = x.cache;
+            part.H_kv = nh;
+            const pck_paged_batch pb = part_of(b, 0, nb);
+            if ((rc = attend_shape(c, &part, &pb, nh * G, window, sinks, p)) != PCK_OK) return rc;
+            const size_t need = paged_rows_plan(p, k->D, sms);
+            if (need > inner) inner = need;
+        }
+    x.total = x.off_inner + inner;
     return PCK_OK;
 }
 
@@ -408,7 +451,7 @@ void read_params(pck_ctx* c, const pck_paged_cache_e4m3* k, const pck_paged_batc
     p.v_page = k->v_page;
     p.v_head = k->v_head;
     p.v_token = k->v_token;
-    p.H = k->H_kv;
+    p.H = p.scale_heads = k->H_kv;
     p.D = k->D;
     p.page = k->page_size;
     p.n_pages = k->n_pages;
@@ -493,7 +536,9 @@ int pck_paged_attend(pck_ctx* c, const pck_paged_cache* cache, const pck_paged_b
                      int64_t q_head, int window, int sinks, const float* O_prior, const float* LSE_prior, void* O, float* LSE,
                      void* workspace, size_t workspace_bytes, void* stream) {
     if (!c) return PCK_EINVAL;
-    return attend_run(c, cache, batch, H_q, Q, q_row, q_head, window, sinks, O_prior, LSE_prior, O, LSE, workspace, workspace_bytes, stream);
+    const int rc = attend_run(c, cache, batch, H_q, H_q, Q, q_row, q_head, window, sinks, O_prior, LSE_prior, O, LSE, workspace, workspace_bytes, stream);
+    if (rc == PCK_OK && batch->B > 0 && batch->T > 0) ctx_count_query(c);
+    return rc;
 }
 
 int pck_paged_workspace_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int q_dtype, int H_q, int window,
@@ -541,21 +586,43 @@ int pck_paged_attend_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const p
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     x.cache.K = ws;
     x.cache.V = ws + x.off_v;
-    x.batch.table = reinterpret_cast<int32_t*>(ws + x.off_map);
-    ReadParams p = {};
-    read_params(c, cache, batch, p);
-    p.max_rows = batch->cu_rows ? (batch->max_rows < batch->T ? batch->max_rows : batch->T) : 1;
-    p.Ko = x.cache.K;
-    p.Vo = x.cache.V;
-    p.pages = 1;
-    p.slots = x.slots;
-    p.by_page = x.by_page;
-    p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
-    p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
-    p.page_map = reinterpret_cast<int32_t*>(ws + x.off_map);
-    if ((rc = run_read(c, p, q_dtype, stream)) != PCK_OK) return rc;
-    return attend_run(c, &x.cache, &x.batch, H_q, Q, q_row, q_head, window, sinks, O_prior, LSE_prior, O, LSE, ws + x.off_inner,
-                      workspace_bytes - x.off_inner, stream);
+    int32_t* const map = reinterpret_cast<int32_t*>(ws + x.off_map);
+    const int64_t D = cache->D, G = H_q / cache->H_kv;
+    for (int b0 = 0; b0 < batch->B; b0 += x.seqs) {
+        pck_paged_batch part = part_of(batch, b0, batch->B - b0 < x.seqs ? batch->B - b0 : x.seqs);
+        for (int h0 = 0; h0 < cache->H_kv; h0 += x.heads) {
+            const int nh = cache->H_kv - h0 < x.heads ? cache->H_kv - h0 : x.heads;
+            ReadParams p = {};
+            read_params(c, cache, &part, p);
+            p.K += h0 * cache->k_head;
+            p.V += h0 * cache->v_head;
+            p.k_scale += (int64_t)h0 * p.page;
+            p.v_scale += (int64_t)h0 * p.page;
+            p.H = nh;
+            p.max_rows = batch->max_rows < batch->T ? batch->max_rows : batch->T;
+            p.Ko = x.cache.K;
+            p.Vo = x.cache.V;
+            p.pages = 1;
+            p.slots = x.slots;
+            p.by_page = x.by_page;
+            p.window = window < MAX_TOKENS ? window : MAX_TOKENS;
+            p.sinks = sinks < MAX_TOKENS ? sinks : MAX_TOKENS;
+            p.page_map = map;
+            if ((rc = run_read(c, p, q_dtype, stream)) != PCK_OK) return rc;
+            pck_paged_cache pages = x.cache;
+            pages.H_kv = nh;
+            pages.k_page = pages.v_page = nh * pages.k_head;
+            pck_paged_batch mapped = part;
+            mapped.table = map;
+            const int64_t head = h0 * G;                 // the part's first q head
+            if ((rc = attend_run(c, &pages, &mapped, static_cast<int>(nh * G), H_q, static_cast<const uint8_t*>(Q) + head * q_head * 2, q_row, q_head,
+                                 window, sinks, O_prior ? O_prior + head * D : nullptr, LSE_prior ? LSE_prior + head : nullptr,
+                                 static_cast<uint8_t*>(O) + head * D * 2, LSE ? LSE + head : nullptr, ws + x.off_inner,
+                                 workspace_bytes - x.off_inner, stream)) != PCK_OK) return rc;
+        }
+    }
+    ctx_count_query(c);
+    return PCK_OK;
 }
 
 int pck_paged_read_e4m3(pck_ctx* c, const pck_paged_cache_e4m3* cache, const pck_paged_batch* batch, int dtype, const pck_rows* K,

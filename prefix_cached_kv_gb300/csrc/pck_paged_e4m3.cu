@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(RD_THREADS, rd_blocks(DEPTH)) paged_read_kerne
         const int64_t ors = P.pages ? P.D : P.ko_row, vrs = P.pages ? P.D : P.vo_row;
         const uint8_t* kc = P.K + pg * P.k_page + h * P.k_head + slot * P.k_token;
         const uint8_t* vc = P.V + pg * P.v_page + h * P.v_head + slot * P.v_token;
-        const int64_t sc = (pg * P.H + h) * P.page + slot;
+        const int64_t sc = (pg * P.scale_heads + h) * P.page + slot;
         const uint32_t scale = tok >= 0 ? (lane < 16 ? P.k_scale : P.v_scale)[sc + (lane & 15)] : 0;    // of token lane % 16
         if constexpr (std::is_same<TO, __half>::value) {
             // Attention would take 65,504 for what fp16 cannot hold: reported. Only rows whose scale allows it are looked at (448 * 2^7 is

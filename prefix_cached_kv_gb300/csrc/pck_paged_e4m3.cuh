@@ -38,6 +38,7 @@ struct ReadParams {
     const uint8_t *k_scale, *v_scale;
     int64_t k_page, k_head, k_token, v_page, v_head, v_token;
     int H, D, page, max_pages, B, T;
+    int scale_heads;                 // heads of a page's scales (H, or more where a call takes some kv heads at a time)
     int64_t n_pages;
     const int32_t* cu_rows;
     const int32_t* kv_len;

@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(RW_THREADS, 1) paged_rows_kernel(const __grid_
                 // the record of spoilt keys is complete
                 asm volatile("barrier.cta.sync %0, 192;" ::"r"(1 + t) : "memory");
                 if (!failed) {
-                    const int row = static_cast<int>(trow * P.H_q + hq);      // (T H_q < 2^31)
+                    const int row = static_cast<int>(trow * P.row_heads + hq);      // (T row_heads < 2^31)
                     const bool direct = P.n_split == 1;
                     RowEnd e = {1.f, 0.f, 0.f, false};
                     if (direct && row_ok) e = row_end(P, row, m, l);
@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(RW_M) paged_rows_join_kernel(const __grid_cons
     const int rtok = t * tpt + r / P.G;
     const int64_t trow = (int64_t)rt.row0 + rt.tok0 + rtok;
     if (r >= tpt * P.G || rtok >= min(rt.n - rt.tok0, tt) || trow < 0 || trow >= P.T) return;
-    const int64_t row = trow * P.H_q + g * P.G + r % P.G;
+    const int64_t row = trow * P.row_heads + g * P.G + r % P.G;
     auto part = [&](int s) { return P.ws + ((size_t)tile_idx * P.H_kv * P.n_split + (size_t)s * P.H_kv + g) * rows_partial_floats(D); };
     float M = -INFINITY, L = 0.f;
 #pragma unroll 4
