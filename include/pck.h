@@ -422,9 +422,9 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
 /* pck_paged_attend over the values of a quantised cache: rows, window, sinks, priors, outputs and limits as there. q_dtype: of
  * Q and O, F16 or BF16.
  * One row per sequence, or a few (as there): the codes are multiplied as they are, exactly, and the scales applied to the
- * scores and to the weights, in fp32. Weights times their V scale are held as fp16 pairs, to 2^-37 of a head's largest (so V rows all
- * of whose scales are below 2^-50 lose bits); a bf16 q to 2^-39 of the row's largest element; a scale of 2^-127 (byte 0, which an append
- * never writes) counts as 0.
+ * scores and to the weights, in fp32. Weights times their V scale are held as fp16 pairs, to 22 bits and to 2^-37 of a head's
+ * largest; where the token with the largest has a V scale of 2^(-40 - b), to 2^(-37 + b) of it (below 2^-77 nothing is left). A bf16 q
+ * is held to 2^-39 of the row's largest element; a scale of 2^-127 (byte 0, which an append never writes) counts as 0.
  * More rows: what they see is first read back, as by pck_paged_read_e4m3, into 16-bit pages of q_dtype in the workspace: as many as
  * max_pages and B name (with a window only those that it reaches), at most as many as the cache has. Where these would
  * take more than 4 GiB and more than half of the codes' bytes, the call goes through its kv heads, and then its sequences, some at a

@@ -17,9 +17,10 @@
 //    of an MMA whose rows are elements in that order. One conversion makes two fp16 values.
 //  * q: fp16 as it is; a bf16 row is moved by a power of two so that its largest element is 2^14 .. 2^15 and then exact in fp16
 //    but for elements 2^-29 of that one and less, which are held to 2^-39 of it.
-//  * Weights: w = 2^(s - m) 2^ev enters the second MMA as an fp16 pair hi + lo, held to 2^-37 of the largest one. m stands so that
-//    the largest of s + ev (a token's largest share of O) is TOP, and moves only when a weight passes W_TOP: that is seen on
-//    the weights themselves, not on the scores. ev counts from EV_LOW up in m, which keeps l within fp32.
+//  * Weights: w = 2^(s - m) 2^ev enters the second MMA as an fp16 pair hi + lo, held to 22 bits or to 2^-25, whichever is more. m stands
+//    so that the largest of s + ev (a token's largest share of O) is TOP, and moves only when a weight passes W_TOP: that is seen on
+//    the weights themselves, not on the scores. So a weight is held to 2^-37 of the largest one. ev counts from EV_LOW up in m, which
+//    keeps l within fp32: where the token that counts most has a V scale 2^-b below 2^EV_LOW, the largest weight is 2^(TOP - b).
 //  * Up to 4 columns (4 q heads per kv head): the weights' lo parts take columns 4-7 of the MMA's 8, one MMA instead of two.
 // Measured (graph replays): one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 47.6 us, 5.7 TB/s; 16 caches of 30-65k
 // tokens (2 kv heads of 256) 125 us, 6.0 TB/s; 64 ragged sequences (8 kv heads of 64, prior) 57 us, 4.1 TB/s; 32 windows of up to
@@ -33,7 +34,7 @@
 namespace pck {
 namespace {
 
-constexpr float EV_LOW = -40.f;      // values of V below 2^-40 * 448 lose bits where no larger ones are seen
+constexpr float EV_LOW = -40.f;      // weights of V scales of 2^(-40 - b) are held to 2^(-37 + b) of the largest
 constexpr float M_NONE = -1e30f;     // m before a visible key: finite, so that a hidden one's 2^(-inf - m) is 0
 constexpr float W_TOP = 61440.f, L_TOP = 1e30f;      // the largest weight (fp16 ends at 65,504), and sum of a unit's p
 // What an item costs beside its units, in units (as tk_item_units). Ranges per half CTA, 24 x 1-4000 tokens: 19.3 us with 12, 19.4 with 16, 21.9
