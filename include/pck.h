@@ -414,7 +414,8 @@ typedef struct pck_paged_cache_e4m3 {
 /* pck_paged_append into a quantised cache. dtype: of Q, K and V, F32, F16 or BF16. A head row y (K normed and rotated in fp32, V as
  * it is) whose largest finite magnitude is a gets the least e with a 2^-e <= 448, held to -126 .. 120 (a row of zeros: -126), and
  * the codes y 2^-e rounded to nearest even: one rounding, of half a step 2^-4 of the value, or 2^-10 * 2^e where that is
- * more. Infinities and NaN become NaN. */
+ * more. Infinities and NaN become NaN. A row whose largest magnitude is 2^128 (1 - 2^-5) or more, the last 2^-5 below fp32's end,
+ * has a code that stands for 2^128: an infinity in fp32 and bf16. */
 int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int dtype,
                           const pck_rows *Q, const pck_rows *K, const pck_rows *V, int norm, float eps,
                           const pck_rotary *rope, void *stream);
@@ -430,7 +431,7 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
  * take more than 4 GiB and more than half of the codes' bytes, the call goes through its kv heads, and then its sequences, some at a
  * time, down to one sequence's pages of one kv head. So the peak is the codes and half of them again (or 4 GiB), and a table no
  * wider than its sequences need keeps the workspace small and the call whole. bf16 holds the values
- * exactly. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one above 65,536 that a row
+ * as far as pck_paged_read_e4m3 says. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one above 65,536 that a row
  * sees makes the call's results invalid (pck_sync reports PCK_ECUDA with code 16): such a cache takes a bf16 q. */
 int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,
                           const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
@@ -443,8 +444,9 @@ int pck_paged_workspace_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, co
 
 /* Rows of a quantised cache read back: each sequence's last cached tokens (its rows, as in pck_paged_batch; cu_rows from
  * kv_len takes whole caches), K->out and V->out [T, H_kv, D] of dtype F32, F16 or BF16 with the strides given (in and weight are
- * not used): [H_kv, N, D], as pck_store takes it, is a row stride of D. Values are rounded once (fp32 and bf16
- * hold them exactly; in fp16 what is beyond 65,504 is 65,504). Rows at a negative cache position are 0. */
+ * not used): [H_kv, N, D], as pck_store takes it, is a row stride of D. Values are rounded once. fp32 holds
+ * them exactly, bf16 those of scales 2^-124 .. 2^119 (below, codes end under its smallest step, 2^-133); in both, a value of 2^128
+ * and more, which codes of 256 and above have at 2^120, is an infinity. In fp16 what is beyond 65,504 is 65,504. Rows at a negative cache position are 0. */
 int pck_paged_read_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int dtype,
                         const pck_rows *K, const pck_rows *V, void *stream);
 

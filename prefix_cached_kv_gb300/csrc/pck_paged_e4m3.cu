@@ -9,8 +9,8 @@
 // ragged prompts, 32 + 8 + 8 heads of 128: 61.5 us as the 16-bit kernel with another store (two heads in registers, 65 % of the issue slots),
 // 61.4 with a loop per kind and packed arithmetic, 51 with the copies, at three blocks an SM; four blocks spill (62), two 57.
 //
-// Reading back: out = code * 2^e, rounded once to the output's type (fp32 and bf16 hold it exactly; in fp16 what is beyond
-// 65,504 becomes 65,504). D + 1 bytes in and 2 D or 4 D out per row, so HBM bounds it. A warp takes tiles of 16 tokens of one kv
+// Reading back: out = code * 2^e, rounded once to the output's type (fp32 holds it exactly below 2^128, bf16 for e of -124 .. 119; in fp16
+// what is beyond 65,504 becomes 65,504). D + 1 bytes in and 2 D or 4 D out per row, so HBM bounds it. A warp takes tiles of 16 tokens of one kv
 // head, K and V: 8 codes a lane, so that its 16-byte stores lie side by side, with DEPTH loads of K and of V in flight before the
 // first is used: 6.1 TB/s read and written on the long sessions (0.90 of a copy).
 // The tiles of all sequences laid end to end are dealt to the warps from the lengths on the device (one block scan), so
