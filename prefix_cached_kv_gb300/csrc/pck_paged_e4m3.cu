@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(RD_THREADS, rd_blocks(DEPTH)) paged_read_kerne
         if (tid == RD_THREADS - 1) pre[P.B] = run;
         __syncthreads();
     }
-    const int64_t total = (int64_t)pre[P.B] * P.H, stride = (int64_t)gridDim.x * (RD_THREADS / 32);
+    // (rows that cu_rows names more than once, which is reported, take no more tiles than T rows can)
+    const int tiles = P.pages ? pre[P.B] : static_cast<int>(min((int64_t)pre[P.B], (int64_t)P.T / 16 + 2 * P.B));
+    const int64_t total = (int64_t)tiles * P.H, stride = (int64_t)gridDim.x * (RD_THREADS / 32);
     const int lpr = P.D / 8, pieces = 16 * lpr;       // pieces of 8 codes of a row, and of a tile
     const int t_lane = lane / lpr, c_lane = lane - t_lane * lpr, t_step = 32 / lpr, c_step = 32 - t_step * lpr;
     // Lane i looks up the warp's next tile but i at once: its head, tokens, page and place in the output.

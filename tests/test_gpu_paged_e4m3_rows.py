@@ -59,3 +59,27 @@ def test_append_beside_rows_left_out(ctx, dtype, B, H_q, H_kv, D, R):   # noqa: 
     for one, other in zip(*got):
         assert torch.equal(one, other)
     ctx.sync()
+
+
+def test_rows_that_cu_rows_names_again_and_again(ctx):   # noqa: F811
+    """A cu_rows that goes up to T and back to 0 for every sequence names 1024 T rows: reported, and no more work than T rows can be."""
+    T, B = 1 << 22, 2048
+    pg = r8.Pages8(2, [40] * 2, 1, 16, 16)
+    table, lens = pg.table[:1].expand(B, -1).contiguous(), torch.full((B,), 40, dtype=i32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=i32, device="cuda")
+    cu[1::2] = T
+    ctx.sync()
+    a, z = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    ctx.paged_read(pg.cache(), table, lens, T=T, cu_rows=cu)
+    z.record()
+    z.synchronize()
+    with pytest.raises(binding.PckError) as e:
+        ctx.sync()
+    assert "code 10" in str(e.value)
+    # T rows of 16 + 16 fp16 values: 268 MB. A thousand times as many would take a second.
+    assert a.elapsed_time(z) < 200
+    K, V = ctx.paged_read(pg.cache(), pg.table, pg.lens, T=80, cu_rows=torch.tensor([0, 40, 80], dtype=i32, device="cuda"))     # the next call is quiet
+    for got, x in zip((K, V), pg.kv()):
+        assert torch.equal(got[:40], x[pg.table[0].long()].transpose(1, 2).reshape(-1, 1, 16)[:40].half())
+    ctx.sync()
