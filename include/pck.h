@@ -378,7 +378,7 @@ int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
  * Scores, maxima, sums and O are held in fp32. The weights 2^(s - m) that multiply V are rounded: in the one-token
  * kernel to a pair of 16-bit values (22 bits in fp16, 16 in bf16; the output's own rounding is coarser), in the
  * row kernel once to the cache's type (11 bits, 8 in bf16; prompts of the kind measured then differ from 64 bits by
- * 1.3 times the output's own rounding). fp16 weights below 2^-37 (rows: 2^-31) of the largest one are lost.
+ * 1.3 times the output's own rounding in bf16, 1.4 times in fp16). fp16 weights below 2^-37 (rows: 2^-31) of the largest one are lost.
  * One row per sequence (cu_rows NULL), or a few (min(max_rows, T) * H_q / H_kv at most 16, 8 at D > 128): split
  * over the cache's length and joined; D in {64, 128, 192, 256}. More rows: tiles of 256 rows (tokens x
  * heads of a kv head) on the tensor cores, D in {64, 128}, H_q / H_kv at most 128. Other head dimensions, which an

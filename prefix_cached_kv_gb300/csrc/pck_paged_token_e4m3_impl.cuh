@@ -22,10 +22,12 @@
 //    the weights themselves, not on the scores. So a weight is held to 2^-37 of the largest one. ev counts from EV_LOW up in m, which
 //    keeps l within fp32: where the token that counts most has a V scale 2^-b below 2^EV_LOW, the largest weight is 2^(TOP - b).
 //  * Up to 4 columns (4 q heads per kv head): the weights' lo parts take columns 4-7 of the MMA's 8, one MMA instead of two.
-// Measured (graph replays): one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 47.6 us, 5.7 TB/s; 16 caches of 30-65k
+// Measured (graph replays): one cache of 131,071 tokens (8 kv heads of 128, 4 q heads each) 48-49 us, 5.5 TB/s; 16 caches of 30-65k
 // tokens (2 kv heads of 256) 125 us, 6.0 TB/s; 64 ragged sequences (8 kv heads of 64, prior) 57 us, 4.1 TB/s; 32 windows of up to
-// 2048 tokens (8 kv heads of 128, 8 q heads each) 32 us, 3.7 TB/s; 300 tokens 6.5 us. What is left: the start (lengths, page table and
-// first loads one after another, 5-8 us), the slowest range's end and the join (3-5 us); in between the loads run at 5.5-6.3 TB/s.
+// 2048 tokens (8 kv heads of 128, 8 q heads each) 32 us, 3.6 TB/s; 300 tokens 6.6 us; a few rows on four caches of 20-32k tokens
+// (8 kv heads of 128, 4 q heads each) 44 us with 2 rows, 57 with 4 (0.71 and 0.55 of HBM: two column blocks, hi and lo). What is
+// left: the start (lengths, page table and first loads one after another, 5-8 us), the slowest range's end and the join (3-5 us); in
+// between the loads run at 5.5-6.3 TB/s.
 #pragma once
 
 #include "pck_paged_e4m3.cuh"
