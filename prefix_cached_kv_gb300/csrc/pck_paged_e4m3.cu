@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(NR_THREADS, A8_BLOCKS) append8_kernel(const __
     for (int i = 0; i < DEPTH; ++i) fetch();
     RowPlace at = {};
     float co[8], si[8];
-    if (!place_row<TI, L>(P, t, lane, mask, h0, at) || (P.R > 0 && !load_angles(P, t, lane, at.pos, rot, s0, s1, co, si))) {
+    // (a cu_rows that makes no sense, which place_row reports, may place a row that is not owned)
+    if (!place_row<TI, L>(P, t, lane, mask, h0, at) || !owned || (P.R > 0 && !load_angles(P, t, lane, at.pos, rot, s0, s1, co, si))) {
         asm volatile("cp.async.wait_all;" ::: "memory");         // the copies land before the block can end
         return;
     }

@@ -83,3 +83,25 @@ def test_rows_that_cu_rows_names_again_and_again(ctx):   # noqa: F811
     for got, x in zip((K, V), pg.kv()):
         assert torch.equal(got[:40], x[pg.table[0].long()].transpose(1, 2).reshape(-1, 1, 16)[:40].half())
     ctx.sync()
+
+
+@pytest.mark.parametrize("cu,stored", [((3, 0, 9, 1, 9), []), ((4, 0, 9, 0, 9), []), ((0, 9, 2, 9, 4), [(0, 0, 31), (1, 0, 32)])])
+def test_rows_that_only_a_senseless_cu_rows_places(ctx, cu, stored):   # noqa: F811
+    """Reported; and a row outside [cu_rows[0], cu_rows[B]), which is not copied, is not stored where a descending cu_rows seems to
+    place it. stored: (row, sequence, position) of those that are."""
+    pg = ref.Pages(3, [40] * 4, 1, 16, 16, F16)            # its table
+    k, v, ks, vs = _empty_pages(int(pg.table.max()) + 2, 2, 16, 64)
+    x = _rand(4, 9, 4, 64, dtype=F16)
+    ctx.sync()
+    ctx.paged_append(binding.QuantizedPagedCache(k, v, ks, vs), pg.table, pg.lens, x[:, :2], x[:, 2:], cu_rows=torch.tensor(cu, dtype=i32, device="cuda"))
+    with pytest.raises(binding.PckError) as e:
+        ctx.sync()
+    assert "code 10" in str(e.value)
+    for t, b, p in stored:
+        at = (pg.table[b, p // 16].long(), slice(None), p % 16)
+        for codes, scale, y in ((k, ks, x[t, :2]), (v, vs, x[t, 2:])):
+            want, exp = r8.quantize(y)
+            assert torch.equal(scale[at].long() - 127, exp)
+            assert torch.equal(r8.values(_bits(codes)[at].view(r8.E4M3), torch.full_like(scale[at], 127)), want)
+            _bits(codes)[at], scale[at] = 0x55, 0x33
+    assert (_bits(k) == 0x55).all() and (_bits(v) == 0x55).all() and (ks == 0x33).all() and (vs == 0x33).all()
