@@ -311,7 +311,8 @@ typedef struct pck_paged_cache {
 } pck_paged_cache;
 
 /* The sequences of a call. Sequence b's rows are cu_rows[b] .. cu_rows[b+1]-1 of T (cu_rows
- * ascending; rows in front of the first sequence's or behind the last's are neither read nor written); they are the
+ * ascending; rows in front of the first sequence's or behind the last's are neither read nor written, but that attention's
+ * tiles may load Q rows behind the last, among the T, that they do not use); they are the
  * last ones of its kv_len[b] cached tokens: row i of its n rows stands at cache position
  * kv_len[b] - n + i, and token p of the cache lies in page table[b][p / page_size], slot
  * p % page_size. Table entries that no visible token needs are not read. cu_rows NULL: one row per
@@ -378,7 +379,8 @@ int pck_paged_append(pck_ctx *ctx, const pck_paged_cache *cache, const pck_paged
  * Scores, maxima, sums and O are held in fp32. The weights 2^(s - m) that multiply V are rounded: in the one-token
  * kernel to a pair of 16-bit values (22 bits in fp16, 16 in bf16; the output's own rounding is coarser), in the
  * row kernel once to the cache's type (11 bits, 8 in bf16; prompts of the kind measured then differ from 64 bits by
- * 1.3 times the output's own rounding in bf16, 1.4 times in fp16). fp16 weights below 2^-37 (rows: 2^-31) of the largest one are lost.
+ * 1.3 times the output's own rounding in bf16, 1.4 times in fp16). fp16 weights below 2^-37 (rows: 2^-31) of the largest
+ * one are lost.
  * One row per sequence (cu_rows NULL), or a few (min(max_rows, T) * H_q / H_kv at most 16, 8 at D > 128): split
  * over the cache's length and joined; D in {64, 128, 192, 256}. More rows: tiles of 256 rows (tokens x
  * heads of a kv head) on the tensor cores, D in {64, 128}, H_q / H_kv at most 128. Other head dimensions, which an
@@ -430,9 +432,10 @@ int pck_paged_append_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const
  * max_pages and B name (with a window only those that it reaches), at most as many as the cache has. Where these would
  * take more than 4 GiB and more than half of the codes' bytes, the call goes through its kv heads, and then its sequences, some at a
  * time, down to one sequence's pages of one kv head. So the peak is the codes and half of them again (or 4 GiB), and a table no
- * wider than its sequences need keeps the workspace small and the call whole. bf16 holds the values
- * as far as pck_paged_read_e4m3 says. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one above 65,536 that a row
- * sees makes the call's results invalid (pck_sync reports PCK_ECUDA with code 16): such a cache takes a bf16 q. */
+ * wider than its sequences need keeps the workspace small and the call whole. bf16 holds the values as far as
+ * pck_paged_read_e4m3 says. fp16 does not reach as far as the cache's scales: values below 2^-14 are held to 2^-25, and one
+ * above 65,536 that a row sees makes the call's results invalid (pck_sync reports PCK_ECUDA with code 16): such a cache
+ * takes a bf16 q. */
 int pck_paged_attend_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int q_dtype, int H_q,
                           const void *Q, int64_t q_row, int64_t q_head, int window, int sinks,
                           const float *O_prior, const float *LSE_prior, void *O, float *LSE,
@@ -446,7 +449,8 @@ int pck_paged_workspace_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, co
  * kv_len takes whole caches), K->out and V->out [T, H_kv, D] of dtype F32, F16 or BF16 with the strides given (in and weight are
  * not used): [H_kv, N, D], as pck_store takes it, is a row stride of D. Values are rounded once. fp32 holds
  * them exactly, bf16 those of scales 2^-124 .. 2^119 (below, codes end under its smallest step, 2^-133); in both, a value of 2^128
- * and more, which codes of 256 and above have at 2^120, is an infinity. In fp16 what is beyond 65,504 is 65,504. Rows at a negative cache position are 0. */
+ * and more, which codes of 256 and above have at 2^120, is an infinity. In fp16 what is beyond 65,504 is 65,504. Rows at a
+ * negative cache position are 0. */
 int pck_paged_read_e4m3(pck_ctx *ctx, const pck_paged_cache_e4m3 *cache, const pck_paged_batch *batch, int dtype,
                         const pck_rows *K, const pck_rows *V, void *stream);
 

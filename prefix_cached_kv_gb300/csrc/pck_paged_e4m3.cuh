@@ -3,8 +3,8 @@
 //
 // A head row of a token is D codes in e4m3 (1-4-3 bits, largest value 448, NaN = 0x7f, no infinities) and one scale, a power
 // of two 2^e held as its biased exponent e + 127 in a byte (E8M0: 0 .. 254, and 255 is NaN; the append writes 1 .. 247). A
-// value is code * 2^e: exact in fp32 (below 2^128) and, for e of -124 .. 119, in bf16. A floating code has the same relative step whatever the scale, so the scale
-// only keeps the row in range, and a power of two keeps every other rounding out of the format.
+// value is code * 2^e: exact in fp32 (below 2^128) and, for e of -124 .. 119, in bf16. A floating code has the same relative step
+// whatever the scale, so the scale only keeps the row in range, and a power of two keeps every other rounding out of the format.
 #pragma once
 
 #include "pck_paged.cuh"
