@@ -7,7 +7,7 @@
 // head, packed fp32 arithmetic, and each lane's next heads on their way into shared memory by asynchronous copies: a thread goes
 // through a dozen heads, each a round trip to memory, and more of them in registers cost the warps that would hide them. 8
 // ragged prompts, 32 + 8 + 8 heads of 128: 61.5 us as the 16-bit kernel with another store (two heads in registers, 65 % of the issue slots),
-// 61.4 with a loop per kind and packed arithmetic, 51 with the copies, at three blocks an SM; four blocks spill (62), two 57.
+// 61.4 with a loop per kind and packed arithmetic, 50.5 with the copies, at three blocks an SM; four blocks spill (62), two 57.
 //
 // Reading back: out = code * 2^e, rounded once to the output's type (fp32 holds it exactly below 2^128, bf16 for e of -124 .. 119; in fp16
 // what is beyond 65,504 becomes 65,504). D + 1 bytes in and 2 D or 4 D out per row, so HBM bounds it. A warp takes tiles of 16 tokens of one kv
